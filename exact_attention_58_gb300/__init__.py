@@ -16,6 +16,14 @@ the forward also d = 256), or, forward only, fp32 with d = 64 and e4m3
 (torch.float8_e4m3fn, O in bf16) with d = 128.  attn_fwd_varlen and
 attn_bwd_varlen take packed sequences: [total, H, d] tensors and cumulative
 offsets.
+
+Serving from a paged key/value cache (bf16 or fp16, grouped query heads):
+
+    cu, seq_lens, slots, taken = ea.attn_page_table(cached_lens, new_lens, page_table,
+                                                    free_pages, num_free, page_size, max_tokens)
+    ea.attn_cache_append(k, v, k_cache, v_cache, slots)
+    o, lse = ea.attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu, max_seqlen_q,
+                               causal=True)
 """
 from __future__ import annotations
 
@@ -32,7 +40,8 @@ from . import _build
 __all__ = [
     "AttnError", "attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preprocess",
     "attn_bwd_main", "attn_bwd_dq_convert", "attn_bwd_noalloc", "attn_fwd_varlen",
-    "attn_bwd_varlen", "attn_selftest_wait", "attn_selftest_fwd_withheld", "attn_status_string",
+    "attn_bwd_varlen", "attn_page_table", "attn_cache_append", "attn_fwd_paged",
+    "attn_fwd_paged_workspace_size", "attn_selftest_wait", "attn_selftest_fwd_withheld", "attn_status_string",
     "attn_version", "library",
     "LIB_PATH", "STATUS",
 ]
@@ -98,7 +107,16 @@ def library():
             lib.attn_selftest_fwd_withheld.restype = ctypes.c_int
             lib.attn_bwd_varlen.argtypes = ([vp] * 11 + [ip] * 8 +
                                             [f, ip, ip, f, u64, vp, sz, vp, vp])
-            for fn in ("attn_fwd", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main",
+            i64 = ctypes.c_int64
+            lib.attn_page_table.argtypes = [vp] * 9 + [ip] * 5 + [vp, vp]
+            lib.attn_cache_append.argtypes = ([vp] * 5 + [ip] * 4 + [i64] * 2 + [ip] * 2 +
+                                              [i64] * 3 + [vp, vp])
+            lib.attn_fwd_paged.argtypes = ([vp] * 8 + [ip] * 10 + [i64] * 5 +
+                                           [f, ip, ip, vp, sz, vp, vp])
+            lib.attn_fwd_paged_workspace_size.argtypes = [ip] * 8
+            lib.attn_fwd_paged_workspace_size.restype = sz
+            for fn in ("attn_page_table", "attn_cache_append", "attn_fwd_paged",
+                       "attn_fwd", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main",
                        "attn_bwd_dq_convert", "attn_bwd_noalloc", "attn_fwd_varlen",
                        "attn_bwd_varlen"):
                 getattr(lib, fn).restype = ctypes.c_int
@@ -472,6 +490,196 @@ def attn_bwd_varlen(q, k, v, o, do, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_
                                    _ptr(dev_status), _stream(stream))
     _raise(st, "attn_bwd_varlen")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# paged key/value cache
+# ---------------------------------------------------------------------------
+def _int_tensor(name: str, t, dtype, shape, ref: torch.Tensor):
+    """A contiguous index tensor of the given type and shape on ref's device."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape)
+            or t.device != ref.device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{ref.device}")
+
+
+def _cache_pair(k_cache, v_cache, d: int, ref: torch.Tensor):
+    """Sizes and strides of the caches: [num_pages, Hkv, page_size, d] views of
+    ref's dtype and device, d innermost, laid out alike."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if (not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[3] != d
+                or t.dtype != ref.dtype or t.device != ref.device):
+            raise ValueError(f"{name} must be [num_pages, Hkv, page_size, d] with d = {d}, "
+                             f"{ref.dtype}, on {ref.device}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name} must have d innermost (stride 1)")
+    shape, strides = k_cache.shape, k_cache.stride()
+    if v_cache.shape != shape:
+        raise ValueError("v_cache must match k_cache in shape")
+    for n, a, b in zip(shape, strides, v_cache.stride()):
+        if n > 1 and a != b:
+            raise ValueError("v_cache must match k_cache in strides")
+    return shape[0], shape[1], shape[2], strides[0], strides[1], strides[2]
+
+
+def _rows(name: str, t, ref: torch.Tensor):
+    """Sizes of [tokens, heads, d] rows, d innermost; strides are free."""
+    if (not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != ref.dtype
+            or t.device != ref.device):
+        raise ValueError(f"{name} must be [tokens, heads, d], {ref.dtype}, on {ref.device}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have d innermost (stride 1)")
+    return t.shape
+
+
+def _call(fn, device: torch.device, stream, *args):
+    """fn(*args, stream) with `device` current: the library runs on the current
+    device, and stream None is that device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return fn(*args, _stream(stream))
+    return fn(*args, _stream(stream))
+
+
+def _empty(shape, dtype, device: torch.device, stream):
+    """An uninitialised tensor for work on `stream` (None: the current one).  It
+    comes from that stream's memory, so nothing still running on another stream
+    uses it, and what is freed after the call is handed out again behind it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _int32(name: str, x) -> int:
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def attn_page_table(cached_lens, new_lens, page_table, free_pages, num_free, page_size: int,
+                    max_tokens: int, *, cu_seqlens_q=None, seq_lens=None, slots=None,
+                    pages_taken=None, dev_status=None, stream=None):
+    """Page table and slot map of one serving step: request b has cached_lens[b]
+    tokens in the cache and gets new_lens[b] more.  Enters the pages it needs
+    into page_table ([B, max_pages], in place), taken from the end of
+    free_pages[:num_free], and returns (cu_seqlens_q [B + 1], seq_lens [B],
+    slots [max_tokens] int64, -1 behind the last token, pages_taken [1]).  All
+    int32 CUDA tensors but slots; see include/gbattn.h."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor")
+    B, max_pages = page_table.shape
+    i32 = torch.int32
+    _int_tensor("page_table", page_table, i32, (B, max_pages), page_table)
+    _int_tensor("cached_lens", cached_lens, i32, (B,), page_table)
+    _int_tensor("new_lens", new_lens, i32, (B,), page_table)
+    _int_tensor("num_free", num_free, i32, (1,), page_table)
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a one-dimensional int32 tensor")
+    _int_tensor("free_pages", free_pages, i32, free_pages.shape, page_table)
+    _on_gpu(page_table)
+    max_tokens = _int32("max_tokens", max_tokens)
+    dev = page_table.device
+    if cu_seqlens_q is None:
+        cu_seqlens_q = _empty(B + 1, i32, dev, stream)
+    if seq_lens is None:
+        seq_lens = _empty(B, i32, dev, stream)
+    if slots is None:
+        slots = _empty(max(max_tokens, 0), torch.int64, dev, stream)
+    if pages_taken is None:
+        pages_taken = _empty(1, i32, dev, stream)
+    _int_tensor("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), page_table)
+    _int_tensor("seq_lens", seq_lens, i32, (B,), page_table)
+    _int_tensor("slots", slots, torch.int64, (max_tokens,), page_table)
+    _int_tensor("pages_taken", pages_taken, i32, (1,), page_table)
+    _check_status(dev_status, page_table)
+    st = _call(library().attn_page_table, dev, stream, _ptr(cached_lens), _ptr(new_lens),
+               _ptr(page_table), _ptr(free_pages), _ptr(num_free), _ptr(cu_seqlens_q),
+               _ptr(seq_lens), _ptr(slots), _ptr(pages_taken), B, max_pages, _int32("page_size", page_size),
+               max_tokens, free_pages.shape[0], _ptr(dev_status))
+    _raise(st, "attn_page_table")
+    return cu_seqlens_q, seq_lens, slots, pages_taken
+
+
+def attn_cache_append(k, v, k_cache, v_cache, slots, *, dev_status=None, stream=None):
+    """Writes k, v ([T, Hkv, d], d innermost, the same strides) into slots
+    slots[t] (int64 [T]; -1 skips a token) of the caches ([num_pages, Hkv,
+    page_size, d] views of like strides); see include/gbattn.h."""
+    T, Hkv, d = _rows("k", k, k)
+    if _rows("v", v, k) != k.shape or any(
+            n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride())):
+        raise ValueError("v must match k in shape and strides")
+    pages, heads, page_size, sp, sh, st_ = _cache_pair(k_cache, v_cache, d, k)
+    if heads != Hkv:
+        raise ValueError("the caches must have k's number of heads")
+    _int_tensor("slots", slots, torch.int64, (T,), k)
+    _check_status(dev_status, k)
+    _on_gpu(k)
+    st = _call(library().attn_cache_append, k.device, stream, _ptr(k), _ptr(v), _ptr(k_cache),
+               _ptr(v_cache), _ptr(slots), T, Hkv, d, _dtype_code(k), k.stride(0), k.stride(1),
+               pages, page_size, sp, sh, st_, _ptr(dev_status))
+    _raise(st, "attn_cache_append")
+
+
+def attn_fwd_paged_workspace_size(B: int, H: int, Hkv: int, total_q: int, max_seqlen_q: int,
+                                  max_pages: int, page_size: int, d: int) -> int:
+    return int(library().attn_fwd_paged_workspace_size(B, H, Hkv, total_q, max_seqlen_q, max_pages,
+                                                       page_size, d))
+
+
+def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_seqlen_q: int, *,
+                   causal: bool = False, window: int = 0, scale: Optional[float] = None, out=None,
+                   lse=None, workspace=None, dev_status=None, stream=None):
+    """Attention of packed new tokens over a paged cache: q [total_q, H, d] (d
+    innermost, other strides free), request b's queries at rows
+    [cu_seqlens_q[b], cu_seqlens_q[b + 1]), the last of its seq_lens[b] key
+    positions; keys and values in the pages that page_table [B, max_pages]
+    names.  Query head h reads key head h // (H // Hkv).  Returns O [total_q,
+    H, d] and LSE [H, total_q]; see include/gbattn.h."""
+    total_q, H, d = _rows("q", q, q)
+    pages, Hkv, page_size, sp, sh, st_ = _cache_pair(k_cache, v_cache, d, q)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor")
+    B, max_pages = page_table.shape
+    _int_tensor("page_table", page_table, torch.int32, (B, max_pages), q)
+    _int_tensor("seq_lens", seq_lens, torch.int32, (B,), q)
+    _int_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), q)
+    _check_status(dev_status, q)
+    _on_gpu(q)
+    max_seqlen_q = _int32("max_seqlen_q", max_seqlen_q)
+    window = _int32("window", window)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = _empty((total_q, H, d), q.dtype, q.device, stream)
+    elif (not isinstance(out, torch.Tensor) or out.shape != q.shape or out.dtype != q.dtype
+          or out.device != q.device or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    if lse is None:
+        lse = _empty((H, total_q), torch.float32, q.device, stream)
+    else:
+        _check_lse(lse, (H, total_q), q)
+    lib = library()
+    ws_bytes = 0
+    if workspace is None:
+        ws_bytes = lib.attn_fwd_paged_workspace_size(B, H, Hkv, total_q, max_seqlen_q, max_pages,
+                                                     page_size, d)
+        if ws_bytes:
+            workspace = _empty(ws_bytes, torch.uint8, q.device, stream)
+    else:
+        _check_workspace(workspace, q)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = _call(lib.attn_fwd_paged, q.device, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache),
+               _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(page_table), B, H,
+               Hkv, total_q, max_seqlen_q, pages, page_size, max_pages, d, _dtype_code(q),
+               q.stride(0), q.stride(1), sp, sh, st_, float(scale), int(bool(causal)),
+               window, _ptr(workspace), ws_bytes, _ptr(dev_status))
+    _raise(st, "attn_fwd_paged")
+    return out, lse
 
 
 def attn_selftest_wait(dev_status, *, arrive: bool, stream=None):

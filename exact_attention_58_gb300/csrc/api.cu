@@ -101,22 +101,34 @@ cuuint64_t elem_bytes(attn_dtype dtype) {
     return dtype == ATTN_DTYPE_FP32 ? 4 : (dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2);
 }
 
+CUtensorMapDataType tmap_type(attn_dtype dtype) {
+    switch (dtype) {
+        case ATTN_DTYPE_FP32: return CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+        case ATTN_DTYPE_FP16: return CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        case ATTN_DTYPE_FP8_E4M3: return CU_TENSOR_MAP_DATA_TYPE_UINT8;   // bytes moved as they are
+        case ATTN_DTYPE_BF16: break;
+    }
+    return CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
 bool encode_3d(CUtensorMap* map, const void* ptr, attn_dtype dtype, const cuuint64_t dims[3],
                const cuuint64_t strides[2], const cuuint32_t box[3]) {
+    return encode_tmap(map, ptr, dtype, 3, dims, strides, box);
+}
+
+}  // namespace
+
+bool encode_tmap(CUtensorMap* map, const void* ptr, attn_dtype dtype, int rank,
+                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (enc == nullptr) return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
-    CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (dtype == ATTN_DTYPE_FP32) ty = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    if (dtype == ATTN_DTYPE_FP16) ty = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if (dtype == ATTN_DTYPE_FP8_E4M3) ty = CU_TENSOR_MAP_DATA_TYPE_UINT8;   // bytes moved as they are
-    const CUresult r = enc(map, ty, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(map, tmap_type(dtype), static_cast<cuuint32_t>(rank),
+                           const_cast<void*>(ptr), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 int fwd_tiles(int d, attn_dtype dtype, int N) {
     if (d > 128) return 1;

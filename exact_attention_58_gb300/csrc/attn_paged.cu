@@ -1,0 +1,97 @@
+// attn_paged.cu — launches of the paged attention kernel (attn_paged_kernel.cuh)
+// at head dims 64 and 128, and the kernel that joins pieces.
+#include "attn_paged_kernel.cuh"
+
+namespace gbattn {
+namespace {
+
+// Joins the pieces of split tiles.  Row r of a tile has n pieces (O_i, lse2_i)
+// over disjoint key sets: with M = max lse2_i and w_i = exp2(lse2_i - M),
+// O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2.  One warp per
+// row, 4 floats of d per lane and step; the pieces were written by the launch
+// before and come from L2.
+constexpr int kJoinWarps = 4;
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedParams p) {
+    grid_dep_wait();
+    const PieceDesc t = p.desc[blockIdx.x];
+    const int u = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);   // (token, head of the group)
+    if (t.n == 0 || u >= t.ntok * p.G) return;
+    const int lane = threadIdx.x & 31;
+    const int tok = u / p.G, g = u - tok * p.G;
+    const int row = tok / p.tile_tokens * kTileRows + (tok % p.tile_tokens) * p.G + g;
+    auto piece_row = [&](int i) {
+        const int slot = i == 0 ? t.slot0 : t.slot1 + (i - 1) * t.step;
+        return static_cast<size_t>(slot) * p.slot_rows + row;
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < t.n; i += 32) M = fmaxf(M, p.part_lse[piece_row(i)]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float m0 = M == -INFINITY ? 0.f : M;
+    constexpr int PER = D / 32;   // floats of a lane
+    float acc[PER], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < t.n; ++i) {
+        const size_t at = piece_row(i);
+        const float w = ex2_approx(p.part_lse[at] - m0);
+        sum += w;
+        const float2* src = reinterpret_cast<const float2*>(p.part_o + at * D) + lane * (PER / 2);
+#pragma unroll
+        for (int e = 0; e < PER / 2; ++e) {
+            const float2 x = src[e];
+            acc[2 * e] += w * x.x;
+            acc[2 * e + 1] += w * x.y;
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int head = t.hk * p.G + g;
+    const size_t out_row = (static_cast<size_t>(t.q_start) + t.tok0 + tok) * p.lq.H + head;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + out_row * D) + lane * (PER / 2);
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) dst[e] = pack_h2<kF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0)
+        p.LSE[static_cast<size_t>(head) * p.lq.total + t.q_start + t.tok0 + tok] =
+            sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int d, bool f16,
+                              cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(descs), static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (d) {
+        case 64: return f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<64, true>, p)
+                            : cudaLaunchKernelEx(&cfg, paged_join_kernel<64, false>, p);
+        case 128: return f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<128, true>, p)
+                             : cudaLaunchKernelEx(&cfg, paged_join_kernel<128, false>, p);
+        case 256: return f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<256, true>, p)
+                             : cudaLaunchKernelEx(&cfg, paged_join_kernel<256, false>, p);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PagedParams& p, int d, bool f16, cudaStream_t stream) {
+    switch (d) {
+        case 64: return f16 ? launch_paged_t<64, true, 2>(tq, tk, tv, p, stream)
+                            : launch_paged_t<64, false, 2>(tq, tk, tv, p, stream);
+        case 128: return f16 ? launch_paged_t<128, true, 2>(tq, tk, tv, p, stream)
+                             : launch_paged_t<128, false, 2>(tq, tk, tv, p, stream);
+        case 256: return launch_paged_tiles_d256(tq, tk, tv, p, f16, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gbattn

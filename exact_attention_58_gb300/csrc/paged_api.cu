@@ -1,0 +1,288 @@
+// paged_api.cu — C entry points of the paged key/value cache declared in
+// include/gbattn.h: argument validation, tensor maps and the choice of kernel
+// and split.  Nothing here allocates, frees or synchronises.
+#include <algorithm>
+#include <cmath>
+
+#include "paged.cuh"
+#include "paged_cache.h"
+
+namespace gbattn {
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+attn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+// A stride in elements: positive, a multiple of 16 bytes, and below the 2^40
+// bytes that a tensor map can hold.  A dimension of one element has no stride.
+bool stride_ok(long long stride, long long extent) {
+    return extent == 1 || (stride > 0 && stride % 8 == 0 && stride < (1ll << 39));
+}
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Shape of the cache and of what is read from or written to it.
+attn_status check_cache(int Hkv, int d, attn_dtype dtype, int num_pages, int page_size,
+                        long long page_stride, long long head_stride, long long token_stride) {
+    if (Hkv < 1 || num_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP16)
+        return dtype == ATTN_DTYPE_FP32 || dtype == ATTN_DTYPE_FP8_E4M3 ? ATTN_ERR_UNSUPPORTED
+                                                                       : ATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+    if (page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_pages) * page_size >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+    if (!stride_ok(page_stride, num_pages) || !stride_ok(head_stride, Hkv) ||
+        !stride_ok(token_stride, page_size))
+        return ATTN_ERR_MISALIGNED;
+    return ATTN_OK;
+}
+
+// How a call's queries are cut into tiles and how many CTAs share a tile.
+struct TilePlan {
+    int tile_tokens, tiles, uniform, splits;
+    size_t slots, descs;
+    int rows;
+};
+
+TilePlan plan_tiles(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d) {
+    TilePlan t{};
+    const int per_cta = d == 256 ? 1 : 2;
+    t.tile_tokens = kTileRows / (H / Hkv);
+    const int cta_tokens = t.tile_tokens * per_cta;
+    const long long per_request = (max_q + cta_tokens - 1) / cta_tokens;
+    const long long packed = total_q / cta_tokens + static_cast<long long>(B);
+    const bool uniform = per_request * B <= packed;
+    t.tiles = static_cast<int>(std::min(uniform ? per_request * B : packed, 0x7fffffffll));
+    t.uniform = uniform ? static_cast<int>(per_request) : 0;
+    // With fewer CTAs than SMs the keys of a tile are shared out, as far as
+    // all CTAs still run at once.
+    const long long ctas = static_cast<long long>(t.tiles) * Hkv;
+    const long long blocks = (max_keys + kTileRows - 1) / kTileRows;
+    t.splits = static_cast<int>(std::max(1ll, std::min(kSMs / ctas, blocks)));
+    t.rows = per_cta * kTileRows;
+    if (t.splits > 1) {
+        t.descs = static_cast<size_t>(ctas);
+        t.slots = t.descs * t.splits;
+    }
+    return t;
+}
+
+attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int max_pages,
+                              int page_size, int d) {
+    if (B < 1 || H < 1 || Hkv < 1 || total_q < 1 || max_q < 1 || max_pages < 1 || page_size < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (H % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (H / Hkv > kTileRows) return ATTN_ERR_UNSUPPORTED;
+    if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(max_pages) * page_size > kMaxPagedKeys) return ATTN_ERR_UNSUPPORTED;
+    if (total_q > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    const TilePlan t = plan_tiles(B, H, Hkv, total_q, std::min(max_q, total_q),
+                                  static_cast<long long>(max_pages) * page_size, d);
+    if (static_cast<long long>(t.tiles) * Hkv * t.splits >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// Tensor map over a cache [num_pages][Hkv][page_size][d] with any strides.
+bool make_tmap_cache(CUtensorMap* map, const void* ptr, attn_dtype dtype, int num_pages, int Hkv,
+                     int page_size, int d, long long page_stride, long long head_stride,
+                     long long token_stride, int box_rows) {
+    auto bytes = [&](long long stride, long long extent) {
+        return static_cast<cuuint64_t>(extent == 1 ? d : stride) * 2;
+    };
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[3] = {bytes(token_stride, page_size), bytes(head_stride, Hkv),
+                                   bytes(page_stride, num_pages)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    return encode_tmap(map, ptr, dtype, 4, dims, strides, box);
+}
+
+// Tensor map over packed queries [total_q][H][d]: boxes of `tokens` tokens of
+// G heads, whose rows land in shared memory as (token, head).
+bool make_tmap_queries(CUtensorMap* map, const void* ptr, attn_dtype dtype, int total_q, int H,
+                       int d, long long token_stride, long long head_stride, int G, int tokens) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
+                                static_cast<cuuint64_t>(total_q)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(H == 1 ? d : head_stride) * 2,
+                                   static_cast<cuuint64_t>(total_q == 1 ? static_cast<long long>(d) * H
+                                                                        : token_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+    return encode_tmap(map, ptr, dtype, 3, dims, strides, box);
+}
+
+}  // namespace
+}  // namespace gbattn
+
+using namespace gbattn;
+
+extern "C" {
+
+attn_status attn_page_table(const int32_t* cached_lens, const int32_t* new_lens,
+                            int32_t* page_table, const int32_t* free_pages,
+                            const int32_t* num_free, int32_t* cu_seqlens_q, int32_t* seq_lens,
+                            int64_t* slots, int32_t* pages_taken, int B, int max_pages,
+                            int page_size, int max_tokens, int free_capacity, int* dev_status,
+                            void* stream) {
+    if (!cached_lens || !new_lens || !page_table || !free_pages || !num_free || !cu_seqlens_q ||
+        !seq_lens || !slots || !pages_taken)
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || page_size < 1 || max_tokens < 1 || free_capacity < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (B > kMaxTableRequests || page_size % 8 != 0 ||
+        static_cast<long long>(max_pages) * page_size > kMaxPagedKeys || max_tokens > (1 << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(page_table, 4) ||
+        !aligned(free_pages, 4) || !aligned(num_free, 4) || !aligned(cu_seqlens_q, 4) ||
+        !aligned(seq_lens, 4) || !aligned(slots, 8) || !aligned(pages_taken, 4))
+        return ATTN_ERR_MISALIGNED;
+    // Every CTA reads the inputs while the first ones already write outputs.
+    const size_t nb = static_cast<size_t>(B) * 4;
+    const struct { const void* ptr; size_t bytes; } ins[] = {
+        {cached_lens, nb}, {new_lens, nb}, {free_pages, static_cast<size_t>(free_capacity) * 4},
+        {num_free, 4}, {page_table, nb * max_pages}};
+    const struct { const void* ptr; size_t bytes; } outs[] = {
+        {cu_seqlens_q, nb + 4}, {seq_lens, nb}, {slots, static_cast<size_t>(max_tokens) * 8},
+        {pages_taken, 4}};
+    for (const auto& o : outs)
+        for (const auto& i : ins)
+            if (overlap(o.ptr, o.bytes, i.ptr, i.bytes)) return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)   // page_table is an output too
+        if (overlap(page_table, nb * max_pages, ins[i].ptr, ins[i].bytes)) return ATTN_ERR_INVALID_ARG;
+    TableParams p{};
+    p.cached_lens = cached_lens;
+    p.new_lens = new_lens;
+    p.page_table = page_table;
+    p.free_pages = free_pages;
+    p.num_free = num_free;
+    p.cu_seqlens_q = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.slots = slots;
+    p.pages_taken = pages_taken;
+    p.dev_status = dev_status;
+    p.B = B;
+    p.max_pages = max_pages;
+    p.page_size = page_size;
+    p.max_tokens = max_tokens;
+    p.free_capacity = free_capacity;
+    return from_cuda(launch_page_table(p, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void* v_cache,
+                              const int64_t* slots, int T, int H_kv, int d, attn_dtype dtype,
+                              int64_t token_stride, int64_t head_stride, int num_pages,
+                              int page_size, int64_t cache_page_stride, int64_t cache_head_stride,
+                              int64_t cache_token_stride, int* dev_status, void* stream) {
+    if (!K || !V || !k_cache || !v_cache || !slots || T < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status st = check_cache(H_kv, d, dtype, num_pages, page_size, cache_page_stride,
+                                       cache_head_stride, cache_token_stride);
+    if (st != ATTN_OK) return st;
+    if (static_cast<long long>(T) * H_kv >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+    if (!stride_ok(token_stride, T) || !stride_ok(head_stride, H_kv)) return ATTN_ERR_MISALIGNED;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(slots, 8))
+        return ATTN_ERR_MISALIGNED;
+    AppendParams p{};
+    p.K = static_cast<const uint16_t*>(K);
+    p.V = static_cast<const uint16_t*>(V);
+    p.k_cache = static_cast<uint16_t*>(k_cache);
+    p.v_cache = static_cast<uint16_t*>(v_cache);
+    p.slots = slots;
+    p.dev_status = dev_status;
+    p.T = T;
+    p.Hkv = H_kv;
+    p.d = d;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.cache_page_stride = cache_page_stride;
+    p.cache_head_stride = cache_head_stride;
+    p.cache_token_stride = cache_token_stride;
+    return from_cuda(launch_cache_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int max_seqlen_q,
+                                     int max_pages, int page_size, int d) {
+    if (check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d) != ATTN_OK)
+        return 0;
+    const TilePlan t = plan_tiles(B, H, H_kv, total_q, std::min(max_seqlen_q, total_q),
+                                  static_cast<long long>(max_pages) * page_size, d);
+    return t.slots == 0 ? 0 : pieces_bytes(t.slots, t.rows, d, t.descs);
+}
+
+attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cache, void* O,
+                           float* LSE, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
+                           const int32_t* page_table, int B, int H, int H_kv, int total_q,
+                           int max_seqlen_q, int num_pages, int page_size, int max_pages, int d,
+                           attn_dtype dtype, int64_t q_token_stride, int64_t q_head_stride,
+                           int64_t cache_page_stride, int64_t cache_head_stride,
+                           int64_t cache_token_stride, float scale, int causal, int window,
+                           void* workspace, size_t workspace_bytes, int* dev_status,
+                           void* stream) {
+    if (!Q || !k_cache || !v_cache || !O || !LSE || !cu_seqlens_q || !seq_lens || !page_table)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status st = check_cache(H_kv, d, dtype, num_pages, page_size, cache_page_stride,
+                                 cache_head_stride, cache_token_stride);
+    if (st != ATTN_OK) return st;
+    st = check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (!stride_ok(q_token_stride, total_q) || !stride_ok(q_head_stride, H)) return ATTN_ERR_MISALIGNED;
+    if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(O, 16) ||
+        !aligned(LSE, 16) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) ||
+        !aligned(page_table, 4))
+        return ATTN_ERR_MISALIGNED;
+    const int max_q = std::min(max_seqlen_q, total_q);
+    const TilePlan t = plan_tiles(B, H, H_kv, total_q, max_q,
+                                  static_cast<long long>(max_pages) * page_size, d);
+    PagedParams p{};
+    if (t.slots > 0) {
+        if (workspace == nullptr || workspace_bytes < pieces_bytes(t.slots, t.rows, d, t.descs))
+            return ATTN_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
+        carve_pieces(p, workspace, t.slots, t.rows, t.descs);
+    }
+    p.O = O;
+    p.LSE = LSE;
+    p.seq_lens = seq_lens;
+    p.page_table = page_table;
+    p.dev_status = dev_status;
+    p.lq = SeqLayout{cu_seqlens_q, H, max_q, total_q};
+    p.B = B;
+    p.Hkv = H_kv;
+    p.G = H / H_kv;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.box_rows = std::min(kTileRows, page_size & -page_size);
+    p.tile_tokens = t.tile_tokens;
+    p.causal = causal != 0;
+    // a window of 2^30 keys is none: no two positions are that far apart
+    p.window = window > 0 && window < kMaxPagedKeys ? window : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.tiles = t.tiles;
+    p.uniform_tiles = t.uniform;
+    p.splits = t.splits;
+    CUtensorMap tq, tk, tv;
+    if (!make_tmap_queries(&tq, Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
+                           p.tile_tokens) ||
+        !make_tmap_cache(&tk, k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+                         cache_head_stride, cache_token_stride, p.box_rows) ||
+        !make_tmap_cache(&tv, v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+                         cache_head_stride, cache_token_stride, p.box_rows))
+        return ATTN_ERR_CUDA;
+    const bool f16 = dtype == ATTN_DTYPE_FP16;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_paged_tiles(tq, tk, tv, p, d, f16, s);
+    if (e == cudaSuccess && t.splits > 1)
+        e = launch_paged_join(p, static_cast<int>(t.descs), t.tile_tokens * p.G * (t.rows / kTileRows),
+                              d, f16, s);
+    return from_cuda(e);
+}
+
+}  // extern "C"

@@ -249,6 +249,118 @@ attn_status attn_bwd_varlen(const void* Q, const void* K, const void* V, const v
                             size_t workspace_bytes, int* dev_status, void* stream);
 
 /*
+ * Serving from a paged key/value cache.  A decoding server keeps the keys and
+ * values of its requests in pages of a common pool, because their lengths
+ * grow and cannot be known ahead.  One step runs three entry points:
+ * attn_page_table gives the step's new tokens their slots, attn_cache_append
+ * writes their K and V rows there, attn_fwd_paged attends over the cache.
+ *   cache      k_cache, v_cache: [num_pages, H_kv, page_size, d], bf16 or fp16,
+ *              the same strides for both, d innermost.  The strides of page,
+ *              head and token (in elements, multiples of 8) are arguments, so
+ *              a cache may be a view: token-major pages [num_pages, page_size,
+ *              H_kv, d], or K and V side by side in one array.  The stride of
+ *              a dimension of extent 1 is ignored.  page_size is a multiple of
+ *              8; num_pages * page_size < 2^31.
+ *   page_table int32 [B, max_pages], contiguous: entry [b, c] is the page that
+ *              holds keys [c page_size, (c+1) page_size) of request b.  Entries
+ *              past a request's last key, or before every key that its window
+ *              still reaches, are not used.  max_pages * page_size <= 2^30.
+ *   slot       page * page_size + row: the place of one token in the pool.
+ *   lengths    int32 device arrays, so that a step captured into a graph can
+ *              be replayed with other lengths.
+ * No backward pass: the cache serves inference.  Conventions (streams, errors,
+ * alignment, ownership) as above.
+ */
+
+/*
+ * Page table and slot map of one step.  Request b has cached_lens[b] tokens in
+ * the cache and gets new_lens[b] more (either may be 0).
+ *   cu_seqlens_q  out [B + 1]  exclusive sums of new_lens
+ *   seq_lens      out [B]      cached_lens + new_lens
+ *   page_table    in/out       the pages that request b holds, entries [0,
+ *                              ceil(cached_lens[b] / page_size)), are read; the
+ *                              pages its new tokens need beyond them are
+ *                              entered behind; nothing else is written
+ *   slots         out int64 [max_tokens]  slot of each packed new token; -1
+ *                              from the last token on
+ *   pages_taken   out [1]      free pages used
+ *   free_pages    in [free_capacity], num_free in [1]: a stack of page ids,
+ *                              free_pages[0, num_free).  Pages are taken from
+ *                              its end, request by request: the i-th taken is
+ *                              free_pages[num_free - 1 - i].  The caller lowers
+ *                              num_free by pages_taken.
+ * Outputs other than page_table must not overlap inputs.  Clamped and reported
+ * as ATTN_ERR_INVALID_ARG through dev_status: negative lengths (to 0),
+ * requests longer than max_pages pages (their new tokens are cut), new tokens
+ * past max_tokens (cut), num_free outside [0, free_capacity].  When the free
+ * pages run out, the pages missing are entered as -1 and their tokens' slots
+ * are -1 (reported too).  B <= 16384, max_tokens <= 2^30.  One launch.
+ */
+attn_status attn_page_table(const int32_t* cached_lens, const int32_t* new_lens,
+                            int32_t* page_table, const int32_t* free_pages,
+                            const int32_t* num_free, int32_t* cu_seqlens_q, int32_t* seq_lens,
+                            int64_t* slots, int32_t* pages_taken, int B, int max_pages,
+                            int page_size, int max_tokens, int free_capacity, int* dev_status,
+                            void* stream);
+
+/*
+ * Writes row t of K and V ([T, H_kv, d], d innermost, the given token and head
+ * strides for both) to slot slots[t] of every head of the caches.  A slot of
+ * -1 is skipped; any other slot outside [0, num_pages * page_size) is skipped
+ * and reported as ATTN_ERR_INVALID_ARG through dev_status.  Slots must differ
+ * from one another: what a slot named twice holds is unspecified.  K and V
+ * must not overlap the caches.  bf16 or fp16, d in {64, 128, 256}.  One launch.
+ */
+attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void* v_cache,
+                              const int64_t* slots, int T, int H_kv, int d, attn_dtype dtype,
+                              int64_t token_stride, int64_t head_stride, int num_pages,
+                              int page_size, int64_t cache_page_stride, int64_t cache_head_stride,
+                              int64_t cache_token_stride, int* dev_status, void* stream);
+
+/*
+ * Attention of packed new tokens over the cache; from single tokens (decoding)
+ * to whole prompts, mixed in one call.
+ *   Q    in  [total_q, H, d], d innermost, the given token and head strides
+ *            (multiples of 8 elements): a slice of a fused projection will do
+ *   O    out [total_q, H, d] contiguous; LSE out float [H, total_q]
+ *   cu_seqlens_q  int32 [B + 1]: request b's queries are rows [cu_seqlens_q[b],
+ *            cu_seqlens_q[b+1]), at most max_seqlen_q of them, possibly none
+ *   seq_lens int32 [B]: keys of request b, its new tokens included; possibly 0
+ * Query head h reads key/value head h / (H / H_kv); H_kv divides H, at most 128
+ * query heads each.  Mask, scale and LSE as in attn_fwd_varlen with Nk_b =
+ * seq_lens[b]: a request's queries are its last key positions; a query without
+ * a key gets O = 0 and LSE = -inf.  Cache slots that no query of a request may
+ * attend (past its last key, before its window) may hold anything, NaN
+ * included, without effect.  Rows of Q behind cu_seqlens_q[B] are ignored, and
+ * those of O and LSE left as they are.
+ * Clamped on the device (no access leaves the tensors) and reported as
+ * ATTN_ERR_INVALID_ARG through dev_status: bad cu_seqlens_q as in
+ * attn_fwd_varlen, seq_lens outside [0, max_pages * page_size], and page ids
+ * outside [0, num_pages) (zeros are read for their keys).
+ * bf16 or fp16, d in {64, 128, 256}.  The workspace holds
+ * attn_fwd_paged_workspace_size(...) bytes (16-byte aligned, contents on entry
+ * do not matter; may be NULL when that is 0); calls that may overlap on the
+ * GPU need one each.  One or two launches.
+ */
+attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cache, void* O,
+                           float* LSE, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
+                           const int32_t* page_table, int B, int H, int H_kv, int total_q,
+                           int max_seqlen_q, int num_pages, int page_size, int max_pages, int d,
+                           attn_dtype dtype, int64_t q_token_stride, int64_t q_head_stride,
+                           int64_t cache_page_stride, int64_t cache_head_stride,
+                           int64_t cache_token_stride, float scale, int causal, int window,
+                           void* workspace, size_t workspace_bytes, int* dev_status,
+                           void* stream);
+
+/*
+ * Bytes of device workspace attn_fwd_paged needs for partial results, where
+ * the keys of a query tile are shared out over several CTAs.  0 where it needs
+ * none, and for arguments that it would reject.
+ */
+size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int max_seqlen_q,
+                                     int max_pages, int page_size, int d);
+
+/*
  * Device self-test of the failure detection the kernels rely on: one warp
  * waits on an mbarrier with the same bounded wait (about 2 s of
  * %globaltimer) that every kernel uses.  arrive != 0: one thread arrives
