@@ -367,7 +367,15 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         bool ok = true;
         for (int j = jlo(t); j < jhi(t); ++j) {
             const int k0 = j * kTileRows;
-            if (edge(j)) {   // V rows outside [klo, khi) become zero
+            if (!mbar_wait_warp(&bar_s[t], (j - jlo(t)) & 1, s_abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // V rows outside [klo, khi) become zero.  Only after S_j: by then
+            // every earlier fill of V_j's slot has been waited for, so that
+            // the parity below can only mean this one.
+            if (edge(j)) {
                 const int vseq = 2 * (j - jbeg) + 1;
                 const int slot = vseq % C::NSLOT;
                 if (!mbar_wait_warp(&full[slot], (vseq / C::NSLOT) & 1, s_abort)) {
@@ -383,11 +391,6 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                 }
                 fence_proxy_async_smem();
             }
-            if (!mbar_wait_warp(&bar_s[t], (j - jlo(t)) & 1, s_abort)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
             const bool wmask = W > 0 && (k0 < last_pos - W + 1 ||
                                          (!p.causal && k0 + kTileRows - 1 > first_pos + W - 1));
             const bool tile_mask = k0 + kTileRows > L ||

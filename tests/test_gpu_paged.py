@@ -56,6 +56,17 @@ def test_page_sizes(page, q_lens):
     check_attention(*run(x, True), x, True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_lens", [[60] * 8, [1] * 8], ids=str)
+def test_last_tile_of_longer_contexts(d, q_lens):
+    """The last tile's V rows past the end are cleared only once that tile has
+    arrived, however late the pages before it come in."""
+    k_lens = [2700, 300, 1111, 129, 255, 2047, 513, 385]
+    x = make_paged(q_lens, k_lens, 4, 2, d, 8, seed=d, poison=math.nan)
+    for _ in range(5):
+        check_attention(*run(x, True), x, True)
+
+
 @pytest.mark.parametrize("window", [1, 7, 128, 300, 10**6, 2**31 - 1])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("q_lens", [[1, 1], [3, 2], [250, 30]], ids=str)
