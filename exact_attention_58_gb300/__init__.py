@@ -82,6 +82,8 @@ class AttnError(RuntimeError):
 def library():
     """The loaded libgbattn.so.  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -495,50 +497,69 @@ def attn_bwd_varlen(q, k, v, o, do, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_
 # ---------------------------------------------------------------------------
 # paged key/value cache
 # ---------------------------------------------------------------------------
-def _int_tensor(name: str, t, dtype, shape, ref: torch.Tensor):
-    """A contiguous index tensor of the given type and shape on ref's device."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape)
-            or t.device != ref.device or not t.is_contiguous()):
+# The calls of a decoding step take a few microseconds on the GPU, so the host
+# side is kept short: one pass over each tensor's attributes, plain integers for
+# pointers and streams (a current_stream() object alone costs 3 us), no
+# allocation beyond the outputs.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _int_tensor(name: str, t, dtype, shape, ref: torch.Tensor) -> int:
+    """Pointer of a contiguous index tensor of the given type and shape on
+    ref's device."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != ref.get_device() or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          f"{ref.device}")
+    return t.data_ptr()
 
 
 def _cache_pair(k_cache, v_cache, d: int, ref: torch.Tensor):
     """Sizes and strides of the caches: [num_pages, Hkv, page_size, d] views of
     ref's dtype and device, d innermost, laid out alike."""
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if (not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[3] != d
-                or t.dtype != ref.dtype or t.device != ref.device):
-            raise ValueError(f"{name} must be [num_pages, Hkv, page_size, d] with d = {d}, "
-                             f"{ref.dtype}, on {ref.device}")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name} must have d innermost (stride 1)")
+        if (not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype is not ref.dtype
+                or t.get_device() != ref.get_device()):
+            raise ValueError(f"{name} must be [num_pages, Hkv, page_size, d], {ref.dtype}, on "
+                             f"{ref.device}")
     shape, strides = k_cache.shape, k_cache.stride()
+    if shape[3] != d or strides[3] != 1:
+        raise ValueError(f"the caches must have d = {d} innermost (stride 1)")
     if v_cache.shape != shape:
         raise ValueError("v_cache must match k_cache in shape")
-    for n, a, b in zip(shape, strides, v_cache.stride()):
-        if n > 1 and a != b:
-            raise ValueError("v_cache must match k_cache in strides")
+    other = v_cache.stride()
+    if other != strides and any(n > 1 and x != y for n, x, y in zip(shape, strides, other)):
+        raise ValueError("v_cache must match k_cache in strides")
     return shape[0], shape[1], shape[2], strides[0], strides[1], strides[2]
 
 
-def _rows(name: str, t, ref: torch.Tensor):
-    """Sizes of [tokens, heads, d] rows, d innermost; strides are free."""
-    if (not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != ref.dtype
-            or t.device != ref.device):
-        raise ValueError(f"{name} must be [tokens, heads, d], {ref.dtype}, on {ref.device}")
-    if t.stride(2) != 1:
+def _rows(name: str, t):
+    """Shape and strides of [tokens, heads, d] rows, d innermost, the other
+    strides free."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, d] tensor")
+    strides = t.stride()
+    if strides[2] != 1:
         raise ValueError(f"{name} must have d innermost (stride 1)")
-    return t.shape
+    return t.shape, strides
 
 
-def _call(fn, device: torch.device, stream, *args):
+def _call(fn, where: str, device: int, stream, *args):
     """fn(*args, stream) with `device` current: the library runs on the current
     device, and stream None is that device's current stream."""
-    if device.index != torch.cuda.current_device():
+    if stream is None:
+        handle = _raw_stream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    if device == torch._C._cuda_getDevice():
+        st = fn(*args, handle)
+    else:
         with torch.cuda.device(device):
-            return fn(*args, _stream(stream))
-    return fn(*args, _stream(stream))
+            st = fn(*args, handle)
+    if st != 0:
+        raise AttnError(st, where)
 
 
 def _empty(shape, dtype, device: torch.device, stream):
@@ -572,36 +593,34 @@ def attn_page_table(cached_lens, new_lens, page_table, free_pages, num_free, pag
     int32 CUDA tensors but slots; see include/gbattn.h."""
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
-    B, max_pages = page_table.shape
-    i32 = torch.int32
-    _int_tensor("page_table", page_table, i32, (B, max_pages), page_table)
-    _int_tensor("cached_lens", cached_lens, i32, (B,), page_table)
-    _int_tensor("new_lens", new_lens, i32, (B,), page_table)
-    _int_tensor("num_free", num_free, i32, (1,), page_table)
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("free_pages must be a one-dimensional int32 tensor")
-    _int_tensor("free_pages", free_pages, i32, free_pages.shape, page_table)
-    _on_gpu(page_table)
+    ref, i32 = page_table, torch.int32
+    B, max_pages = ref.shape
     max_tokens = _int32("max_tokens", max_tokens)
-    dev = page_table.device
-    if cu_seqlens_q is None:
-        cu_seqlens_q = _empty(B + 1, i32, dev, stream)
-    if seq_lens is None:
-        seq_lens = _empty(B, i32, dev, stream)
-    if slots is None:
-        slots = _empty(max(max_tokens, 0), torch.int64, dev, stream)
-    if pages_taken is None:
-        pages_taken = _empty(1, i32, dev, stream)
-    _int_tensor("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), page_table)
-    _int_tensor("seq_lens", seq_lens, i32, (B,), page_table)
-    _int_tensor("slots", slots, torch.int64, (max_tokens,), page_table)
-    _int_tensor("pages_taken", pages_taken, i32, (1,), page_table)
-    _check_status(dev_status, page_table)
-    st = _call(library().attn_page_table, dev, stream, _ptr(cached_lens), _ptr(new_lens),
-               _ptr(page_table), _ptr(free_pages), _ptr(num_free), _ptr(cu_seqlens_q),
-               _ptr(seq_lens), _ptr(slots), _ptr(pages_taken), B, max_pages, _int32("page_size", page_size),
-               max_tokens, free_pages.shape[0], _ptr(dev_status))
-    _raise(st, "attn_page_table")
+    page_size = _int32("page_size", page_size)
+    inputs = (_int_tensor("cached_lens", cached_lens, i32, (B,), ref),
+              _int_tensor("new_lens", new_lens, i32, (B,), ref),
+              _int_tensor("page_table", ref, i32, (B, max_pages), ref),
+              _int_tensor("free_pages", free_pages, i32, free_pages.shape, ref),
+              _int_tensor("num_free", num_free, i32, (1,), ref))
+    _check_status(dev_status, ref)
+    _on_gpu(ref)
+    dev = ref.device
+
+    def output(name, t, dtype, n):
+        if t is None:
+            return _empty(n, dtype, dev, stream)
+        _int_tensor(name, t, dtype, (n,), ref)
+        return t
+
+    cu_seqlens_q = output("cu_seqlens_q", cu_seqlens_q, i32, B + 1)
+    seq_lens = output("seq_lens", seq_lens, i32, B)
+    slots = output("slots", slots, torch.int64, max(max_tokens, 0))
+    pages_taken = output("pages_taken", pages_taken, i32, 1)
+    _call(library().attn_page_table, "attn_page_table", dev.index, stream, *inputs,
+          cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(), pages_taken.data_ptr(),
+          B, max_pages, page_size, max_tokens, free_pages.shape[0], _ptr(dev_status))
     return cu_seqlens_q, seq_lens, slots, pages_taken
 
 
@@ -609,20 +628,22 @@ def attn_cache_append(k, v, k_cache, v_cache, slots, *, dev_status=None, stream=
     """Writes k, v ([T, Hkv, d], d innermost, the same strides) into slots
     slots[t] (int64 [T]; -1 skips a token) of the caches ([num_pages, Hkv,
     page_size, d] views of like strides); see include/gbattn.h."""
-    T, Hkv, d = _rows("k", k, k)
-    if _rows("v", v, k) != k.shape or any(
-            n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride())):
-        raise ValueError("v must match k in shape and strides")
-    pages, heads, page_size, sp, sh, st_ = _cache_pair(k_cache, v_cache, d, k)
+    shape, strides = _rows("k", k)
+    v_shape, v_strides = _rows("v", v)
+    T, Hkv, d = shape
+    if (v_shape != shape or v.dtype is not k.dtype or v.get_device() != k.get_device()
+            or (v_strides != strides
+                and any(n > 1 and x != y for n, x, y in zip(shape, strides, v_strides)))):
+        raise ValueError("v must match k in shape, strides, dtype and device")
+    pages, heads, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, k)
     if heads != Hkv:
         raise ValueError("the caches must have k's number of heads")
-    _int_tensor("slots", slots, torch.int64, (T,), k)
+    at = _int_tensor("slots", slots, torch.int64, (T,), k)
     _check_status(dev_status, k)
     _on_gpu(k)
-    st = _call(library().attn_cache_append, k.device, stream, _ptr(k), _ptr(v), _ptr(k_cache),
-               _ptr(v_cache), _ptr(slots), T, Hkv, d, _dtype_code(k), k.stride(0), k.stride(1),
-               pages, page_size, sp, sh, st_, _ptr(dev_status))
-    _raise(st, "attn_cache_append")
+    _call(library().attn_cache_append, "attn_cache_append", k.get_device(), stream, k.data_ptr(),
+          v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), at, T, Hkv, d, _dtype_code(k),
+          strides[0], strides[1], pages, page_size, sp, sh, st, _ptr(dev_status))
 
 
 def attn_fwd_paged_workspace_size(B: int, H: int, Hkv: int, total_q: int, max_seqlen_q: int,
@@ -640,27 +661,28 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_
     positions; keys and values in the pages that page_table [B, max_pages]
     names.  Query head h reads key head h // (H // Hkv).  Returns O [total_q,
     H, d] and LSE [H, total_q]; see include/gbattn.h."""
-    total_q, H, d = _rows("q", q, q)
-    pages, Hkv, page_size, sp, sh, st_ = _cache_pair(k_cache, v_cache, d, q)
+    (total_q, H, d), strides = _rows("q", q)
+    pages, Hkv, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, q)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
     B, max_pages = page_table.shape
-    _int_tensor("page_table", page_table, torch.int32, (B, max_pages), q)
-    _int_tensor("seq_lens", seq_lens, torch.int32, (B,), q)
-    _int_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), q)
+    table = _int_tensor("page_table", page_table, torch.int32, (B, max_pages), q)
+    lens = _int_tensor("seq_lens", seq_lens, torch.int32, (B,), q)
+    cu = _int_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), q)
     _check_status(dev_status, q)
-    _on_gpu(q)
     max_seqlen_q = _int32("max_seqlen_q", max_seqlen_q)
     window = _int32("window", window)
+    _on_gpu(q)
+    dev = q.device
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = _empty((total_q, H, d), q.dtype, q.device, stream)
-    elif (not isinstance(out, torch.Tensor) or out.shape != q.shape or out.dtype != q.dtype
-          or out.device != q.device or not out.is_contiguous()):
+        out = _empty((total_q, H, d), q.dtype, dev, stream)
+    elif (not isinstance(out, torch.Tensor) or out.shape != q.shape or out.dtype is not q.dtype
+          or out.get_device() != dev.index or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     if lse is None:
-        lse = _empty((H, total_q), torch.float32, q.device, stream)
+        lse = _empty((H, total_q), torch.float32, dev, stream)
     else:
         _check_lse(lse, (H, total_q), q)
     lib = library()
@@ -669,16 +691,15 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_
         ws_bytes = lib.attn_fwd_paged_workspace_size(B, H, Hkv, total_q, max_seqlen_q, max_pages,
                                                      page_size, d)
         if ws_bytes:
-            workspace = _empty(ws_bytes, torch.uint8, q.device, stream)
+            workspace = _empty(ws_bytes, torch.uint8, dev, stream)
     else:
         _check_workspace(workspace, q)
         ws_bytes = workspace.numel() * workspace.element_size()
-    st = _call(lib.attn_fwd_paged, q.device, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache),
-               _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(page_table), B, H,
-               Hkv, total_q, max_seqlen_q, pages, page_size, max_pages, d, _dtype_code(q),
-               q.stride(0), q.stride(1), sp, sh, st_, float(scale), int(bool(causal)),
-               window, _ptr(workspace), ws_bytes, _ptr(dev_status))
-    _raise(st, "attn_fwd_paged")
+    _call(lib.attn_fwd_paged, "attn_fwd_paged", dev.index, stream, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), cu, lens, table, B, H, Hkv, total_q,
+          max_seqlen_q, pages, page_size, max_pages, d, _dtype_code(q), strides[0], strides[1], sp,
+          sh, st, float(scale), int(bool(causal)), window, _ptr(workspace), ws_bytes,
+          _ptr(dev_status))
     return out, lse
 
 

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
             acc[2 * e + 1] += w * x.y;
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int head = t.hk * p.G + g;
     const size_t out_row = (static_cast<size_t>(t.q_start) + t.tok0 + tok) * p.lq.H + head;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + out_row * D) + lane * (PER / 2);
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
     for (int e = 0; e < PER / 2; ++e) dst[e] = pack_h2<kF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if (lane == 0)
         p.LSE[static_cast<size_t>(head) * p.lq.total + t.q_start + t.tok0 + tok] =
-            sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+            sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
 }  // namespace

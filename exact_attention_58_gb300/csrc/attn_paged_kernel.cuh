@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             tc_fence_after();
         }
         if (ok) {
-            const float inv = (l > 0.f) ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t piece_row =
                 (static_cast<size_t>(unit) * p.splits + split) * p.slot_rows + t * kTileRows + r;
             const size_t out_row = (static_cast<size_t>(sq.start) + tok) * p.lq.H + head;
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                 }
             }
             if (row_ok) {
-                const float lse2 = (l > 0.f) ? m_ref + log2f(l) : -INFINITY;
+                const float lse2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
                 if (joined) p.part_lse[piece_row] = lse2;
                 else p.LSE[static_cast<size_t>(head) * p.lq.total + sq.start + tok] = lse2 * kLn2;
             }

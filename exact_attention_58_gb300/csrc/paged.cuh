@@ -133,6 +133,13 @@ cudaError_t launch_paged_tiles(const CUtensorMap& tq, const CUtensorMap& tk, con
 cudaError_t launch_paged_tiles_d256(const CUtensorMap& tq, const CUtensorMap& tk,
                                     const CUtensorMap& tv, const PagedParams& p, bool f16,
                                     cudaStream_t stream);
+// Few query rows per request (max_seqlen_q * G <= 64): p.tiles persistent CTAs,
+// p.slot_rows = 16, 32 or 64 rows.
+cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedParams& p, int d, bool f16, cudaStream_t stream);
+cudaError_t launch_paged_decode_d256(const CUtensorMap& tq, const CUtensorMap& tk,
+                                     const CUtensorMap& tv, const PagedParams& p, bool f16,
+                                     cudaStream_t stream);
 // Joins the pieces of p.desc[0, descs).
 cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int d, bool f16,
                               cudaStream_t stream);

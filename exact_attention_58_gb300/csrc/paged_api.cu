@@ -42,17 +42,31 @@ attn_status check_cache(int Hkv, int d, attn_dtype dtype, int num_pages, int pag
     return ATTN_OK;
 }
 
-// How a call's queries are cut into tiles and how many CTAs share a tile.
-struct TilePlan {
-    int tile_tokens, tiles, uniform, splits;
-    size_t slots, descs;
-    int rows;
+// Which kernel runs, and over how many CTAs.
+struct Plan {
+    bool decode;           // attn_decode_kernel: few query rows per request
+    int tile_tokens;       // tokens of a query tile
+    int tiles, uniform, splits;
+    size_t slots, descs;   // pieces and joined tiles that the workspace holds
+    int rows;              // rows of a slot
 };
 
-TilePlan plan_tiles(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d) {
-    TilePlan t{};
+Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d) {
+    Plan t{};
+    const int G = H / Hkv;
+    const long long blocks = (max_keys + kTileRows - 1) / kTileRows;
+    if (static_cast<long long>(max_q) * G <= 64) {
+        t.decode = true;
+        t.tile_tokens = max_q;
+        t.rows = max_q * G <= 16 ? 16 : (max_q * G <= 32 ? 32 : 64);
+        t.tiles = static_cast<int>(std::min(static_cast<long long>(kSMs), blocks * Hkv * B));
+        t.splits = t.tiles > 1 && blocks > 1 ? 2 : 1;   // a tile can be cut
+        t.descs = t.tiles;
+        t.slots = 2 * t.descs;
+        return t;
+    }
     const int per_cta = d == 256 ? 1 : 2;
-    t.tile_tokens = kTileRows / (H / Hkv);
+    t.tile_tokens = kTileRows / G;
     const int cta_tokens = t.tile_tokens * per_cta;
     const long long per_request = (max_q + cta_tokens - 1) / cta_tokens;
     const long long packed = total_q / cta_tokens + static_cast<long long>(B);
@@ -62,7 +76,6 @@ TilePlan plan_tiles(int B, int H, int Hkv, int total_q, int max_q, long long max
     // With fewer CTAs than SMs the keys of a tile are shared out, as far as
     // all CTAs still run at once.
     const long long ctas = static_cast<long long>(t.tiles) * Hkv;
-    const long long blocks = (max_keys + kTileRows - 1) / kTileRows;
     t.splits = static_cast<int>(std::max(1ll, std::min(kSMs / ctas, blocks)));
     t.rows = per_cta * kTileRows;
     if (t.splits > 1) {
@@ -81,8 +94,11 @@ attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int
     if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<long long>(max_pages) * page_size > kMaxPagedKeys) return ATTN_ERR_UNSUPPORTED;
     if (total_q > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
-    const TilePlan t = plan_tiles(B, H, Hkv, total_q, std::min(max_q, total_q),
-                                  static_cast<long long>(max_pages) * page_size, d);
+    // key blocks of all heads of a request, counted in 32 bits on the device
+    if ((static_cast<long long>(max_pages) * page_size / kTileRows + 1) * Hkv >= (1ll << 31))
+        return ATTN_ERR_UNSUPPORTED;
+    const Plan t = plan_paged(B, H, Hkv, total_q, std::min(max_q, total_q),
+                              static_cast<long long>(max_pages) * page_size, d);
     if (static_cast<long long>(t.tiles) * Hkv * t.splits >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
@@ -210,7 +226,7 @@ size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int ma
                                      int max_pages, int page_size, int d) {
     if (check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d) != ATTN_OK)
         return 0;
-    const TilePlan t = plan_tiles(B, H, H_kv, total_q, std::min(max_seqlen_q, total_q),
+    const Plan t = plan_paged(B, H, H_kv, total_q, std::min(max_seqlen_q, total_q),
                                   static_cast<long long>(max_pages) * page_size, d);
     return t.slots == 0 ? 0 : pieces_bytes(t.slots, t.rows, d, t.descs);
 }
@@ -238,7 +254,7 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
         !aligned(page_table, 4))
         return ATTN_ERR_MISALIGNED;
     const int max_q = std::min(max_seqlen_q, total_q);
-    const TilePlan t = plan_tiles(B, H, H_kv, total_q, max_q,
+    const Plan t = plan_paged(B, H, H_kv, total_q, max_q,
                                   static_cast<long long>(max_pages) * page_size, d);
     PagedParams p{};
     if (t.slots > 0) {
@@ -278,10 +294,12 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
         return ATTN_ERR_CUDA;
     const bool f16 = dtype == ATTN_DTYPE_FP16;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_paged_tiles(tq, tk, tv, p, d, f16, s);
-    if (e == cudaSuccess && t.splits > 1)
-        e = launch_paged_join(p, static_cast<int>(t.descs), t.tile_tokens * p.G * (t.rows / kTileRows),
-                              d, f16, s);
+    cudaError_t e = t.decode ? launch_paged_decode(tq, tk, tv, p, d, f16, s)
+                             : launch_paged_tiles(tq, tk, tv, p, d, f16, s);
+    if (e == cudaSuccess && t.splits > 1) {
+        const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
+        e = launch_paged_join(p, static_cast<int>(t.descs), rows, d, f16, s);
+    }
     return from_cuda(e);
 }
 

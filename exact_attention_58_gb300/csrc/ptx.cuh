@@ -79,6 +79,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Whether the phase of `bar` with the given parity has completed, without
+// waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Single-thread bounded wait for the phase of `bar` with the given parity.
 // Returns false (and raises *abort) when the limit expires or another role has
 // already raised *abort.
@@ -188,6 +202,19 @@ __device__ __forceinline__ void grid_dep_launch_dependents() {
 // (1-15; 0 is the one __syncthreads uses).
 __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// The same barrier with a vote: true on every thread when `x` is on any.
+__device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return any != 0;
 }
 
 // Untiled bulk copy global -> shared (both 16-byte aligned, bytes % 16 == 0).

@@ -115,7 +115,8 @@ def cpu_args():
 
 def test_binding_refuses(lib):
     x, args = cpu_args()
-    with pytest.raises(ValueError, match="CUDA"):
+    refused = lambda: pytest.raises(ValueError, match="^(?!.*on a CUDA device)")  # noqa: E731
+    with pytest.raises(ValueError, match="on a CUDA device"):   # the last check
         ea.attn_fwd_paged(*args, 2)
     wrong = {0: [x.q[0], x.q.float(), x.q.transpose(1, 2)],
              1: [x.k_cache[0], x.k_cache.half(), x.k_cache[..., :32], x.k_cache[:, :1]],
@@ -125,25 +126,32 @@ def test_binding_refuses(lib):
              5: [x.cu[:2], x.cu.float()]}
     for i, bad in wrong.items():
         for t in bad:
-            with pytest.raises(ValueError):
+            with refused():
                 ea.attn_fwd_paged(*args[:i], t, *args[i + 1:], 2)
-    with pytest.raises(ValueError):
+    with refused():
         ea.attn_fwd_paged(*args, 2**32 + 1)
-    with pytest.raises(ValueError):
+    with refused():
         ea.attn_fwd_paged(*args, 2, window=2**32 + 5)
     k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     slots = torch.zeros(3, dtype=torch.int64)
     for bad in [(k, k[:2], slots), (k, k.transpose(0, 1).contiguous().transpose(0, 1), slots),
                 (k, k, slots.int()), (k, k, slots[:2]), (k[:, :1], k[:, :1], slots),
-                (k, k, slots)]:
-        with pytest.raises(ValueError):
+                (k, k.half(), slots), (k[0], k[0], slots), (k.float(), k.float(), slots)]:
+        with refused():
             ea.attn_cache_append(bad[0], bad[1], x.k_cache, x.v_cache, bad[2])
     i = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
     good = [i(1, 2), i(1, 1), x.page_table, i(1, 2, 3), i(3)]
     for at, t in [(0, i(1)), (1, i(1, 1).long()), (2, x.page_table[0]), (3, i(1, 2).reshape(1, 2)),
-                  (4, i(3, 3)), (4, i(3))]:
-        with pytest.raises(ValueError):
+                  (4, i(3, 3))]:
+        with refused():
             ea.attn_page_table(*good[:at], t, *good[at + 1:], 16, 8)
+    for tail in [(2**31, 8), (16, 2**31)]:
+        with refused():
+            ea.attn_page_table(*good, *tail)
+    with pytest.raises(ValueError, match="on a CUDA device"):
+        ea.attn_page_table(*good, 16, 8)
+    with pytest.raises(ValueError, match="on a CUDA device"):
+        ea.attn_cache_append(k, k, x.k_cache, x.v_cache, slots)
 
 
 def test_reference_attention_against_closed_forms():
