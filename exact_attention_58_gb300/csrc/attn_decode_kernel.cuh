@@ -19,11 +19,15 @@
 //     run, whatever the request lengths are.  Tiles (request, head) cut by a run's
 //     end are joined by a second launch (paged_join_kernel), at most two
 //     pieces per CTA.
-//   * The producer runs ahead over the ends of tiles: a ring of up to 176 KB
-//     of K/V tiles is in flight while the other warps finish a tile.
+//   * The producers run ahead over the ends of tiles: rings of up to 176 KB
+//     of K and V tiles are in flight while the other warps finish a tile.
 //
-// Warps 0-3: softmax, one key per thread.  Warp 4: TMA producer; walks the
-// run, tells the others each segment (a tile's part of the run).  Warp 5: MMA.
+// Warps 0-3: softmax, one key per thread.  Warp 4: walks the run, tells the
+// others each segment (a tile's part of the run), loads Q and K.  Warp 5: loads
+// V (a TMA instruction costs its warp about 65 cycles, and small pages take
+// many).  Warp 6: S^T products.  Warp 7: P V products; an issuing warp stalls on
+// every product and commit, and of these two neither waits for the other's
+// operands.
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
@@ -45,12 +49,13 @@ struct DecodeCfg {
     static constexpr int MISC = 2048;                        // barriers, segments, row values
     static constexpr int AVAIL = 232448 - 1024 - MISC - 2 * Q_BYTES - 2 * P_BYTES;
     static constexpr int NSLOT = AVAIL / SLOT < 11 ? AVAIL / SLOT : 11;
+    static constexpr int NK = (NSLOT + 1) / 2, NV = NSLOT / 2;   // K and V rings
     static constexpr int SMEM = 2 * Q_BYTES + 2 * P_BYTES + NSLOT * SLOT + MISC + 1024;
     static constexpr int HALVES = D == 256 ? 2 : 1;          // 128-lane halves of O^T
     static constexpr uint32_t O_COL = 2 * N;                 // S^T in [0, 2N), two buffers
     static constexpr uint32_t TMEM_COLS = 4 * N;
-    static constexpr int THREADS = 192;
-    static_assert(NSLOT >= 4, "K and V of two blocks in flight");
+    static constexpr int THREADS = 256;
+    static_assert(NV >= 2 && NV >= CHUNKS, "two slots a ring, and a tile");
 };
 
 // One tile's part of a CTA's run.
@@ -139,6 +144,54 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t t, const uint32_t (&r)[N])
     }
 }
 
+// Walks a CTA's run [u, end), segment by segment, with the whole warp:
+// body(request index, request, head, first block, blocks, first unit) returns
+// false to stop.  Returns whether the walk came to its end.
+template <typename Body>
+__device__ __forceinline__ bool walk_run(const PagedParams& p, int b, long long b_unit, long long u,
+                                         long long end, int lane, Body&& body) {
+    // lane x holds request win + x
+    auto load = [&](int at) {
+        return at + lane < p.B ? request_of(p, at + lane) : Request{0, 0, 0, 0, 0, 0, 0};
+    };
+    int win = b;
+    Request held = load(win);
+    int in_req = static_cast<int>(u - b_unit);   // unit within the request: head * units + block
+    while (u < end) {
+        Request r;
+        const int x = b - win;
+        r.start = __shfl_sync(0xffffffffu, held.start, x);
+        r.n = __shfl_sync(0xffffffffu, held.n, x);
+        r.L = __shfl_sync(0xffffffffu, held.L, x);
+        r.klo = __shfl_sync(0xffffffffu, held.klo, x);
+        r.khi = __shfl_sync(0xffffffffu, held.khi, x);
+        r.j0 = __shfl_sync(0xffffffffu, held.j0, x);
+        r.units = __shfl_sync(0xffffffffu, held.units, x);
+        const int hk = in_req / r.units, blk = in_req - hk * r.units;
+        const int nblk = static_cast<int>(min(static_cast<long long>(r.units - blk), end - u));
+        if (!body(b, r, hk, blk, nblk, u)) return false;
+        u += nblk;
+        in_req += nblk;
+        if (in_req == r.units * p.Hkv && u < end) {   // next request with queries
+            in_req = 0;
+            for (++b;;) {
+                if (b >= win + 32) {
+                    win = b;
+                    held = load(win);
+                }
+                const unsigned has = __ballot_sync(0xffffffffu, win + lane >= b && held.units > 0);
+                if (has != 0) {
+                    b = win + __ffs(has) - 1;
+                    break;
+                }
+                b = win + 32;
+                if (b >= p.B) return true;   // lengths changed under the kernel
+            }
+        }
+    }
+    return true;
+}
+
 template <int D, bool kF16, int N>
 __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -154,32 +207,37 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* sKV = smem;
-    uint8_t* sP = sKV + C::NSLOT * C::SLOT;      // two buffers
+    uint8_t* sK = smem;                          // NK slots
+    uint8_t* sV = sK + C::NK * C::SLOT;          // NV slots
+    uint8_t* sP = sV + C::NV * C::SLOT;          // two buffers
     uint8_t* sQ = sP + 2 * C::P_BYTES;           // two buffers
     uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + 2 * C::Q_BYTES);
     uint64_t* q_full = bars;            // [2] a segment and its queries are there
-    uint64_t* q_empty = bars + 2;       // [2] every role is done with them
+    uint64_t* q_empty = bars + 2;       // [2] both readers are done with them
     uint64_t* s_full = bars + 4;        // [2] S^T of a block
     uint64_t* p_full = bars + 6;        // [2] P^T of a block (V's edge cleared)
     uint64_t* pv_done = bars + 8;       // [2] O^T += V^T P^T of a block
-    uint64_t* bar_fin = bars + 10;
-    uint64_t* full = bars + 11;         // [NSLOT]
-    uint64_t* empty = full + 11;        // [NSLOT]
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(empty + 11);
+    uint64_t* bar_fin = bars + 10;      // [2] every MMA of an issuing warp
+    uint64_t* k_full = bars + 12;       // [NK]
+    uint64_t* k_empty = bars + 18;
+    uint64_t* v_full = bars + 24;       // [NV]
+    uint64_t* v_empty = bars + 30;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 36);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-    volatile Segment* s_seg = reinterpret_cast<volatile Segment*>(bars + 36);   // [2]
-    float* s_row = reinterpret_cast<float*>(bars + 48);   // [4][N]: maxima, then sums, of each warp
-    float* s_m = s_row + 4 * N;       // [N] reference maxima, log2 units
-    float* s_fac = s_m + N;           // [N] factors: of a rescale, then 1 / l
-    long long* s_scan = reinterpret_cast<long long*>(s_row);                    // set-up only
+    volatile int* s_kind = reinterpret_cast<volatile int*>(bars + 37);   // [2] of a block's P V
+    volatile Segment* s_seg = reinterpret_cast<volatile Segment*>(bars + 38);   // [2]
+    float* s_row = reinterpret_cast<float*>(bars + 50);   // [4][N]: maxima, then sums, of each warp
+    float* s_negm = s_row + 4 * N;    // [N] minus the reference maxima, log2 units
+    float* s_fac = s_negm + N;        // [N] factors: of a rescale, then 1 / l
+    long long* s_scan = reinterpret_cast<long long*>(s_row);   // set-up only
+    static_assert(C::NK <= 6 && C::NV <= 6, "ring barriers");
     static_assert(2 * sizeof(Segment) <= 12 * 8, "segments fit their place");
-    static_assert(48 * 8 + 6 * N * 4 <= C::MISC, "row values fit their place");
+    static_assert(50 * 8 + 6 * N * 4 <= C::MISC, "row values fit their place");
+    constexpr int kFirst = 1, kStop = 2;   // s_kind: O^T starts anew; no more blocks
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int cta = static_cast<int>(blockIdx.x);
-    const int ctas = static_cast<int>(gridDim.x);
 
     // ---- this CTA's run [u0, u1) of the key blocks of all requests and heads ----
     if (threadIdx.x == 0) {
@@ -189,16 +247,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], kSoftmax);
             mbar_init(&pv_done[s], 1);
+            mbar_init(&bar_fin[s], 1);
         }
-        mbar_init(bar_fin, 1);
-        for (int s = 0; s < C::NSLOT; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < C::NV; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
         }
         *s_abort = 0;
         fence_mbar_init();
     }
-    if (warp == 5) {
+    if (warp == 6) {
         tmem_alloc(s_tmem, C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -231,7 +293,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         all += total;
     }
     // No run is empty: the pieces of a tile are in consecutive CTAs.
-    const long long parts = min(all, static_cast<long long>(ctas));
+    const long long parts = min(all, static_cast<long long>(gridDim.x));
     const long long u0 = cta < parts ? all * cta / parts : 0;
     const long long u1 = cta < parts ? all * (cta + 1) / parts : 0;
     // request that holds unit u0, and where it starts
@@ -259,128 +321,99 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    const int at_b = u0 < u1 ? static_cast<int>(s_at[0]) : 0;
+    const long long at_u = u0 < u1 ? s_at[1] : 0;
+    __syncthreads();   // s_at shares its place with the row values
+
+    // One tile's chunk into a ring slot (whole warp).
+    auto load_chunk = [&](const CUtensorMap* map, uint8_t* slot, uint64_t* bar, const PageBox& box,
+                          uint32_t bytes, int c0, int hk) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (box.needed) {
+            const int page = page_box_checked(p, box);
+            uint8_t* dst = slot + lane * p.box_rows * 128;
+#pragma unroll
+            for (int cb = 0; cb < C::CCB; ++cb)
+                tma_load_4d(dst + cb * C::CB_BYTES, map, bar, c0 + cb * 64, box.row, hk, page);
+        }
+        __syncwarp();
+    };
+    // The K (or V) tiles of one segment through their ring.
+    auto load_tiles = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                          int slots, int& fills, int b, const Request& r, int hk, int blk, int nblk) {
+        if (r.khi <= r.klo) return true;
+        const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
+        const int jbeg = r.j0 + blk;
+        PageBox box = page_box(p, table, jbeg * kTileRows, r.klo, r.khi, lane);
+        for (int j = jbeg; j < jbeg + nblk; ++j) {
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
+                                   static_cast<uint32_t>(p.box_rows) * (2 * C::CW);
+            PageBox next = box;
+            if (j + 1 < jbeg + nblk) next = page_box(p, table, (j + 1) * kTileRows, r.klo, r.khi, lane);
+            for (int c = 0; c < C::CHUNKS; ++c, ++fills) {
+                const int slot = fills % slots;
+                if (!mbar_wait_warp_soon(&empty[slot], ((fills / slots) & 1) ^ 1, s_abort)) return false;
+                load_chunk(map, ring + slot * C::SLOT, &full[slot], box, bytes, c * C::CW, hk);
+            }
+            box = next;
+        }
+        return true;
+    };
+    // Every load of a ring has landed.
+    auto drain = [&](uint64_t* full, int slots, int fills) {
+        volatile int no_abort = 0;
+        for (int s = 0; s < slots && s < fills; ++s) {
+            const int uses = (fills - s + slots - 1) / slots;
+            mbar_wait(&full[s], (uses - 1) & 1, &no_abort);
+        }
+    };
 
     if (warp == 4) {
-        // ================= producer =================
-        const long long at_b = s_at[0], at_u = s_at[1];
-        __syncwarp();
-        if (lane == 0) p.desc[cta].n = 0;
-        int fills = 0;    // ring slots filled so far
-        int seg = 0;
-        bool ok = true;
-        if (u0 < u1) {
-            if (lane == 0) {
-                tma_prefetch_desc(&tmQ);
-                tma_prefetch_desc(&tmK);
-                tma_prefetch_desc(&tmV);
-            }
-            // lane x holds request win + x
-            int win = static_cast<int>(at_b), b = win;
-            Request held = win + lane < p.B ? request_of(p, win + lane) : Request{0, 0, 0, 0, 0, 0, 0};
-            int in_req = static_cast<int>(u0 - at_u);   // unit within the request: hk * units + block
-            long long u = u0;
-            while (u < u1 && ok) {
-                Request r;
-                {
-                    const int x = b - win;
-                    r.start = __shfl_sync(0xffffffffu, held.start, x);
-                    r.n = __shfl_sync(0xffffffffu, held.n, x);
-                    r.L = __shfl_sync(0xffffffffu, held.L, x);
-                    r.klo = __shfl_sync(0xffffffffu, held.klo, x);
-                    r.khi = __shfl_sync(0xffffffffu, held.khi, x);
-                    r.j0 = __shfl_sync(0xffffffffu, held.j0, x);
-                    r.units = __shfl_sync(0xffffffffu, held.units, x);
-                }
-                const int hk = in_req / r.units, blk = in_req - hk * r.units;
-                const int nblk = static_cast<int>(min(static_cast<long long>(r.units - blk), u1 - u));
-                const bool whole = nblk == r.units;
-                const bool none = r.khi <= r.klo;
-                const int buf = seg & 1;
-                ok = seg < 2 || mbar_wait_warp(&q_empty[buf], ((seg >> 1) & 1) ^ 1, s_abort);
-                if (!ok) break;
-                if (lane == 0) {
-                    volatile Segment& s = s_seg[buf];
-                    s.q_start = r.start;
-                    s.ntok = r.n;
-                    s.hk = hk;
-                    s.off = r.L - r.n;
-                    s.L = r.L;
-                    s.klo = r.klo;
-                    s.khi = r.khi;
-                    s.j0 = r.j0 + blk;
-                    s.nblk = nblk;
-                    s.out = whole ? -1 : 2 * cta + (blk == 0 ? 1 : 0);
-                    s.none = none;
-                    if (!whole && blk == 0) {   // this CTA has the tile's first piece
-                        const long long end = u + r.units;
-                        const long long last = (end * parts + all - 1) / all - 1;   // CTA that ends it
-                        p.desc[cta] = PieceDesc{r.start, 0, r.n, hk, static_cast<int>(last) - cta + 1,
-                                                2 * cta + 1, 2 * cta + 2, 2};
-                    }
-                    if (none) {
-                        mbar_arrive(&q_full[buf]);
-                    } else {
-                        mbar_arrive_expect_tx(&q_full[buf],
-                                              static_cast<uint32_t>(p.tile_tokens * p.G) * (2 * D));
-                        for (int cb = 0; cb < D / 64; ++cb)
-                            tma_load_3d(sQ + buf * C::Q_BYTES + cb * C::QCB_BYTES, &tmQ, &q_full[buf],
-                                        cb * 64, hk * p.G, r.start);
-                    }
-                }
-                __syncwarp();
-                if (!none) {
-                    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
-                    const int jbeg = r.j0 + blk;
-                    PageBox box = page_box(p, table, jbeg * kTileRows, r.klo, r.khi, lane);
-                    for (int j = jbeg; j < jbeg + nblk && ok; ++j) {
-                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
-                                               static_cast<uint32_t>(p.box_rows) * (2 * C::CW);
-                        PageBox next = box;
-                        if (j + 1 < jbeg + nblk) next = page_box(p, table, (j + 1) * kTileRows, r.klo, r.khi, lane);
-                        for (int part = 0; part < 2 * C::CHUNKS; ++part) {   // K, then V
-                            const int slot = fills % C::NSLOT;
-                            const uint32_t ph = (fills / C::NSLOT) & 1;
-                            if (!mbar_wait_warp(&empty[slot], ph ^ 1, s_abort)) {
-                                ok = false;
-                                break;
-                            }
-                            if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                            __syncwarp();
-                            if (box.needed) {
-                                const CUtensorMap* m = part < C::CHUNKS ? &tmK : &tmV;
-                                const int c0 = (part % C::CHUNKS) * C::CW;
-                                uint8_t* dst = sKV + slot * C::SLOT + lane * p.box_rows * 128;
-                                for (int cb = 0; cb < C::CCB; ++cb)
-                                    tma_load_4d(dst + cb * C::CB_BYTES, m, &full[slot], c0 + cb * 64, box.row,
-                                                hk, box.page);
-                            }
-                            __syncwarp();
-                            ++fills;
-                        }
-                        box = next;
-                    }
-                }
-                ++seg;
-                u += nblk;
-                in_req += nblk;
-                if (in_req == r.units * p.Hkv && u < u1) {   // next request with queries
-                    in_req = 0;
-                    int nb = -1;
-                    int from = b + 1;
-                    while (nb < 0 && from < p.B) {
-                        if (from >= win + 32) {
-                            win = from;
-                            held = win + lane < p.B ? request_of(p, win + lane) : Request{0, 0, 0, 0, 0, 0, 0};
-                        }
-                        const unsigned has = __ballot_sync(0xffffffffu, win + lane >= from && held.units > 0);
-                        if (has != 0) nb = win + __ffs(has) - 1;
-                        else from = win + 32;
-                    }
-                    if (nb < 0) break;   // cannot happen: the run ends inside the last request
-                    b = nb;
-                }
-            }
+        // ================= producer of segments, Q and K =================
+        if (lane == 0) {
+            p.desc[cta].n = 0;
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
         }
+        int fills = 0, seg = 0;
+        bool ok = walk_run(p, at_b, at_u, u0, u1, lane, [&](int b, const Request& r, int hk, int blk, int nblk,
+                                                            long long u) {
+            const int buf = seg & 1;
+            if (seg >= 2 && !mbar_wait_warp_soon(&q_empty[buf], ((seg >> 1) & 1) ^ 1, s_abort)) return false;
+            if (lane == 0) {
+                const bool whole = nblk == r.units, none = r.khi <= r.klo;
+                volatile Segment& s = s_seg[buf];
+                s.q_start = r.start;
+                s.ntok = r.n;
+                s.hk = hk;
+                s.off = r.L - r.n;
+                s.L = r.L;
+                s.klo = r.klo;
+                s.khi = r.khi;
+                s.j0 = r.j0 + blk;
+                s.nblk = nblk;
+                s.out = whole ? -1 : 2 * cta + (blk == 0 ? 1 : 0);
+                s.none = none;
+                if (!whole && blk == 0) {   // this CTA has the tile's first piece
+                    const long long end = u + r.units;
+                    const long long last = (end * parts + all - 1) / all - 1;   // CTA that ends it
+                    p.desc[cta] = PieceDesc{r.start, 0, r.n, hk, static_cast<int>(last) - cta + 1,
+                                            2 * cta + 1, 2 * cta + 2, 2};
+                }
+                if (none) {
+                    mbar_arrive(&q_full[buf]);
+                } else {
+                    mbar_arrive_expect_tx(&q_full[buf], static_cast<uint32_t>(p.tile_tokens * p.G) * (2 * D));
+                    for (int cb = 0; cb < D / 64; ++cb)
+                        tma_load_3d(sQ + buf * C::Q_BYTES + cb * C::QCB_BYTES, &tmQ, &q_full[buf], cb * 64,
+                                    hk * p.G, r.start);
+                }
+            }
+            __syncwarp();
+            ++seg;
+            return load_tiles(&tmK, sK, k_full, k_empty, C::NK, fills, b, r, hk, blk, nblk);
+        });
         // no more segments
         bool told = false;
         if (ok && (seg < 2 || mbar_wait_warp(&q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, s_abort))) {
@@ -396,55 +429,29 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         if (lane == 0) {
             volatile int no_abort = 0;
             for (int s = max(0, seg - (told ? 1 : 2)); s < seg; ++s) mbar_wait(&q_full[s & 1], (s >> 1) & 1, &no_abort);
-            for (int s = 0; s < C::NSLOT && s < fills; ++s) {
-                const int uses = (fills - s + C::NSLOT - 1) / C::NSLOT;
-                mbar_wait(&full[s], (uses - 1) & 1, &no_abort);
-            }
+            drain(k_full, C::NK, fills);
         }
         __syncwarp();
     } else if (warp == 5) {
-        // ================= MMA issuer =================
+        // ================= producer of V =================
+        if (lane == 0) tma_prefetch_desc(&tmV);
+        int fills = 0;
+        walk_run(p, at_b, at_u, u0, u1, lane, [&](int b, const Request& r, int hk, int blk, int nblk, long long) {
+            return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, b, r, hk, blk, nblk);
+        });
+        if (lane == 0) drain(v_full, C::NV, fills);
+        __syncwarp();
+    } else if (warp == 6) {
+        // ================= S^T = K Q^T =================
         if (lane == 0) {
-            const uint64_t dk0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
-            // V^T: 64 head-dim columns, the next 64 a column block on (for
-            // d = 64 the same again: lanes 64-127 of O^T are not used)
-            const uint64_t dv0 = sdesc_sw128(smem_u32(sKV), D == 64 ? 0 : C::CB_BYTES, 1024);
-            const uint64_t dp0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+            const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);
             const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
             constexpr uint32_t CA = C::CB_BYTES / 16 - 6, CQ = C::QCB_BYTES / 16 - 6;
-            int blk = 0;               // blocks issued, over all segments
-            int fill = 0;              // ring slot of the next K or V chunk
+            int blk = 0, fill = 0;   // blocks and ring chunks so far, over all segments
             bool ok = true;
-            // the block whose P V is still to come
-            bool have = false;
-            bool first = false;
-            int v_fill = 0;
-            auto wait_fill = [&](int f) { return mbar_wait(&full[f % C::NSLOT], (f / C::NSLOT) & 1, s_abort); };
-            auto pv = [&]() {   // O^T (+)= V^T P^T of block blk - 1
-                const int i = blk - 1;
-                if (!mbar_wait(&p_full[i & 1], (i >> 1) & 1, s_abort)) return false;
-                tc_fence_after();
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    if (!wait_fill(v_fill + c)) return false;
-                    tc_fence_after();
-                    const int slot = (v_fill + c) % C::NSLOT;
-                    mma8_ss_f16<128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128>(
-                        tmem + C::O_COL + c * N, sdesc_adv(dv0, slot * C::SLOT),
-                        sdesc_adv(dp0, (i & 1) * C::P_BYTES), IDESC_O, first ? 0u : 1u);
-                    tc_commit(&empty[slot]);
-                }
-                tc_commit(&pv_done[i & 1]);
-                have = false;
-                return true;
-            };
             for (int seg = 0; ok; ++seg) {
                 const int buf = seg & 1;
-                // let the last block's P V go first if the next segment is not there yet
-                if (have && !mbar_test(&q_full[buf], (seg >> 1) & 1)) ok = pv();
-                if (!ok || !mbar_wait(&q_full[buf], (seg >> 1) & 1, s_abort)) {
-                    ok = false;
-                    break;
-                }
+                if (!mbar_wait(&q_full[buf], (seg >> 1) & 1, s_abort)) break;
                 tc_fence_after();
                 const int nblk = s_seg[buf].nblk;
                 if (nblk == 0) break;
@@ -452,14 +459,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     mbar_arrive(&q_empty[buf]);
                     continue;
                 }
-                for (int x = 0; x < nblk && ok; ++x) {
-                    // S^T of this block before P V of the one before it, unless K is late
-                    if (have && !mbar_test(&full[fill % C::NSLOT], (fill / C::NSLOT) & 1)) ok = pv();
-                    for (int c = 0; c < C::CHUNKS && ok; ++c) {
-                        ok = wait_fill(fill + c);
+                for (int x = 0; x < nblk && ok; ++x, ++blk) {
+                    // S^T's buffer is read once P^T of two blocks before is there
+                    ok = blk < 2 || mbar_wait(&p_full[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
+                    for (int c = 0; c < C::CHUNKS && ok; ++c, ++fill) {
+                        const int slot = fill % C::NK;
+                        ok = mbar_wait(&k_full[slot], (fill / C::NK) & 1, s_abort);
                         if (!ok) break;
                         tc_fence_after();
-                        const int slot = (fill + c) % C::NSLOT;
                         const uint64_t ad = sdesc_adv(dk0, slot * C::SLOT);
                         const uint64_t bd = sdesc_adv(dq0, buf * C::Q_BYTES + c * C::CCB * C::QCB_BYTES);
                         if constexpr (D == 64)
@@ -467,25 +474,48 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                         else
                             mma8_ss_f16<2, 2, 2, CA, 2, 2, 2, 2, 2, 2, CQ, 2, 2, 2>(
                                 tmem + (blk & 1) * N, ad, bd, IDESC_S, c > 0 ? 1u : 0u);
-                        tc_commit(&empty[slot]);
+                        if (c == C::CHUNKS - 1) tc_commit(&s_full[blk & 1]);
+                        tc_commit(&k_empty[slot]);
                     }
-                    if (!ok) break;
-                    tc_commit(&s_full[blk & 1]);
-                    if (x == nblk - 1) tc_commit(&q_empty[buf]);
-                    if (have) ok = pv();
-                    if (!ok) break;
-                    have = true;
-                    first = x == 0;
-                    v_fill = fill + C::CHUNKS;
-                    fill += 2 * C::CHUNKS;
-                    ++blk;
+                    if (ok && x == nblk - 1) tc_commit(&q_empty[buf]);
                 }
             }
-            if (ok && have) ok = pv();
-            // Drain: no MMA of this CTA is in flight at teardown.
-            tc_commit(bar_fin);
+            // Drain: no MMA of this warp is in flight at teardown.
+            tc_commit(&bar_fin[0]);
             volatile int no_abort = 0;
-            mbar_wait(bar_fin, 0, &no_abort);
+            mbar_wait(&bar_fin[0], 0, &no_abort);
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ================= O^T (+)= V^T P^T =================
+        if (lane == 0) {
+            // V^T: 64 head-dim columns, the next 64 a column block on (for
+            // d = 64 the same again: lanes 64-127 of O^T are not used)
+            const uint64_t dv0 = sdesc_sw128(smem_u32(sV), D == 64 ? 0 : C::CB_BYTES, 1024);
+            const uint64_t dp0 = sdesc_sw128(smem_u32(sP), 16, 1024);
+            int fill = 0;
+            bool ok = true;
+            for (int blk = 0; ok; ++blk) {
+                if (!mbar_wait(&p_full[blk & 1], (blk >> 1) & 1, s_abort)) break;
+                tc_fence_after();
+                const int kind = s_kind[blk & 1];
+                if (kind == kStop) break;
+                for (int c = 0; c < C::CHUNKS; ++c, ++fill) {
+                    const int slot = fill % C::NV;
+                    ok = mbar_wait(&v_full[slot], (fill / C::NV) & 1, s_abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma8_ss_f16<128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128>(
+                        tmem + C::O_COL + c * N, sdesc_adv(dv0, slot * C::SLOT),
+                        sdesc_adv(dp0, (blk & 1) * C::P_BYTES), IDESC_O, kind == kFirst ? 0u : 1u);
+                    if (c == C::CHUNKS - 1) tc_commit(&pv_done[blk & 1]);
+                    tc_commit(&v_empty[slot]);
+                }
+            }
+            // Drain: no MMA of this warp is in flight at teardown.
+            tc_commit(&bar_fin[1]);
+            volatile int no_abort = 0;
+            mbar_wait(&bar_fin[1], 0, &no_abort);
         }
         __syncwarp();
     } else {
@@ -495,8 +525,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         const uint32_t t_O = t_lane + C::O_COL;
         const int G = p.G;
         const float sc = p.scale_log2;
+        const uint64_t sc2 = f2_pack(sc, sc);
         int blk = 0;    // blocks so far, over all segments
-        int fill = 0;   // ring slot of the next K chunk
         bool ok = true;
         for (int seg = 0;; ++seg) {
             const int buf = seg & 1;
@@ -520,13 +550,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             s.none = s_seg[buf].none;
             mbar_arrive_warp(&q_empty[buf]);
             const int rows = s.ntok * G;
-            float l[N];   // this thread's sums
+            uint64_t l[N / 2];   // this thread's sums, two rows each
 #pragma unroll
-            for (int n = 0; n < N; ++n) l[n] = 0.f;
-            for (int x = 0; x < (s.none ? 0 : s.nblk); ++x, ++blk, fill += 2 * C::CHUNKS) {
+            for (int n = 0; n < N / 2; ++n) l[n] = f2_pack(0.f, 0.f);
+            for (int x = 0; x < (s.none ? 0 : s.nblk); ++x, ++blk) {
                 const int k0 = (s.j0 + x) * kTileRows;
                 const int key = k0 + tid;
-                ok = ok && mbar_wait_warp(&s_full[blk & 1], (blk >> 1) & 1, s_abort);
+                ok = ok && mbar_wait_warp_soon(&s_full[blk & 1], (blk >> 1) & 1, s_abort);
                 tc_fence_after();
                 uint32_t sr[N];
                 tmem_ld_cols<N>(t_lane + (blk & 1) * N, sr);
@@ -540,134 +570,138 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 const bool sliding = p.window > 0 &&
                                      (k0 < s.off + s.ntok - p.window ||
                                       (!p.causal && k0 + kTileRows - 1 > s.off + p.window - 1));
-                float v[N];
                 if (cut || diagonal || sliding) {
                     int pos = s.off, g = 0;   // key position of row n
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        bool ok_n = n < rows && key >= s.klo && key < s.khi;
-                        if (p.causal) ok_n = ok_n && key <= pos;
-                        if (p.window > 0) ok_n = ok_n && pos - key < p.window && (p.causal || key - pos < p.window);
-                        v[n] = ok_n ? __uint_as_float(sr[n]) * sc : -INFINITY;
+                        bool in = key >= s.klo && key < s.khi;
+                        if (p.causal) in = in && key <= pos;
+                        if (p.window > 0) in = in && pos - key < p.window && (p.causal || key - pos < p.window);
+                        if (!in) sr[n] = __float_as_uint(-INFINITY);
                         if (++g == G) {
                             g = 0;
                             ++pos;
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < N; ++n) v[n] = __uint_as_float(sr[n]) * sc;
                 }
+                // Exponents s scale log2e - m, two rows at a time.  Rows past the
+                // tile's have m = inf: exponent -inf, weight 0.
+                auto exponents = [&](int c, float (&e)[8]) {   // of rows 8 c .. 8 c + 7
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = 8 * c + 2 * i;
+                        const uint64_t nm = reinterpret_cast<const uint64_t*>(s_negm)[n / 2];
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1])), sc2, nm),
+                                  e[2 * i], e[2 * i + 1]);
+                    }
+                };
                 bool grows = x == 0;
                 if (x > 0) {
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < N / 4; ++c) {
-                        const float4 m4 = reinterpret_cast<const float4*>(s_m)[c];
-                        const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            grows |= 4 * c + e < rows && v[4 * c + e] > mm[e] + kRescaleThreshold;
+                    for (int c = 0; c < N / 8; ++c) {
+                        float e[8];
+                        exponents(c, e);
+                        mx = max3f(max3f(e[0], e[1], e[2]), max3f(e[3], e[4], e[5]), max3f(e[6], e[7], mx));
                     }
+                    grows = mx > kRescaleThreshold;
                 }
                 if (named_barrier_or(1, kSoftmax, grows)) {
                     // new reference maxima: over the warp's keys, then over the four warps
                     float mine_max = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(v[n])));
+                        const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(__uint_as_float(sr[n]))));
                         if ((n & 31) == lane) mine_max = wm;
                         if ((n & 31) == 31 || n == N - 1)
                             if (lane < N) s_row[warp * N + (n & ~31) + lane] = mine_max;
                     }
                     named_barrier_sync(1, kSoftmax);
                     if (tid < N) {
-                        const float old = x > 0 ? s_m[tid] : kNoMax;
-                        const float mt = fmaxf(fmaxf(old, fmaxf(s_row[tid], s_row[N + tid])),
-                                               fmaxf(s_row[2 * N + tid], s_row[3 * N + tid]));
-                        s_m[tid] = mt;
-                        s_fac[tid] = ex2_approx(old - mt);
+                        const float old = x > 0 ? -s_negm[tid] : kNoMax;
+                        const float mt = fmaxf(old, sc * fmaxf(fmaxf(s_row[tid], s_row[N + tid]),
+                                                               fmaxf(s_row[2 * N + tid], s_row[3 * N + tid])));
+                        s_negm[tid] = tid < rows ? -mt : -INFINITY;
+                        s_fac[tid] = tid < rows ? ex2_approx(old - mt) : 0.f;
                     }
                     named_barrier_sync(1, kSoftmax);
                     if (x > 0) {   // sums and O^T columns, once P V of the block before is in
                         ok = ok && mbar_wait_warp(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
                         tc_fence_after();
 #pragma unroll
-                        for (int n = 0; n < N; ++n) l[n] *= s_fac[n];
-#pragma unroll
-                        for (int h = 0; h < C::HALVES; ++h) {
-                            uint32_t o[N];
-                            tmem_ld_cols<N>(t_O + h * N, o);
+                        for (int n = 0; n < N / 2; ++n) l[n] = f2_mul(l[n], reinterpret_cast<const uint64_t*>(s_fac)[n]);
+#pragma unroll 1
+                        for (int c = 0; c < C::HALVES * N / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(t_O + 16 * c, o);
                             tmem_ld_wait();
                             reg_fence(o);
 #pragma unroll
-                            for (int n = 0; n < N; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[n]);
-                            tmem_st_cols<N>(t_O + h * N, o);
+                            for (int n = 0; n < 16; ++n)
+                                o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[(16 * c + n) % N]);
+                            tmem_st16(t_O + 16 * c, o);
                         }
                         tmem_st_wait();
                     }
                 }
                 // P^T: this key's N weights, rounded to the storage type for the
                 // product with V; the sum takes them unrounded
-                if (blk >= 2) ok = ok && mbar_wait_warp(&pv_done[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
+                if (blk >= 2) ok = ok && mbar_wait_warp_soon(&pv_done[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
                 uint8_t* row = sP + (blk & 1) * C::P_BYTES + tid * 128;
 #pragma unroll
                 for (int c = 0; c < N / 8; ++c) {
-                    const float4 ma = reinterpret_cast<const float4*>(s_m)[2 * c];
-                    const float4 mb = reinterpret_cast<const float4*>(s_m)[2 * c + 1];
-                    const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+                    float e[8];
+                    exponents(c, e);
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int n = 8 * c + 2 * e;
-                        const float p0 = ex2_approx(v[n] - mm[2 * e]);
-                        const float p1 = ex2_approx(v[n + 1] - mm[2 * e + 1]);
-                        l[n] += p0;
-                        l[n + 1] += p1;
-                        w[e] = pack_h2<kF16>(p0, p1);
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = ex2_approx(e[2 * i]);
+                        const float p1 = ex2_approx(e[2 * i + 1]);
+                        l[4 * c + i] = f2_add(l[4 * c + i], f2_pack(p0, p1));
+                        w[i] = pack_h2<kF16>(p0, p1);
                     }
                     *reinterpret_cast<uint4*>(row + ((c ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 if (cut) {
                     // V rows of keys outside [klo, khi) become zero.  Their slots'
                     // fills before this one must have landed, or the parity would
-                    // be theirs: with two slots a tile that takes P V of the block
-                    // before.
+                    // be theirs: with a tile in two slots that takes P V of the
+                    // block before, else that of two blocks before (above).
                     if (C::CHUNKS == 2 && blk > 0)
                         ok = ok && mbar_wait_warp(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
                     for (int c = 0; c < C::CHUNKS; ++c) {
-                        const int f = fill + C::CHUNKS + c;
-                        ok = ok && mbar_wait_warp(&full[f % C::NSLOT], (f / C::NSLOT) & 1, s_abort);
+                        const int f = C::CHUNKS * blk + c;
+                        ok = ok && mbar_wait_warp(&v_full[f % C::NV], (f / C::NV) & 1, s_abort);
                         if (ok && (key < s.klo || key >= s.khi)) {
                             for (int cb = 0; cb < C::CCB; ++cb) {
-                                uint4* vr = reinterpret_cast<uint4*>(sKV + (f % C::NSLOT) * C::SLOT +
-                                                                     cb * C::CB_BYTES + tid * 128);
+                                uint4* vr = reinterpret_cast<uint4*>(sV + (f % C::NV) * C::SLOT + cb * C::CB_BYTES +
+                                                                     tid * 128);
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) vr[e] = make_uint4(0u, 0u, 0u, 0u);
                             }
                         }
                     }
                 }
+                if (tid == 0) s_kind[blk & 1] = x == 0 ? kFirst : 0;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive_warp(&p_full[blk & 1]);
             }
             // ---- the segment's result: sums over all keys, O = acc / l ----
-            if (!s.none) {
-                const int last = blk - 1;
-                ok = ok && mbar_wait_warp(&pv_done[last & 1], (last >> 1) & 1, s_abort);
-                tc_fence_after();
-            }
-            const int col = warp_sum_scatter<N>(l, lane);
+            float ls[N];
+#pragma unroll
+            for (int n = 0; n < N / 2; ++n) f2_unpack(l[n], ls[2 * n], ls[2 * n + 1]);
+            const int col = warp_sum_scatter<N>(ls, lane);
             if (N >= 32 || (lane & 1) == 0) {
-                s_row[warp * N + col] = l[0];
-                if (N == 64) s_row[warp * N + col + 1] = l[1];
+                s_row[warp * N + col] = ls[0];
+                if (N == 64) s_row[warp * N + col + 1] = ls[1];
             }
             named_barrier_sync(1, kSoftmax);
             if (tid < N) {
                 const float sum = (s_row[tid] + s_row[N + tid]) + (s_row[2 * N + tid] + s_row[3 * N + tid]);
                 s_fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
                 if (tid < rows) {
-                    const float lse2 = sum == 0.f ? -INFINITY : s_m[tid] + log2f(sum);
+                    const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - s_negm[tid];
                     if (s.out >= 0) {
                         p.part_lse[static_cast<size_t>(s.out) * p.slot_rows + tid] = lse2;
                     } else {
@@ -677,32 +711,45 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     }
                 }
             }
+            if (!s.none) {
+                const int last = blk - 1;
+                ok = ok && mbar_wait_warp(&pv_done[last & 1], (last >> 1) & 1, s_abort);
+                tc_fence_after();
+            }
             named_barrier_sync(1, kSoftmax);
-#pragma unroll
+            // Row n of lane d: consecutive lanes, consecutive columns of a row.
+            // A piece's rows are D floats apart, the output's H D after the last
+            // head of a token.
+            const size_t out0 = s.out >= 0 ? static_cast<size_t>(s.out) * p.slot_rows * D
+                                           : (static_cast<size_t>(s.q_start) * p.lq.H + s.hk * G) * D;
+            const size_t skip = s.out >= 0 ? 0 : static_cast<size_t>(p.lq.H - G) * D;
+#pragma unroll 1
             for (int h = 0; h < C::HALVES; ++h) {
-                uint32_t o[N];
-                if (!s.none) {
-                    tmem_ld_cols<N>(t_O + h * N, o);
-                    tmem_ld_wait();
-                    reg_fence(o);
-                } else {
+                size_t at = out0 + h * 128 + tid;
+                int g = 0;
+#pragma unroll 1
+                for (int c = 0; c < N / 16; ++c) {
+                    if (16 * c >= rows) break;
+                    uint32_t o[16];
+                    if (!s.none) {
+                        tmem_ld16(t_O + h * N + 16 * c, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < N; ++n) o[n] = 0u;
-                }
-                if (D >= 128 || tid < D) {
-                    const int dcol = h * 128 + tid;
-                    size_t at = s.out >= 0 ? static_cast<size_t>(s.out) * p.slot_rows * D + dcol
-                                           : (static_cast<size_t>(s.q_start) * p.lq.H + s.hk * G) * D + dcol;
-                    const size_t skip = s.out >= 0 ? 0 : static_cast<size_t>(p.lq.H - G) * D;   // to the next token
-                    int g = 0;
+                        for (int n = 0; n < 16; ++n) o[n] = 0u;
+                    }
+                    if (D >= 128 || tid < D) {
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        if (n < rows) {
-                            const float x = __uint_as_float(o[n]) * s_fac[n];
-                            if (s.out >= 0)
-                                p.part_o[at] = x;
-                            else
-                                static_cast<uint16_t*>(p.O)[at] = static_cast<uint16_t>(pack_h2<kF16>(x, 0.f));
+                        for (int n = 0; n < 16; ++n) {
+                            if (16 * c + n < rows) {
+                                const float y = __uint_as_float(o[n]) * s_fac[16 * c + n];
+                                if (s.out >= 0)
+                                    p.part_o[at] = y;
+                                else
+                                    static_cast<uint16_t*>(p.O)[at] =
+                                        static_cast<uint16_t>(pack_h2<kF16>(y, 0.f));
+                            }
                             at += D;
                             if (++g == G) {
                                 g = 0;
@@ -710,12 +757,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                             }
                         }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             // O^T is read: the next segment's first P V, which overwrites it,
             // waits for P^T of these threads.
             tc_fence_before();
+        }
+        if (ok) {   // tell the P V warp
+            if (tid == 0) s_kind[blk & 1] = kStop;
+            mbar_arrive_warp(&p_full[blk & 1]);
         }
     }
 
@@ -723,7 +774,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == 6) tmem_dealloc(tmem, C::TMEM_COLS);
     if (threadIdx.x == 0 && *s_abort && p.dev_status != nullptr)
         atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_DEVICE_TIMEOUT));
     if (blockIdx.x == 0) paged_report(p);

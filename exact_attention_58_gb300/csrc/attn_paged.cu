@@ -7,18 +7,25 @@ namespace {
 
 // Joins the pieces of split tiles.  Row r of a tile has n pieces (O_i, lse2_i)
 // over disjoint key sets: with M = max lse2_i and w_i = exp2(lse2_i - M),
-// O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2.  One warp per
-// row, 4 floats of d per lane and step; the pieces were written by the launch
-// before and come from L2.
+// O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2.  The pieces were
+// written by the launch before and come from L2, so the time is that of the
+// dependent loads: lse2 of all pieces at once, then the O_i several at a time.
+// A row takes one warp, or four that share its pieces (after the decode
+// kernel, which can cut one long context into as many pieces as there are
+// CTAs), and a fixed order of sums either way.
 constexpr int kJoinWarps = 4;
 
-template <int D, bool kF16>
+template <int D, bool kF16, int kPerRow>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedParams p) {
     grid_dep_wait();
+    constexpr int PER = D / 32;   // floats of a lane
+    __shared__ float s_acc[kPerRow > 1 ? kPerRow : 1][D];
+    __shared__ float s_sum[kJoinWarps];
     const PieceDesc t = p.desc[blockIdx.x];
-    const int u = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);   // (token, head of the group)
-    if (t.n == 0 || u >= t.ntok * p.G) return;
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % kPerRow;
+    const int u = blockIdx.y * (kJoinWarps / kPerRow) + warp / kPerRow;   // (token, head of the group)
+    if (t.n == 0 || u >= t.ntok * p.G) return;   // the same for all warps of a row
     const int tok = u / p.G, g = u - tok * p.G;
     const int row = tok / p.tile_tokens * kTileRows + (tok % p.tile_tokens) * p.G + g;
     auto piece_row = [&](int i) {
@@ -30,21 +37,41 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     const float m0 = M == -INFINITY ? 0.f : M;
-    constexpr int PER = D / 32;   // floats of a lane
     float acc[PER], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < t.n; ++i) {
-        const size_t at = piece_row(i);
-        const float w = ex2_approx(p.part_lse[at] - m0);
-        sum += w;
-        const float2* src = reinterpret_cast<const float2*>(p.part_o + at * D) + lane * (PER / 2);
+    for (int i0 = part; i0 < t.n; i0 += 32 * kPerRow) {
+        // lane x: the weight of piece i0 + x * kPerRow
+        const int mine = i0 + lane * kPerRow;
+        const float w_mine = mine < t.n ? ex2_approx(p.part_lse[piece_row(mine)] - m0) : 0.f;
+        const int count = min(32, (t.n - i0 + kPerRow - 1) / kPerRow);
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+            const float w = __shfl_sync(0xffffffffu, w_mine, k);
+            sum += w;
+            const float2* src = reinterpret_cast<const float2*>(p.part_o + piece_row(i0 + k * kPerRow) * D) +
+                                lane * (PER / 2);
 #pragma unroll
-        for (int e = 0; e < PER / 2; ++e) {
-            const float2 x = src[e];
-            acc[2 * e] += w * x.x;
-            acc[2 * e + 1] += w * x.y;
+            for (int e = 0; e < PER / 2; ++e) {
+                const float2 x = src[e];
+                acc[2 * e] += w * x.x;
+                acc[2 * e + 1] += w * x.y;
+            }
+        }
+    }
+    if constexpr (kPerRow > 1) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) s_acc[part][lane * PER + e] = acc[e];
+        if (lane == 0) s_sum[part] = sum;
+        __syncthreads();
+        if (part != 0) return;
+        sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+        for (int w = 0; w < kPerRow; ++w) {
+            sum += s_sum[w];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += s_acc[w][lane * PER + e];
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -58,12 +85,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
             sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
+template <int D, bool kF16>
+cudaError_t launch_join_t(const cudaLaunchConfig_t& cfg, int warps, const PagedParams& p) {
+    return warps == 1 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, 1>, p)
+                      : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, kJoinWarps>, p);
+}
+
 }  // namespace
 
-cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int d, bool f16,
+cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int warps, int d, bool f16,
                               cudaStream_t stream) {
+    const int per_cta = kJoinWarps / warps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(descs), static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    cfg.gridDim = dim3(static_cast<unsigned>(descs), static_cast<unsigned>((rows + per_cta - 1) / per_cta));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -72,12 +106,9 @@ cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int d, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (d) {
-        case 64: return f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<64, true>, p)
-                            : cudaLaunchKernelEx(&cfg, paged_join_kernel<64, false>, p);
-        case 128: return f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<128, true>, p)
-                             : cudaLaunchKernelEx(&cfg, paged_join_kernel<128, false>, p);
-        case 256: return f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<256, true>, p)
-                             : cudaLaunchKernelEx(&cfg, paged_join_kernel<256, false>, p);
+        case 64: return f16 ? launch_join_t<64, true>(cfg, warps, p) : launch_join_t<64, false>(cfg, warps, p);
+        case 128: return f16 ? launch_join_t<128, true>(cfg, warps, p) : launch_join_t<128, false>(cfg, warps, p);
+        case 256: return f16 ? launch_join_t<256, true>(cfg, warps, p) : launch_join_t<256, false>(cfg, warps, p);
     }
     return cudaErrorInvalidValue;
 }

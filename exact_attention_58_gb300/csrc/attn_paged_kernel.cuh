@@ -214,11 +214,12 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                     if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     __syncwarp();
                     if (box.needed) {
+                        const int page = page_box_checked(p, box);
                         uint8_t* dst = sKV + slot * C::TILE + lane * p.box_rows * 128;
                         const CUtensorMap* m = which ? &tmV : &tmK;
                         for (int cb = 0; cb < C::NCB; ++cb)
                             tma_load_4d(dst + cb * C::CB_BYTES, m, &full[slot], cb * C::BOXW, box.row,
-                                        hk, box.page);
+                                        hk, page);
                     }
                     __syncwarp();
                     ++seq;

@@ -36,6 +36,7 @@ struct PagedParams {
     SeqLayout lq;               // packed queries: cu, H, N = max_seqlen_q, total
     int B, Hkv, G;              // G = H / Hkv query heads read one key/value head
     int num_pages, page_size, max_pages;
+    unsigned long long page_magic;   // floor(2^62 / page_size) + 1
     int box_rows;               // keys of one TMA box: the power of two dividing page_size, <= 128
     int tile_tokens;            // tokens of one 128-row query tile (rows are (token, head of the group))
     int causal, window;
@@ -91,23 +92,25 @@ struct PageBox {
     int row;
 };
 
+// Reads the box's table entry; page_box_checked() is for when it is used, a
+// tile later, so that nothing waits for the load.
 __device__ __forceinline__ PageBox page_box(const PagedParams& p, const int32_t* table, int k0,
                                             int klo, int khi, int lane) {
     PageBox x{false, 0, 0};
     const int key = k0 + lane * p.box_rows;
     if (lane * p.box_rows < kTileRows && key < khi && key + p.box_rows > klo) {
         x.needed = true;
-        const int col = key / p.page_size;
+        // key / page_size: exact, key * page_size < 2^62
+        const int col = static_cast<int>(__umul64hi(static_cast<unsigned long long>(key) << 2, p.page_magic));
         x.row = key - col * p.page_size;
         x.page = table[col];
-        if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(p.num_pages)) {
-            // outside the cache: the load fills zeros
-            x.page = p.num_pages;
-            if (p.dev_status != nullptr)
-                atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
-        }
     }
     return x;
+}
+__device__ __forceinline__ int page_box_checked(const PagedParams& p, const PageBox& x) {
+    if (static_cast<unsigned>(x.page) < static_cast<unsigned>(p.num_pages)) return x.page;
+    if (p.dev_status != nullptr) atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+    return p.num_pages;   // outside the cache: the load fills zeros
 }
 
 // Host side of the partial results: bytes of `slots` slots of `rows` rows and
@@ -140,8 +143,9 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tk, co
 cudaError_t launch_paged_decode_d256(const CUtensorMap& tq, const CUtensorMap& tk,
                                      const CUtensorMap& tv, const PagedParams& p, bool f16,
                                      cudaStream_t stream);
-// Joins the pieces of p.desc[0, descs).
-cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int d, bool f16,
+// Joins the pieces of p.desc[0, descs), up to `rows` rows each, with 1 or 4
+// warps a row.
+cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, int warps, int d, bool f16,
                               cudaStream_t stream);
 
 }  // namespace gbattn

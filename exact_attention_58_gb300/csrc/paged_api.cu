@@ -275,6 +275,7 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     p.num_pages = num_pages;
     p.page_size = page_size;
     p.max_pages = max_pages;
+    p.page_magic = (1ull << 62) / static_cast<unsigned long long>(page_size) + 1;
     p.box_rows = std::min(kTileRows, page_size & -page_size);
     p.tile_tokens = t.tile_tokens;
     p.causal = causal != 0;
@@ -298,7 +299,7 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
                              : launch_paged_tiles(tq, tk, tv, p, d, f16, s);
     if (e == cudaSuccess && t.splits > 1) {
         const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
-        e = launch_paged_join(p, static_cast<int>(t.descs), rows, d, f16, s);
+        e = launch_paged_join(p, static_cast<int>(t.descs), rows, t.decode ? 4 : 1, d, f16, s);
     }
     return from_cuda(e);
 }

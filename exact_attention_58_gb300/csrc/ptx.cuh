@@ -79,20 +79,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Whether the phase of `bar` with the given parity has completed, without
-// waiting for it.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Single-thread bounded wait for the phase of `bar` with the given parity.
 // Returns false (and raises *abort) when the limit expires or another role has
 // already raised *abort.
@@ -131,6 +117,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
             }
         }
     }
+}
+
+// The same for waits that are often over when they start: the timer, whose
+// reading alone takes about 100 cycles, is left alone until the first poll
+// has failed.
+__device__ __forceinline__ bool mbar_wait_warp_soon(uint64_t* bar, uint32_t parity,
+                                                    volatile int* abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, abort);
 }
 
 // ---------------------------------------------------------------------------
