@@ -46,11 +46,11 @@ struct DecodeCfg {
     static constexpr int QCB_BYTES = N * 128;                // Q: column blocks of N rows
     static constexpr int Q_BYTES = (D / 64) * QCB_BYTES;
     static constexpr int P_BYTES = kTileRows * 128;          // P^T: 128 keys of up to 64 rows
-    static constexpr int MISC = 2048;                        // barriers, segments, row values
-    static constexpr int AVAIL = 232448 - 1024 - MISC - 2 * Q_BYTES - 2 * P_BYTES;
+    static constexpr int MISC = 3072;                        // barriers, segments, row values
+    static constexpr int AVAIL = 232448 - MISC - 2 * Q_BYTES - 2 * P_BYTES;
     static constexpr int NSLOT = AVAIL / SLOT < 11 ? AVAIL / SLOT : 11;
     static constexpr int NK = (NSLOT + 1) / 2, NV = NSLOT / 2;   // K and V rings
-    static constexpr int SMEM = 2 * Q_BYTES + 2 * P_BYTES + NSLOT * SLOT + MISC + 1024;
+    static constexpr int SMEM = 2 * Q_BYTES + 2 * P_BYTES + NSLOT * SLOT + MISC;
     static constexpr int HALVES = D == 256 ? 2 : 1;          // 128-lane halves of O^T
     static constexpr uint32_t O_COL = 2 * N;                 // S^T in [0, 2N), two buffers
     static constexpr uint32_t TMEM_COLS = 4 * N;
@@ -204,9 +204,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     constexpr uint32_t IDESC_O = idesc_f32acc(128, N, FMT, true, true);
     grid_dep_wait();
     grid_dep_launch_dependents();   // the join: it waits for this grid itself
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled tiles need 1024-byte alignment
+        if (threadIdx.x == 0) {
+            p.desc[blockIdx.x].n = 0;
+            if (p.dev_status != nullptr) atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_CUDA));
+        }
+        return;
+    }
     uint8_t* sK = smem;                          // NK slots
     uint8_t* sV = sK + C::NK * C::SLOT;          // NV slots
     uint8_t* sP = sV + C::NV * C::SLOT;          // two buffers
@@ -229,10 +234,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     float* s_row = reinterpret_cast<float*>(bars + 50);   // [4][N]: maxima, then sums, of each warp
     float* s_negm = s_row + 4 * N;    // [N] minus the reference maxima, log2 units
     float* s_fac = s_negm + N;        // [N] factors: of a rescale, then 1 / l
+    int* s_lo = reinterpret_cast<int*>(s_fac + N);         // [N] first key that a row attends,
+    uint32_t* s_num = reinterpret_cast<uint32_t*>(s_lo + N);   // [N] and how many from there on
     long long* s_scan = reinterpret_cast<long long*>(s_row);   // set-up only
     static_assert(C::NK <= 6 && C::NV <= 6, "ring barriers");
     static_assert(2 * sizeof(Segment) <= 12 * 8, "segments fit their place");
-    static_assert(50 * 8 + 6 * N * 4 <= C::MISC, "row values fit their place");
+    static_assert(50 * 8 + 8 * N * 4 <= C::MISC, "row values fit their place");
     constexpr int kFirst = 1, kStop = 2;   // s_kind: O^T starts anew; no more blocks
 
     const int warp = threadIdx.x >> 5;
@@ -550,6 +557,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             s.none = s_seg[buf].none;
             mbar_arrive_warp(&q_empty[buf]);
             const int rows = s.ntok * G;
+            if (tid < N) {   // what row tid attends: a run of keys
+                const int pos = s.off + tid / G;
+                int lo = s.klo, hi = s.khi;
+                if (p.causal) hi = min(hi, pos + 1);
+                if (p.window > 0) {
+                    lo = max(lo, pos - p.window + 1);
+                    if (!p.causal) hi = min(hi, pos + p.window);
+                }
+                s_lo[tid] = lo;
+                s_num[tid] = static_cast<uint32_t>(max(0, hi - lo));
+            }
+            named_barrier_sync(1, kSoftmax);
             uint64_t l[N / 2];   // this thread's sums, two rows each
 #pragma unroll
             for (int n = 0; n < N / 2; ++n) l[n] = f2_pack(0.f, 0.f);
@@ -571,18 +590,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                                      (k0 < s.off + s.ntok - p.window ||
                                       (!p.causal && k0 + kTileRows - 1 > s.off + p.window - 1));
                 if (cut || diagonal || sliding) {
-                    int pos = s.off, g = 0;   // key position of row n
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        bool in = key >= s.klo && key < s.khi;
-                        if (p.causal) in = in && key <= pos;
-                        if (p.window > 0) in = in && pos - key < p.window && (p.causal || key - pos < p.window);
-                        if (!in) sr[n] = __float_as_uint(-INFINITY);
-                        if (++g == G) {
-                            g = 0;
-                            ++pos;
-                        }
-                    }
+                    for (int n = 0; n < N; ++n)
+                        if (static_cast<uint32_t>(key - s_lo[n]) >= s_num[n]) sr[n] = __float_as_uint(-INFINITY);
                 }
                 // Exponents s scale log2e - m, two rows at a time.  Rows past the
                 // tile's have m = inf: exponent -inf, weight 0.
