@@ -19,6 +19,9 @@
 //     run, whatever the request lengths are.  Tiles (request, head) cut by a run's
 //     end are joined by a second launch (paged_join_kernel), at most two
 //     pieces per CTA.
+//   * Where tiles are few and short, a cluster of up to eight CTAs takes a tile
+//     instead and joins its pieces through distributed shared memory: no
+//     workspace, no second launch.
 //   * The producers run ahead over the ends of tiles: rings of up to 176 KB
 //     of K and V tiles are in flight while the other warps finish a tile.
 //
@@ -55,6 +58,7 @@ struct DecodeCfg {
     static constexpr uint32_t O_COL = 2 * N;                 // S^T in [0, 2N), two buffers
     static constexpr uint32_t TMEM_COLS = 4 * N;
     static constexpr int THREADS = 256;
+    static_assert(N * D * 4 <= NK * SLOT, "a cluster's piece fits the K ring");
     static_assert(NV >= 2 && NV >= CHUNKS, "two slots a ring, and a tile");
 };
 
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) {
-            p.desc[blockIdx.x].n = 0;
+            if (p.cluster == 0) p.desc[blockIdx.x].n = 0;
             if (p.dev_status != nullptr) atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_CUDA));
         }
         return;
@@ -236,10 +240,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     float* s_fac = s_negm + N;        // [N] factors: of a rescale, then 1 / l
     int* s_lo = reinterpret_cast<int*>(s_fac + N);         // [N] first key that a row attends,
     uint32_t* s_num = reinterpret_cast<uint32_t*>(s_lo + N);   // [N] and how many from there on
+    float* s_lse = reinterpret_cast<float*>(s_num + N);        // [N] of a cluster's piece
     long long* s_scan = reinterpret_cast<long long*>(s_row);   // set-up only
     static_assert(C::NK <= 6 && C::NV <= 6, "ring barriers");
     static_assert(2 * sizeof(Segment) <= 12 * 8, "segments fit their place");
-    static_assert(50 * 8 + 8 * N * 4 <= C::MISC, "row values fit their place");
+    static_assert(50 * 8 + 9 * N * 4 <= C::MISC, "row values fit their place");
     constexpr int kFirst = 1, kStop = 2;   // s_kind: O^T starts anew; no more blocks
 
     const int warp = threadIdx.x >> 5;
@@ -291,37 +296,52 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
         return before + incl - x;
     };
-    long long all = 0, mine = 0, excl = 0;
-    for (int b0 = 0; b0 < p.B; b0 += C::THREADS) {
-        const int b = b0 + static_cast<int>(threadIdx.x);
-        mine = b < p.B ? static_cast<long long>(request_of(p, b).units) * p.Hkv : 0;
-        long long total;
-        excl = block_scan(mine, total);
-        all += total;
-    }
-    // No run is empty: the pieces of a tile are in consecutive CTAs.
-    const long long parts = min(all, static_cast<long long>(gridDim.x));
-    const long long u0 = cta < parts ? all * cta / parts : 0;
-    const long long u1 = cta < parts ? all * (cta + 1) / parts : 0;
-    // request that holds unit u0, and where it starts
-    long long* s_at = s_scan + 8;
-    if (p.B <= C::THREADS) {   // one round: the sums of above
-        if (excl <= u0 && u0 < excl + mine) {
-            s_at[0] = threadIdx.x;
-            s_at[1] = excl;
+    long long all = 0, parts = 1, u0 = 0, u1 = 0;
+    long long* s_at = s_scan + 8;   // request that holds unit u0, and where it starts
+    if (p.cluster > 0) {
+        // A cluster has one tile and shares its blocks out evenly.
+        const int rank = cta % p.cluster, tile = cta / p.cluster;
+        const int b = tile / p.Hkv, hk = tile - b * p.Hkv;
+        const int units = request_of(p, b).units;
+        const int share = (units + p.cluster - 1) / p.cluster;
+        const int first = min(units, rank * share);
+        u0 = static_cast<long long>(hk) * units + first;
+        u1 = static_cast<long long>(hk) * units + min(units, first + share);
+        if (threadIdx.x == 0) {
+            s_at[0] = b;
+            s_at[1] = 0;
         }
     } else {
-        long long done = 0;
-        for (int b0 = 0; b0 < p.B && done <= u0; b0 += C::THREADS) {
+        long long mine = 0, excl = 0;
+        for (int b0 = 0; b0 < p.B; b0 += C::THREADS) {
             const int b = b0 + static_cast<int>(threadIdx.x);
             mine = b < p.B ? static_cast<long long>(request_of(p, b).units) * p.Hkv : 0;
             long long total;
-            excl = done + block_scan(mine, total);
+            excl = block_scan(mine, total);
+            all += total;
+        }
+        // No run is empty: the pieces of a tile are in consecutive CTAs.
+        parts = min(all, static_cast<long long>(gridDim.x));
+        u0 = cta < parts ? all * cta / parts : 0;
+        u1 = cta < parts ? all * (cta + 1) / parts : 0;
+        if (p.B <= C::THREADS) {   // one round: the sums of above
             if (excl <= u0 && u0 < excl + mine) {
-                s_at[0] = b;
+                s_at[0] = threadIdx.x;
                 s_at[1] = excl;
             }
-            done += total;
+        } else {
+            long long done = 0;
+            for (int b0 = 0; b0 < p.B && done <= u0; b0 += C::THREADS) {
+                const int b = b0 + static_cast<int>(threadIdx.x);
+                mine = b < p.B ? static_cast<long long>(request_of(p, b).units) * p.Hkv : 0;
+                long long total;
+                excl = done + block_scan(mine, total);
+                if (excl <= u0 && u0 < excl + mine) {
+                    s_at[0] = b;
+                    s_at[1] = excl;
+                }
+                done += total;
+            }
         }
     }
     tc_fence_before();
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     if (warp == 4) {
         // ================= producer of segments, Q and K =================
         if (lane == 0) {
-            p.desc[cta].n = 0;
+            if (p.cluster == 0) p.desc[cta].n = 0;
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmK);
         }
@@ -400,9 +420,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 s.khi = r.khi;
                 s.j0 = r.j0 + blk;
                 s.nblk = nblk;
-                s.out = whole ? -1 : 2 * cta + (blk == 0 ? 1 : 0);
+                s.out = whole ? -1 : (p.cluster > 0 ? 0 : 2 * cta + (blk == 0 ? 1 : 0));
                 s.none = none;
-                if (!whole && blk == 0) {   // this CTA has the tile's first piece
+                if (p.cluster == 0 && !whole && blk == 0) {   // this CTA has the tile's first piece
                     const long long end = u + r.units;
                     const long long last = (end * parts + all - 1) / all - 1;   // CTA that ends it
                     p.desc[cta] = PieceDesc{r.start, 0, r.n, hk, static_cast<int>(last) - cta + 1,
@@ -533,6 +553,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         const int G = p.G;
         const float sc = p.scale_log2;
         const uint64_t sc2 = f2_pack(sc, sc);
+        // Pieces go to the workspace, or, in a cluster, to shared memory where
+        // the K ring was (this CTA's only segment is over by then).
+        float* const piece_o = p.cluster > 0 ? reinterpret_cast<float*>(sK) : p.part_o;
+        float* const piece_lse = p.cluster > 0 ? s_lse : p.part_lse;
+        const int piece_rows = p.cluster > 0 ? N : p.slot_rows;
         int blk = 0;    // blocks so far, over all segments
         bool ok = true;
         for (int seg = 0;; ++seg) {
@@ -713,7 +738,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 if (tid < rows) {
                     const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - s_negm[tid];
                     if (s.out >= 0) {
-                        p.part_lse[static_cast<size_t>(s.out) * p.slot_rows + tid] = lse2;
+                        piece_lse[static_cast<size_t>(s.out) * piece_rows + tid] = lse2;
                     } else {
                         const int tok = tid / G;
                         p.LSE[static_cast<size_t>(s.hk * G + tid - tok * G) * p.lq.total + s.q_start + tok] =
@@ -730,7 +755,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             // Row n of lane d: consecutive lanes, consecutive columns of a row.
             // A piece's rows are D floats apart, the output's H D after the last
             // head of a token.
-            const size_t out0 = s.out >= 0 ? static_cast<size_t>(s.out) * p.slot_rows * D
+            const size_t out0 = s.out >= 0 ? static_cast<size_t>(s.out) * piece_rows * D
                                            : (static_cast<size_t>(s.q_start) * p.lq.H + s.hk * G) * D;
             const size_t skip = s.out >= 0 ? 0 : static_cast<size_t>(p.lq.H - G) * D;
 #pragma unroll 1
@@ -755,7 +780,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                             if (16 * c + n < rows) {
                                 const float y = __uint_as_float(o[n]) * s_fac[16 * c + n];
                                 if (s.out >= 0)
-                                    p.part_o[at] = y;
+                                    piece_o[at] = y;
                                 else
                                     static_cast<uint16_t*>(p.O)[at] =
                                         static_cast<uint16_t>(pack_h2<kF16>(y, 0.f));
@@ -780,6 +805,55 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
     }
 
+    // ---- a cluster's pieces become its tile's result ----
+    if (p.cluster > 1) {
+        // pieces without a key, for CTAs that had no block
+        if (u0 >= u1 && threadIdx.x < N) s_lse[threadIdx.x] = -INFINITY;
+        cluster_sync();
+        const int rank = cta % p.cluster, tile = cta / p.cluster;
+        const int b = tile / p.Hkv, hk = tile - b * p.Hkv;
+        const Request r = request_of(p, b);
+        const bool whole = (r.units + p.cluster - 1) / p.cluster >= r.units;   // written by rank 0
+        for (int n = rank * (C::THREADS / 32) + warp; n < r.n * p.G && !whole;
+             n += p.cluster * (C::THREADS / 32)) {
+            float w = lane < p.cluster ? ld_cluster(&s_lse[n], lane) : -INFINITY;
+            float M = w;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            M = __shfl_sync(0xffffffffu, M, 0);
+            w = M == -INFINITY ? 0.f : ex2_approx(w - M);
+            float sum = w;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            constexpr int PER = D / 32;
+            float acc[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+            for (int i = 0; i < p.cluster; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                if (wi == 0.f) continue;   // no key, and nothing written
+                const float* src = reinterpret_cast<const float*>(sK) + n * D + lane * PER;
+#pragma unroll
+                for (int e = 0; e < PER; e += 2) {
+                    const float2 x = ld_cluster2(src + e, i);
+                    acc[e] += wi * x.x;
+                    acc[e + 1] += wi * x.y;
+                }
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int tok = n / p.G, head = hk * p.G + n - tok * p.G;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                static_cast<uint16_t*>(p.O) + ((static_cast<size_t>(r.start) + tok) * p.lq.H + head) * D + lane * PER);
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) dst[e] = pack_h2<kF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+            if (lane == 0)
+                p.LSE[static_cast<size_t>(head) * p.lq.total + r.start + tok] =
+                    sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+        }
+        cluster_sync();   // no CTA leaves while another reads its piece
+    }
+
     // ---- teardown ----
     tc_fence_before();
     __syncthreads();
@@ -798,7 +872,8 @@ cudaError_t launch_decode_t(const CUtensorMap& tq, const CUtensorMap& tk, const 
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kern, static_cast<unsigned>(p.tiles), C::THREADS, C::SMEM, stream, tq, tk, tv, p);
+    return launch_overlapped_cluster(kern, static_cast<unsigned>(p.tiles), C::THREADS, C::SMEM, p.cluster, stream,
+                                     tq, tk, tv, p);
 }
 
 template <int D, bool kF16>

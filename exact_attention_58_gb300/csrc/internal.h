@@ -88,21 +88,31 @@ cudaError_t enable_smem_per_device(Kernel kern, int bytes, std::atomic<unsigned 
 
 // Launch on `stream` with programmatic stream serialization, so that the
 // kernel's CTAs may start (and run up to their grid_dep_wait()) while the
-// kernel before it finishes.
+// kernel before it finishes; in clusters of `cluster` CTAs if that is > 1.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
-                              cudaStream_t stream, Args&&... args) {
+cudaError_t launch_overlapped_cluster(void (*kern)(KArgs...), unsigned grid, unsigned block,
+                                      size_t smem, int cluster, cudaStream_t stream,
+                                      Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                              cudaStream_t stream, Args&&... args) {
+    return launch_overlapped_cluster(kern, grid, block, smem, 1, stream, std::forward<Args>(args)...);
 }
 
 // Tensor map of `rank` dimensions (innermost first; strides in bytes, one

@@ -46,7 +46,7 @@ attn_status check_cache(int Hkv, int d, attn_dtype dtype, int num_pages, int pag
 struct Plan {
     bool decode;           // attn_decode_kernel: few query rows per request
     int tile_tokens;       // tokens of a query tile
-    int tiles, uniform, splits;
+    int tiles, uniform, splits, cluster;
     size_t slots, descs;   // pieces and joined tiles that the workspace holds
     int rows;              // rows of a slot
 };
@@ -59,7 +59,21 @@ Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_key
         t.decode = true;
         t.tile_tokens = max_q;
         t.rows = max_q * G <= 16 ? 16 : (max_q * G <= 32 ? 32 : 64);
-        t.tiles = static_cast<int>(std::min(static_cast<long long>(kSMs), blocks * Hkv * B));
+        const long long all = static_cast<long long>(B) * Hkv;
+        // Few short tiles: clusters (at most 128 CTAs, which leave room in every
+        // group of SMs) as long as a CTA's share is at most 4 blocks more than in
+        // equal runs, about what the second launch and the pieces' way through
+        // memory take.
+        for (int cs = 8; cs >= 1 && t.cluster == 0; cs /= 2)
+            if (all * cs <= 128 && (cs == 1 || cs / 2 < blocks) &&
+                (blocks + cs - 1) / cs <= 4 + blocks * all / kSMs)
+                t.cluster = cs;
+        if (t.cluster > 0) {
+            t.tiles = static_cast<int>(all) * t.cluster;
+            t.splits = 1;
+            return t;
+        }
+        t.tiles = static_cast<int>(std::min(static_cast<long long>(kSMs), blocks * all));
         t.splits = t.tiles > 1 && blocks > 1 ? 2 : 1;   // a tile can be cut
         t.descs = t.tiles;
         t.slots = 2 * t.descs;
@@ -285,6 +299,8 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     p.tiles = t.tiles;
     p.uniform_tiles = t.uniform;
     p.splits = t.splits;
+    p.cluster = t.cluster;
+    p.slot_rows = t.rows;
     CUtensorMap tq, tk, tv;
     if (!make_tmap_queries(&tq, Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
                            p.tile_tokens) ||

@@ -222,6 +222,32 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         : "memory");
 }
 
+// Barrier over all threads of the cluster (its CTAs' shared-memory writes are
+// visible to one another behind it).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A value at the place of this CTA's `p` in the shared memory of CTA `rank`.
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(const float* p, int rank) {
+    float2 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+        "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // Fire-and-forget adds into global memory (no value comes back, so the issuing
 // warp never waits on them).  red_add_v4 needs a 16-byte aligned address.
 __device__ __forceinline__ void red_add_v4(float* gptr, float a, float b, float c, float d) {

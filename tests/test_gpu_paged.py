@@ -18,6 +18,8 @@ def run(x, causal, window=0, **kw):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     args = [kw.pop(n, getattr(x, n)) for n in
             ("q", "k_cache", "v_cache", "page_table", "seq_lens", "cu")]
+    if kw.pop("wide", False):   # room for 64000 keys and more, unused
+        args[3] = torch.nn.functional.pad(args[3], (0, 8000), value=-1)
     args = [a if a.is_cuda else a.cuda() for a in args]
     o, lse = ea.attn_fwd_paged(*args, kw.pop("max_q", x.max_q), causal=causal, window=window,
                                dev_status=status, **kw)
@@ -44,9 +46,10 @@ LENS = [
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("heads", [(2, 2), (8, 2), (7, 1)], ids=str)
 @pytest.mark.parametrize("causal", [True, False])
-def test_lengths_and_heads(lens, d, heads, causal):
+@pytest.mark.parametrize("wide", [False, True], ids=["short table", "wide table"])
+def test_lengths_and_heads(lens, d, heads, causal, wide):
     x = make_paged(*lens, *heads, d, 16, seed=d + sum(lens[1]), poison=math.nan)
-    check_attention(*run(x, causal), x, causal)
+    check_attention(*run(x, causal, wide=wide), x, causal)
 
 
 @pytest.mark.parametrize("page", [8, 24, 48, 64, 128, 256, 384])
@@ -54,6 +57,7 @@ def test_lengths_and_heads(lens, d, heads, causal):
 def test_page_sizes(page, q_lens):
     x = make_paged(q_lens, [300, 129, 777], 4, 2, 128, page, seed=page, poison=math.inf)
     check_attention(*run(x, True), x, True)
+    check_attention(*run(x, True, wide=True), x, True)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -80,6 +84,7 @@ def test_window(window, causal, q_lens):
             x.k_cache[lost], x.v_cache[lost] = math.nan, math.nan
             x.page_table[b, :gone] = 2**31 - 1
     check_attention(*run(x, causal, window), x, causal, window)
+    check_attention(*run(x, causal, window, wide=True), x, causal, window)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -87,6 +92,7 @@ def test_window(window, causal, q_lens):
 def test_fp16(d, q_lens):
     x = make_paged(q_lens, [400, 1300], 6, 2, d, 32, dtype=FP16, seed=d, poison=math.nan)
     check_attention(*run(x, True), x, True)
+    check_attention(*run(x, True, wide=True), x, True)
 
 
 @pytest.mark.parametrize("heads", [(128, 1), (65, 1), (48, 1), (20, 4), (6, 2), (16, 1), (33, 1)],
@@ -95,6 +101,7 @@ def test_fp16(d, q_lens):
 def test_groups(heads, q_lens):
     x = make_paged(q_lens, [140, 300], *heads, 64, 16, seed=heads[0], poison=math.nan)
     check_attention(*run(x, True), x, True)
+    check_attention(*run(x, True, wide=True), x, True)
 
 
 def test_spiky_keys():
@@ -108,6 +115,7 @@ def test_spiky_keys():
             m = min(16, 1500 - 16 * c)
             x.k_cache[x.page_table[0, c], :, :m] = k[16 * c:16 * c + m].transpose(0, 1)
         check_attention(*run(x, True), x, True)
+        check_attention(*run(x, True, wide=True), x, True)
 
 
 def test_many_requests():
@@ -166,19 +174,21 @@ def test_scale_and_dirty_workspace():
     """An own scale, and a workspace whose contents on entry are NaN."""
     for q_lens in ([1, 1], [20, 100]):
         x = make_paged(q_lens, [3000, 200], 8, 2, 128, 16, seed=4, poison=math.nan)
-        n = ea.attn_fwd_paged_workspace_size(2, 8, 2, sum(q_lens), x.max_q, x.page_table.shape[1],
-                                             16, 128)
-        ws = torch.full((max(n, 16) // 4 + 1,), math.nan, device="cuda")
-        check_attention(*run(x, True, scale=0.3, workspace=ws), x, True, scale=0.3)
+        n = ea.attn_fwd_paged_workspace_size(2, 8, 2, sum(q_lens), x.max_q,
+                                             x.page_table.shape[1] + 8000, 16, 128)
+        assert n > 0
+        ws = torch.full((n // 4 + 1,), math.nan, device="cuda")
+        check_attention(*run(x, True, scale=0.3, workspace=ws, wide=True), x, True, scale=0.3)
 
 
 def test_same_result_every_time():
     x = make_paged([1] * 7 + [4], [4000, 33, 800, 1, 129, 2500, 64, 900], 8, 2, 128, 16, seed=8,
                    poison=math.nan)
-    a = run(x, True)
-    for _ in range(3):
-        b = run(x, True)
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for wide in (False, True):
+        a = run(x, True, wide=wide)
+        for _ in range(3):
+            b = run(x, True, wide=wide)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_cache_past_32_bit_offsets():
