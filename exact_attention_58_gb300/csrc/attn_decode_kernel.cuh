@@ -827,18 +827,26 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             sum = __shfl_sync(0xffffffffu, sum, 0);
             constexpr int PER = D / 32;
+            const float* src = reinterpret_cast<const float*>(sK) + n * D + lane * PER;
+            float2 x[8][PER / 2];   // all pieces' loads before the first is used
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < p.cluster) {
+#pragma unroll
+                    for (int e = 0; e < PER / 2; ++e) x[i][e] = ld_cluster2(src + 2 * e, i);
+                }
             float acc[PER];
 #pragma unroll
             for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-            for (int i = 0; i < p.cluster; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                if (wi == 0.f) continue;   // no key, and nothing written
-                const float* src = reinterpret_cast<const float*>(sK) + n * D + lane * PER;
 #pragma unroll
-                for (int e = 0; e < PER; e += 2) {
-                    const float2 x = ld_cluster2(src + e, i);
-                    acc[e] += wi * x.x;
-                    acc[e + 1] += wi * x.y;
+            for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                if (i < p.cluster && wi != 0.f) {   // else no key, or no piece at all
+#pragma unroll
+                    for (int e = 0; e < PER / 2; ++e) {
+                        acc[2 * e] += wi * x[i][e].x;
+                        acc[2 * e + 1] += wi * x[i][e].y;
+                    }
                 }
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -7,9 +7,11 @@
 //     floor(128 / G) tokens of G heads and K/V is read once for all of them.
 //   * A 128-key tile is gathered page by page: 128 / box_rows TMA boxes, one
 //     issued per lane, each at the (page, row) its page-table entry names.
-//   * A tile's key blocks can be shared by `splits` CTAs.  Each writes its
-//     normalised output and log-sum-exp as a piece, and a second launch joins
-//     them: O = sum_i w_i O_i / sum_i w_i with w_i = exp2(lse2_i - max lse2).
+//   * A tile's key blocks can be shared by `splits` CTAs.  Each leaves its
+//     normalised output and log-sum-exp as a piece, and they are joined:
+//     O = sum_i w_i O_i / sum_i w_i with w_i = exp2(lse2_i - max lse2).  Up to
+//     eight CTAs are a cluster and join through distributed shared memory; more
+//     leave their pieces in the workspace for a second launch.
 //
 // Keys outside the range that the CTA's queries attend between them may be
 // anything (slots past the last token, pages given back): their scores are
@@ -128,13 +130,76 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         if (jhi1 <= jlo1) jlo1 = jhi1 = 0;
     }
     const bool joined = pieces > 1;
-    const bool works = live && split < pieces;
     const int unit = tile * p.Hkv + hk;
-    if (threadIdx.x == 0 && split == 0 && p.splits > 1)
+    if (threadIdx.x == 0 && split == 0 && p.splits > 1 && p.cluster == 0)
         p.desc[unit] = PieceDesc{sq.start, tok0, ntok, hk, live && joined ? pieces : 0,
                                  unit * p.splits, unit * p.splits + 1, 1};
     if (blockIdx.x == 0) paged_report(p);
-    if (!works) return;
+    if (!live) return;
+
+    // A cluster's pieces, where the K/V ring and the queries were: rows of D
+    // floats in 16-byte groups, group c of row r at c ^ r (mod the groups of a
+    // row), so that neither the rows' writers (a row per thread) nor the readers (a
+    // group per lane) meet in a bank; and the rows' log-sum-exp.
+    float* const s_piece = reinterpret_cast<float*>(sKV);
+    float* const s_lse = reinterpret_cast<float*>(sQ);
+    constexpr int GROUPS = D / 4;
+    static_assert(C::TILES * kTileRows * D * 4 <= C::NSLOT * C::TILE, "a piece fits the ring");
+    auto piece_group = [&](int row, int c) { return s_piece + row * D + 4 * (c ^ (row & (GROUPS - 1))); };
+    // Joins them, a row per warp, rows dealt out over the cluster's warps.
+    auto join_cluster = [&]() {
+        cluster_sync();
+        constexpr int WARPS = C::THREADS / 32;
+        for (int u = split * WARPS + warp; u < ntok * G; u += p.splits * WARPS) {
+            const int ut = u / G, g = u - ut * G;
+            const int row = ut / TT * kTileRows + (ut % TT) * G + g;
+            float w = lane < p.splits ? ld_cluster(&s_lse[row], lane) : -INFINITY;
+            float M = w;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            M = __shfl_sync(0xffffffffu, M, 0);
+            w = M == -INFINITY ? 0.f : ex2_approx(w - M);
+            float sum = w;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int head = hk * G + g;
+            uint2* dst = reinterpret_cast<uint2*>(
+                static_cast<uint16_t*>(p.O) + ((static_cast<size_t>(sq.start) + tok0 + ut) * p.lq.H + head) * D);
+            for (int c = lane; c < GROUPS; c += 32) {
+                // all pieces' loads before the first is used
+                constexpr unsigned LANES = GROUPS < 32 ? (1u << (GROUPS & 31)) - 1u : 0xffffffffu;
+                float4 x[8], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < p.splits) x[i] = ld_cluster4(piece_group(row, c), i);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float wi = __shfl_sync(LANES, w, i);
+                    if (i < p.splits && wi != 0.f) {   // else no key, or no piece at all
+                        acc.x += wi * x[i].x;
+                        acc.y += wi * x[i].y;
+                        acc.z += wi * x[i].z;
+                        acc.w += wi * x[i].w;
+                    }
+                }
+                dst[c] = make_uint2(pack_h2<kF16>(acc.x * inv, acc.y * inv), pack_h2<kF16>(acc.z * inv, acc.w * inv));
+            }
+            __syncwarp();
+            if (lane == 0)
+                p.LSE[static_cast<size_t>(head) * p.lq.total + sq.start + tok0 + ut] =
+                    sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+        }
+        cluster_sync();   // no CTA leaves while another reads its piece
+    };
+    if (split >= pieces) {   // no blocks left for this CTA
+        if (p.cluster > 0 && joined) {
+            for (int r = threadIdx.x; r < C::TILES * kTileRows; r += C::THREADS) s_lse[r] = -INFINITY;
+            join_cluster();
+        }
+        return;
+    }
 
     auto jlo = [&](int t) { return t ? jlo1 : jlo0; };
     auto jhi = [&](int t) { return t ? jhi1 : jhi0; };
@@ -494,6 +559,8 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             ok = mbar_wait_warp(&bar_o[t], 0, s_abort);
             tc_fence_after();
         }
+        if (joined && p.cluster > 0)   // the ring and the queries are free once every product is done
+            ok = mbar_wait_warp(bar_fin, 0, s_abort) && ok;
         if (ok) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t piece_row =
@@ -511,7 +578,13 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                if (row_ok && joined) {
+                if (joined && p.cluster > 0) {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        *reinterpret_cast<float4*>(piece_group(t * kTileRows + r, 8 * c + v)) =
+                            make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                        __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+                } else if (row_ok && joined) {
                     float4* dst = reinterpret_cast<float4*>(p.part_o + piece_row * D + 32 * c);
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
@@ -531,14 +604,20 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                     }
                 }
             }
-            if (row_ok) {
-                const float lse2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
+            const float lse2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
+            if (joined && p.cluster > 0) {
+                s_lse[t * kTileRows + r] = lse2;
+            } else if (row_ok) {
                 if (joined) p.part_lse[piece_row] = lse2;
                 else p.LSE[static_cast<size_t>(head) * p.lq.total + sq.start + tok] = lse2 * kLn2;
             }
         }
     }
 
+    if (joined && p.cluster > 0) {
+        __syncwarp();
+        join_cluster();
+    }
     // ---- teardown ----
     tc_fence_before();
     __syncthreads();
@@ -557,7 +636,7 @@ cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(p.tiles) * static_cast<unsigned>(p.Hkv * p.splits);
-    return launch_overlapped(kern, grid, C::THREADS, C::SMEM, stream, tq, tk, tv, p);
+    return launch_overlapped_cluster(kern, grid, C::THREADS, C::SMEM, p.cluster, stream, tq, tk, tv, p);
 }
 
 }  // namespace

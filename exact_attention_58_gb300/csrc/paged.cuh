@@ -49,7 +49,7 @@ struct PagedParams {
     int tiles;                  // query tiles of the grid (per key/value head)
     int uniform_tiles;          // > 0: every request has this many tiles; 0: tiles follow the packed offsets
     int splits;                 // CTAs that share one tile's keys
-    int cluster;                // decode kernel: CTAs of a cluster that takes one tile; 0: runs
+    int cluster;                // > 0: CTAs of a cluster, which takes one tile and joins its pieces itself
 };
 
 // Keys of request b, clamped to what its page-table row can hold.

@@ -51,6 +51,10 @@ struct Plan {
     int rows;              // rows of a slot
 };
 
+// Clusters of 1 to 8 CTAs of one SM each that a GB300 runs at once (groups of
+// SMs are not all of one size).
+constexpr int kClusters[9] = {0, kSMs, 76, 46, 36, 28, 23, 15, 15};
+
 Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d) {
     Plan t{};
     const int G = H / Hkv;
@@ -60,12 +64,11 @@ Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_key
         t.tile_tokens = max_q;
         t.rows = max_q * G <= 16 ? 16 : (max_q * G <= 32 ? 32 : 64);
         const long long all = static_cast<long long>(B) * Hkv;
-        // Few short tiles: clusters (at most 128 CTAs, which leave room in every
-        // group of SMs) as long as a CTA's share is at most 4 blocks more than in
-        // equal runs, about what the second launch and the pieces' way through
-        // memory take.
+        // Few short tiles: the largest clusters that run at once, as long as a
+        // CTA's share is at most 4 blocks more than in equal runs, about what
+        // the second launch and the pieces' way through memory take.
         for (int cs = 8; cs >= 1 && t.cluster == 0; cs /= 2)
-            if (all * cs <= 128 && (cs == 1 || cs / 2 < blocks) &&
+            if (all <= kClusters[cs] && (cs == 1 || cs / 2 < blocks) &&
                 (blocks + cs - 1) / cs <= 4 + blocks * all / kSMs)
                 t.cluster = cs;
         if (t.cluster > 0) {
@@ -88,9 +91,17 @@ Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_key
     t.tiles = static_cast<int>(std::min(uniform ? per_request * B : packed, 0x7fffffffll));
     t.uniform = uniform ? static_cast<int>(per_request) : 0;
     // With fewer CTAs than SMs the keys of a tile are shared out, as far as
-    // all CTAs still run at once.
+    // all CTAs still run at once: over a cluster, or over more CTAs where that
+    // saves more blocks than joining in a second launch costs (4, about 8 us).
     const long long ctas = static_cast<long long>(t.tiles) * Hkv;
     t.splits = static_cast<int>(std::max(1ll, std::min(kSMs / ctas, blocks)));
+    int cs = 8;
+    while (cs > 1 && (ctas > kClusters[cs] || cs > blocks)) --cs;
+    if (t.splits > 1 && cs > 1 && (blocks + cs - 1) / cs <= (blocks + t.splits - 1) / t.splits + 4) {
+        t.splits = t.cluster = cs;
+        t.rows = per_cta * kTileRows;
+        return t;
+    }
     t.rows = per_cta * kTileRows;
     if (t.splits > 1) {
         t.descs = static_cast<size_t>(ctas);
@@ -313,7 +324,7 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = t.decode ? launch_paged_decode(tq, tk, tv, p, d, f16, s)
                              : launch_paged_tiles(tq, tk, tv, p, d, f16, s);
-    if (e == cudaSuccess && t.splits > 1) {
+    if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
         const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
         e = launch_paged_join(p, static_cast<int>(t.descs), rows, t.decode ? 4 : 1, d, f16, s);
     }

@@ -247,6 +247,16 @@ __device__ __forceinline__ float2 ld_cluster2(const float* p, int rank) {
         : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_cluster4(const float* p, int rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
 
 // Fire-and-forget adds into global memory (no value comes back, so the issuing
 // warp never waits on them).  red_add_v4 needs a 16-byte aligned address.

@@ -44,7 +44,7 @@ def paged(lib, **kw):
     (dict(cu=FAKE + 2), 3), (dict(seq=FAKE + 1), 3), (dict(table=FAKE + 2), 3),
     (dict(qt=1020), 3), (dict(qh=0), 3), (dict(sp=-8), 3), (dict(sh=12), 3), (dict(st=1 << 40), 3),
     (dict(ws=None, width=10000), 4), (dict(wsb=100, width=10000), 4),
-    (dict(ws=None, max_q=2, total=4, H=128), 4),
+    (dict(ws=None, max_q=2, total=4, H=128, width=10000), 4),
 ])
 def test_attention_refusals(lib, kw, expected):
     assert paged(lib, **kw) == expected
@@ -98,7 +98,7 @@ def test_workspace_sizes(lib):
     size = ea.attn_fwd_paged_workspace_size
     assert size(1, 8, 2, 1, 1, 10000, 16, 128) > 0        # one request: its keys are shared out
     assert size(1, 8, 2, 1, 1, 100, 16, 128) == 0         # among a cluster, if they are few
-    assert size(1, 8, 2, 200, 200, 100, 16, 128) > 0
+    assert size(1, 8, 2, 200, 200, 10000, 16, 128) > 0 == size(1, 8, 2, 200, 200, 100, 16, 128)
     assert size(4, 16, 16, 4 * 4096, 4096, 32, 128, 128) == 0   # enough tiles without
     for bad in (dict(B=0), dict(H=7), dict(d=96), dict(max_pages=0)):
         a = dict(B=1, H=8, Hkv=2, total_q=1, max_seqlen_q=1, max_pages=100, page_size=16, d=128)
