@@ -25,12 +25,12 @@
 //   * The producers run ahead over the ends of tiles: rings of up to 176 KB
 //     of K and V tiles are in flight while the other warps finish a tile.
 //
-// Warps 0-3: softmax, one key per thread.  Warp 4: walks the run, tells the
-// others each segment (a tile's part of the run), loads Q and K.  Warp 5: loads
-// V (a TMA instruction costs its warp about 65 cycles, and small pages take
-// many).  Warp 6: S^T products.  Warp 7: P V products; an issuing warp stalls on
-// every product and commit, and of these two neither waits for the other's
-// operands.
+// Warps: four (or, with more than 16 rows, eight, which halve the rows) for
+// softmax, one key per thread; one that walks the run, tells the others each
+// segment (a tile's part of the run) and loads Q and K; one that loads V (a TMA
+// instruction costs its warp about 65 cycles, and small pages take many); one
+// that issues S^T products and one for P V: an issuing warp stalls on every
+// product and commit, and of these two neither waits for the other's operands.
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
@@ -57,7 +57,11 @@ struct DecodeCfg {
     static constexpr int HALVES = D == 256 ? 2 : 1;          // 128-lane halves of O^T
     static constexpr uint32_t O_COL = 2 * N;                 // S^T in [0, 2N), two buffers
     static constexpr uint32_t TMEM_COLS = 4 * N;
-    static constexpr int THREADS = 256;
+    // Softmax warpgroups: with 32 or 64 rows two of them share the columns.
+    static constexpr int GROUPS = N > 16 ? 2 : 1;
+    static constexpr int NC = N / GROUPS;                    // columns of a thread
+    static constexpr int K_WARP = 4 * GROUPS, V_WARP = K_WARP + 1, S_WARP = K_WARP + 2, PV_WARP = K_WARP + 3;
+    static constexpr int THREADS = 32 * (4 * GROUPS + 4);
     static_assert(N * D * 4 <= NK * SLOT, "a cluster's piece fits the K ring");
     static_assert(NV >= 2 && NV >= CHUNKS, "two slots a ring, and a tile");
 };
@@ -102,8 +106,8 @@ __device__ __forceinline__ int float_key(float x) {
 }
 __device__ __forceinline__ float key_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// Sums of v[0..N) over the warp, scattered: after it, lane x holds in v[0]
-// (and v[1] for N = 64) the sum of column `col` (and col + 1).
+// Sums of v[0..N) over the warp, N = 16 or 32, scattered: after it, a lane holds
+// in v[0] the sum of the column returned (of N = 16, two lanes each).
 template <int N>
 __device__ __forceinline__ int warp_sum_scatter(float (&v)[N], int lane) {
     int col = 0;
@@ -130,22 +134,9 @@ __device__ __forceinline__ int warp_sum_scatter(float (&v)[N], int lane) {
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t t, uint32_t (&r)[N]) {
-    if constexpr (N == 16) {
-        tmem_ld16(t, r);
-    } else {
-#pragma unroll
-        for (int c = 0; c < N / 32; ++c) tmem_ld32(t + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
-    }
-}
-template <int N>
-__device__ __forceinline__ void tmem_st_cols(uint32_t t, const uint32_t (&r)[N]) {
-    if constexpr (N == 16) {
-        tmem_st16(t, r);
-    } else {
-#pragma unroll
-        for (int c = 0; c < N / 32; ++c)
-            tmem_st32(t + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(&r[32 * c]));
-    }
+    static_assert(N == 16 || N == 32, "columns of a thread");
+    if constexpr (N == 16) tmem_ld16(t, r);
+    else tmem_ld32(t, r);
 }
 
 // Walks a CTA's run [u, end), segment by segment, with the whole warp:
@@ -202,7 +193,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
     using C = DecodeCfg<D, N>;
-    constexpr int kSoftmax = 128;   // threads of warps 0-3
+    constexpr int NC = C::NC;
+    constexpr int kSoftmax = 128 * C::GROUPS;   // threads of the softmax warps
     constexpr uint32_t FMT = fmt16<kF16>();
     constexpr uint32_t IDESC_S = idesc_f32acc(128, N, FMT, false, false);
     constexpr uint32_t IDESC_O = idesc_f32acc(128, N, FMT, true, true);
@@ -272,7 +264,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         *s_abort = 0;
         fence_mbar_init();
     }
-    if (warp == 6) {
+    if (warp == C::S_WARP) {
         tmem_alloc(s_tmem, C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -297,7 +289,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         return before + incl - x;
     };
     long long all = 0, parts = 1, u0 = 0, u1 = 0;
-    long long* s_at = s_scan + 8;   // request that holds unit u0, and where it starts
+    long long* s_at = s_scan + 16;   // request that holds unit u0, and where it starts
     if (p.cluster > 0) {
         // A cluster has one tile and shares its blocks out evenly.
         const int rank = cta % p.cluster, tile = cta / p.cluster;
@@ -396,7 +388,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
     };
 
-    if (warp == 4) {
+    if (warp == C::K_WARP) {
         // ================= producer of segments, Q and K =================
         if (lane == 0) {
             if (p.cluster == 0) p.desc[cta].n = 0;
@@ -459,7 +451,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             drain(k_full, C::NK, fills);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == C::V_WARP) {
         // ================= producer of V =================
         if (lane == 0) tma_prefetch_desc(&tmV);
         int fills = 0;
@@ -468,7 +460,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         });
         if (lane == 0) drain(v_full, C::NV, fills);
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == C::S_WARP) {
         // ================= S^T = K Q^T =================
         if (lane == 0) {
             const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);
@@ -513,7 +505,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             mbar_wait(&bar_fin[0], 0, &no_abort);
         }
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == C::PV_WARP) {
         // ================= O^T (+)= V^T P^T =================
         if (lane == 0) {
             // V^T: 64 head-dim columns, the next 64 a column block on (for
@@ -546,10 +538,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
         __syncwarp();
     } else {
-        // ================= softmax (one thread per key) =================
-        const int tid = static_cast<int>(threadIdx.x);
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const uint32_t t_O = t_lane + C::O_COL;
+        // ================= softmax (one thread per key and group of columns) =================
+        // The groups share nothing but the barriers: rows are columns here.
+        const int tid = static_cast<int>(threadIdx.x) & 127;
+        const int quarter = warp & 3;
+        const int group = C::GROUPS == 1 ? 0 : warp >> 2;
+        const int c0 = group * NC;      // first row of this group
+        const int bar = 1 + group;      // the group's hardware barrier
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_S = t_lane + c0;
+        const uint32_t t_O = t_lane + C::O_COL + c0;
+        float* const g_row = s_row + c0;     // [4][N]
+        float* const g_negm = s_negm + c0;   // [NC], as the rest
+        float* const g_fac = s_fac + c0;
+        int* const g_lo = s_lo + c0;
+        uint32_t* const g_num = s_num + c0;
         const int G = p.G;
         const float sc = p.scale_log2;
         const uint64_t sc2 = f2_pack(sc, sc);
@@ -562,11 +565,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         bool ok = true;
         for (int seg = 0;; ++seg) {
             const int buf = seg & 1;
-            // The four warps meet at barriers inside a segment, so all of them
+            // A group's warps meet at barriers inside a segment, so all of them
             // take it or none does; a wait that fails inside leaves the results
             // unspecified and ends the walk at the next segment.
             ok = ok && mbar_wait_warp(&q_full[buf], (seg >> 1) & 1, s_abort);
-            if (named_barrier_or(1, kSoftmax, !ok)) break;
+            if (named_barrier_or(bar, 128, !ok)) break;
             Segment s;
             s.nblk = s_seg[buf].nblk;
             if (s.nblk == 0) break;
@@ -581,29 +584,29 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             s.out = s_seg[buf].out;
             s.none = s_seg[buf].none;
             mbar_arrive_warp(&q_empty[buf]);
-            const int rows = s.ntok * G;
-            if (tid < N) {   // what row tid attends: a run of keys
-                const int pos = s.off + tid / G;
+            const int rows = min(NC, s.ntok * G - c0);   // of this group; may be none
+            if (tid < NC) {   // what row c0 + tid attends: a run of keys
+                const int pos = s.off + (c0 + tid) / G;
                 int lo = s.klo, hi = s.khi;
                 if (p.causal) hi = min(hi, pos + 1);
                 if (p.window > 0) {
                     lo = max(lo, pos - p.window + 1);
                     if (!p.causal) hi = min(hi, pos + p.window);
                 }
-                s_lo[tid] = lo;
-                s_num[tid] = static_cast<uint32_t>(max(0, hi - lo));
+                g_lo[tid] = lo;
+                g_num[tid] = static_cast<uint32_t>(max(0, hi - lo));
             }
-            named_barrier_sync(1, kSoftmax);
-            uint64_t l[N / 2];   // this thread's sums, two rows each
+            named_barrier_sync(bar, 128);
+            uint64_t l[NC / 2];   // this thread's sums, two rows each
 #pragma unroll
-            for (int n = 0; n < N / 2; ++n) l[n] = f2_pack(0.f, 0.f);
+            for (int n = 0; n < NC / 2; ++n) l[n] = f2_pack(0.f, 0.f);
             for (int x = 0; x < (s.none ? 0 : s.nblk); ++x, ++blk) {
                 const int k0 = (s.j0 + x) * kTileRows;
                 const int key = k0 + tid;
                 ok = ok && mbar_wait_warp_soon(&s_full[blk & 1], (blk >> 1) & 1, s_abort);
                 tc_fence_after();
-                uint32_t sr[N];
-                tmem_ld_cols<N>(t_lane + (blk & 1) * N, sr);
+                uint32_t sr[NC];
+                tmem_ld_cols<NC>(t_S + (blk & 1) * N, sr);
                 tmem_ld_wait();
                 reg_fence(sr);
                 // Blocks where some row does not attend some key: the range's
@@ -616,8 +619,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                                       (!p.causal && k0 + kTileRows - 1 > s.off + p.window - 1));
                 if (cut || diagonal || sliding) {
 #pragma unroll
-                    for (int n = 0; n < N; ++n)
-                        if (static_cast<uint32_t>(key - s_lo[n]) >= s_num[n]) sr[n] = __float_as_uint(-INFINITY);
+                    for (int n = 0; n < NC; ++n)
+                        if (static_cast<uint32_t>(key - g_lo[n]) >= g_num[n]) sr[n] = __float_as_uint(-INFINITY);
                 }
                 // Exponents s scale log2e - m, two rows at a time.  Rows past the
                 // tile's have m = inf: exponent -inf, weight 0.
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = 8 * c + 2 * i;
-                        const uint64_t nm = reinterpret_cast<const uint64_t*>(s_negm)[n / 2];
+                        const uint64_t nm = reinterpret_cast<const uint64_t*>(g_negm)[n / 2];
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1])), sc2, nm),
                                   e[2 * i], e[2 * i + 1]);
                     }
@@ -634,47 +637,47 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 if (x > 0) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < N / 8; ++c) {
+                    for (int c = 0; c < NC / 8; ++c) {
                         float e[8];
                         exponents(c, e);
                         mx = max3f(max3f(e[0], e[1], e[2]), max3f(e[3], e[4], e[5]), max3f(e[6], e[7], mx));
                     }
                     grows = mx > kRescaleThreshold;
                 }
-                if (named_barrier_or(1, kSoftmax, grows)) {
+                if (named_barrier_or(bar, 128, grows)) {
                     // new reference maxima: over the warp's keys, then over the four warps
                     float mine_max = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
+                    for (int n = 0; n < NC; ++n) {
                         const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(__uint_as_float(sr[n]))));
-                        if ((n & 31) == lane) mine_max = wm;
-                        if ((n & 31) == 31 || n == N - 1)
-                            if (lane < N) s_row[warp * N + (n & ~31) + lane] = mine_max;
+                        if (n == lane) mine_max = wm;
                     }
-                    named_barrier_sync(1, kSoftmax);
-                    if (tid < N) {
-                        const float old = x > 0 ? -s_negm[tid] : kNoMax;
-                        const float mt = fmaxf(old, sc * fmaxf(fmaxf(s_row[tid], s_row[N + tid]),
-                                                               fmaxf(s_row[2 * N + tid], s_row[3 * N + tid])));
-                        s_negm[tid] = tid < rows ? -mt : -INFINITY;
-                        s_fac[tid] = tid < rows ? ex2_approx(old - mt) : 0.f;
+                    if (lane < NC) g_row[quarter * N + lane] = mine_max;
+                    named_barrier_sync(bar, 128);
+                    if (tid < NC) {
+                        const float old = x > 0 ? -g_negm[tid] : kNoMax;
+                        const float mt = fmaxf(old, sc * fmaxf(fmaxf(g_row[tid], g_row[N + tid]),
+                                                               fmaxf(g_row[2 * N + tid], g_row[3 * N + tid])));
+                        g_negm[tid] = tid < rows ? -mt : -INFINITY;
+                        g_fac[tid] = tid < rows ? ex2_approx(old - mt) : 0.f;
                     }
-                    named_barrier_sync(1, kSoftmax);
+                    named_barrier_sync(bar, 128);
                     if (x > 0) {   // sums and O^T columns, once P V of the block before is in
                         ok = ok && mbar_wait_warp(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
                         tc_fence_after();
 #pragma unroll
-                        for (int n = 0; n < N / 2; ++n) l[n] = f2_mul(l[n], reinterpret_cast<const uint64_t*>(s_fac)[n]);
+                        for (int n = 0; n < NC / 2; ++n) l[n] = f2_mul(l[n], reinterpret_cast<const uint64_t*>(g_fac)[n]);
 #pragma unroll 1
-                        for (int c = 0; c < C::HALVES * N / 16; ++c) {
+                        for (int c = 0; c < C::HALVES * NC / 16; ++c) {
+                            const uint32_t at = t_O + c / (NC / 16) * N + 16 * (c % (NC / 16));
                             uint32_t o[16];
-                            tmem_ld16(t_O + 16 * c, o);
+                            tmem_ld16(at, o);
                             tmem_ld_wait();
                             reg_fence(o);
 #pragma unroll
                             for (int n = 0; n < 16; ++n)
-                                o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[(16 * c + n) % N]);
-                            tmem_st16(t_O + 16 * c, o);
+                                o[n] = __float_as_uint(__uint_as_float(o[n]) * g_fac[(16 * c + n) % NC]);
+                            tmem_st16(at, o);
                         }
                         tmem_st_wait();
                     }
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 if (blk >= 2) ok = ok && mbar_wait_warp_soon(&pv_done[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
                 uint8_t* row = sP + (blk & 1) * C::P_BYTES + tid * 128;
 #pragma unroll
-                for (int c = 0; c < N / 8; ++c) {
+                for (int c = 0; c < NC / 8; ++c) {
                     float e[8];
                     exponents(c, e);
                     uint32_t w[4];
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                         l[4 * c + i] = f2_add(l[4 * c + i], f2_pack(p0, p1));
                         w[i] = pack_h2<kF16>(p0, p1);
                     }
-                    *reinterpret_cast<uint4*>(row + ((c ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(row + (((c0 / 8 + c) ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 if (cut) {
                     // V rows of keys outside [klo, khi) become zero.  Their slots'
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     // block before, else that of two blocks before (above).
                     if (C::CHUNKS == 2 && blk > 0)
                         ok = ok && mbar_wait_warp(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
-                    for (int c = 0; c < C::CHUNKS; ++c) {
+                    for (int c = 0; c < C::CHUNKS; ++c) {   // (each group clears all of them)
                         const int f = C::CHUNKS * blk + c;
                         ok = ok && mbar_wait_warp(&v_full[f % C::NV], (f / C::NV) & 1, s_abort);
                         if (ok && (key < s.klo || key >= s.khi)) {
@@ -717,31 +720,29 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                         }
                     }
                 }
-                if (tid == 0) s_kind[blk & 1] = x == 0 ? kFirst : 0;
+                if (threadIdx.x == 0) s_kind[blk & 1] = x == 0 ? kFirst : 0;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive_warp(&p_full[blk & 1]);
             }
             // ---- the segment's result: sums over all keys, O = acc / l ----
-            float ls[N];
+            float ls[NC];
 #pragma unroll
-            for (int n = 0; n < N / 2; ++n) f2_unpack(l[n], ls[2 * n], ls[2 * n + 1]);
-            const int col = warp_sum_scatter<N>(ls, lane);
-            if (N >= 32 || (lane & 1) == 0) {
-                s_row[warp * N + col] = ls[0];
-                if (N == 64) s_row[warp * N + col + 1] = ls[1];
-            }
-            named_barrier_sync(1, kSoftmax);
-            if (tid < N) {
-                const float sum = (s_row[tid] + s_row[N + tid]) + (s_row[2 * N + tid] + s_row[3 * N + tid]);
-                s_fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
+            for (int n = 0; n < NC / 2; ++n) f2_unpack(l[n], ls[2 * n], ls[2 * n + 1]);
+            const int col = warp_sum_scatter<NC>(ls, lane);
+            if (NC == 32 || (lane & 1) == 0) g_row[quarter * N + col] = ls[0];
+            named_barrier_sync(bar, 128);
+            if (tid < NC) {
+                const float sum = (g_row[tid] + g_row[N + tid]) + (g_row[2 * N + tid] + g_row[3 * N + tid]);
+                g_fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
                 if (tid < rows) {
-                    const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - s_negm[tid];
+                    const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - g_negm[tid];
+                    const int n = c0 + tid;
                     if (s.out >= 0) {
-                        piece_lse[static_cast<size_t>(s.out) * piece_rows + tid] = lse2;
+                        piece_lse[static_cast<size_t>(s.out) * piece_rows + n] = lse2;
                     } else {
-                        const int tok = tid / G;
-                        p.LSE[static_cast<size_t>(s.hk * G + tid - tok * G) * p.lq.total + s.q_start + tok] =
+                        const int tok = n / G;
+                        p.LSE[static_cast<size_t>(s.hk * G + n - tok * G) * p.lq.total + s.q_start + tok] =
                             lse2 * kLn2;
                     }
                 }
@@ -751,19 +752,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 ok = ok && mbar_wait_warp(&pv_done[last & 1], (last >> 1) & 1, s_abort);
                 tc_fence_after();
             }
-            named_barrier_sync(1, kSoftmax);
+            named_barrier_sync(bar, 128);
             // Row n of lane d: consecutive lanes, consecutive columns of a row.
             // A piece's rows are D floats apart, the output's H D after the last
             // head of a token.
-            const size_t out0 = s.out >= 0 ? static_cast<size_t>(s.out) * piece_rows * D
-                                           : (static_cast<size_t>(s.q_start) * p.lq.H + s.hk * G) * D;
+            const int tok0 = c0 / G, g0 = c0 - tok0 * G;   // of the group's first row
+            const size_t out0 = s.out >= 0 ? (static_cast<size_t>(s.out) * piece_rows + c0) * D
+                                           : ((static_cast<size_t>(s.q_start) + tok0) * p.lq.H + s.hk * G + g0) * D;
             const size_t skip = s.out >= 0 ? 0 : static_cast<size_t>(p.lq.H - G) * D;
 #pragma unroll 1
             for (int h = 0; h < C::HALVES; ++h) {
                 size_t at = out0 + h * 128 + tid;
-                int g = 0;
+                int g = g0;
 #pragma unroll 1
-                for (int c = 0; c < N / 16; ++c) {
+                for (int c = 0; c < NC / 16; ++c) {
                     if (16 * c >= rows) break;
                     uint32_t o[16];
                     if (!s.none) {
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
 #pragma unroll
                         for (int n = 0; n < 16; ++n) {
                             if (16 * c + n < rows) {
-                                const float y = __uint_as_float(o[n]) * s_fac[16 * c + n];
+                                const float y = __uint_as_float(o[n]) * g_fac[16 * c + n];
                                 if (s.out >= 0)
                                     piece_o[at] = y;
                                 else
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             tc_fence_before();
         }
         if (ok) {   // tell the P V warp
-            if (tid == 0) s_kind[blk & 1] = kStop;
+            if (threadIdx.x == 0) s_kind[blk & 1] = kStop;
             mbar_arrive_warp(&p_full[blk & 1]);
         }
     }
@@ -866,7 +868,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 6) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == C::S_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
     if (threadIdx.x == 0 && *s_abort && p.dev_status != nullptr)
         atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_DEVICE_TIMEOUT));
     if (blockIdx.x == 0) paged_report(p);
