@@ -575,6 +575,13 @@ def _empty(shape, dtype, device: torch.device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _output(name: str, t, dtype, n: int, ref: torch.Tensor, stream):
+    if t is None:
+        return _empty(n, dtype, ref.device, stream)
+    _int_tensor(name, t, dtype, (n,), ref)
+    return t
+
+
 def _int32(name: str, x) -> int:
     x = int(x)
     if not -2**31 <= x < 2**31:
@@ -608,16 +615,10 @@ def attn_page_table(cached_lens, new_lens, page_table, free_pages, num_free, pag
     _on_gpu(ref)
     dev = ref.device
 
-    def output(name, t, dtype, n):
-        if t is None:
-            return _empty(n, dtype, dev, stream)
-        _int_tensor(name, t, dtype, (n,), ref)
-        return t
-
-    cu_seqlens_q = output("cu_seqlens_q", cu_seqlens_q, i32, B + 1)
-    seq_lens = output("seq_lens", seq_lens, i32, B)
-    slots = output("slots", slots, torch.int64, max(max_tokens, 0))
-    pages_taken = output("pages_taken", pages_taken, i32, 1)
+    cu_seqlens_q = _output("cu_seqlens_q", cu_seqlens_q, i32, B + 1, ref, stream)
+    seq_lens = _output("seq_lens", seq_lens, i32, B, ref, stream)
+    pages_taken = _output("pages_taken", pages_taken, i32, 1, ref, stream)
+    slots = _output("slots", slots, torch.int64, max(max_tokens, 0), ref, stream)
     _call(library().attn_page_table, "attn_page_table", dev.index, stream, *inputs,
           cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(), pages_taken.data_ptr(),
           B, max_pages, page_size, max_tokens, free_pages.shape[0], _ptr(dev_status))

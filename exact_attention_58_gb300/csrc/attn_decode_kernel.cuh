@@ -198,10 +198,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     constexpr uint32_t FMT = fmt16<kF16>();
     constexpr uint32_t IDESC_S = idesc_f32acc(128, N, FMT, false, false);
     constexpr uint32_t IDESC_O = idesc_f32acc(128, N, FMT, true, true);
-    grid_dep_wait();
-    grid_dep_launch_dependents();   // the join: it waits for this grid itself
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled tiles need 1024-byte alignment
+        grid_dep_wait();
         if (threadIdx.x == 0) {
             if (p.cluster == 0) p.desc[blockIdx.x].n = 0;
             if (p.dev_status != nullptr) atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_CUDA));
@@ -268,6 +267,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         tmem_alloc(s_tmem, C::TMEM_COLS);
         tmem_relinquish();
     }
+    // Up to here nothing in global memory was touched: the kernel before may
+    // still have been running.
+    grid_dep_wait();
+    grid_dep_launch_dependents();   // the join: it waits for this grid itself
     // Block sum (total of x) and exclusive prefix of the calling thread.
     auto block_scan = [&](long long x, long long& total) {
         long long incl = x;

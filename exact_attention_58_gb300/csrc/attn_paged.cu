@@ -18,6 +18,7 @@ constexpr int kJoinWarps = 4;
 template <int D, bool kF16, int kPerRow>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedParams p) {
     grid_dep_wait();
+    grid_dep_launch_dependents();
     constexpr int PER = D / 32;   // floats of a lane
     __shared__ float s_acc[kPerRow > 1 ? kPerRow : 1][D];
     __shared__ float s_sum[kJoinWarps];

@@ -19,6 +19,7 @@ constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
     grid_dep_wait();
+    grid_dep_launch_dependents();   // the next kernel sets itself up meanwhile
     const unsigned vecs = static_cast<unsigned>(p.d) / 8;   // 16-byte pieces of a row
     const long long i = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
     const long long row = i / vecs;
@@ -80,6 +81,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
 
 __global__ void __launch_bounds__(kTableThreads) page_table_kernel(const TableParams p) {
     grid_dep_wait();
+    grid_dep_launch_dependents();   // the next kernel sets itself up meanwhile
     extern __shared__ int table_smem[];
     int* s_cu = table_smem;               // [B + 1] first token of each request
     int* s_take = table_smem + p.B + 1;   // [B] pages taken by the requests before
