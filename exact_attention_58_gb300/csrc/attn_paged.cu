@@ -119,8 +119,11 @@ cudaError_t launch_paged_tiles(const CUtensorMap& tq, const CUtensorMap& tk, con
     switch (d) {
         case 64: return f16 ? launch_paged_t<64, true, 2>(tq, tk, tv, p, stream)
                             : launch_paged_t<64, false, 2>(tq, tk, tv, p, stream);
-        case 128: return f16 ? launch_paged_t<128, true, 2>(tq, tk, tv, p, stream)
-                             : launch_paged_t<128, false, 2>(tq, tk, tv, p, stream);
+        case 128:
+            if (p.fine) return f16 ? launch_paged_t<128, true, 2, true>(tq, tk, tv, p, stream)
+                                   : launch_paged_t<128, false, 2, true>(tq, tk, tv, p, stream);
+            return f16 ? launch_paged_t<128, true, 2>(tq, tk, tv, p, stream)
+                       : launch_paged_t<128, false, 2>(tq, tk, tv, p, stream);
         case 256: return launch_paged_tiles_d256(tq, tk, tv, p, f16, stream);
     }
     return cudaErrorInvalidValue;

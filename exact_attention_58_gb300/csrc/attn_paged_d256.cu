@@ -7,6 +7,8 @@ namespace gbattn {
 cudaError_t launch_paged_tiles_d256(const CUtensorMap& tq, const CUtensorMap& tk,
                                     const CUtensorMap& tv, const PagedParams& p, bool f16,
                                     cudaStream_t stream) {
+    if (p.fine) return f16 ? launch_paged_t<256, true, 1, true>(tq, tk, tv, p, stream)
+                           : launch_paged_t<256, false, 1, true>(tq, tk, tv, p, stream);
     return f16 ? launch_paged_t<256, true, 1>(tq, tk, tv, p, stream)
                : launch_paged_t<256, false, 1>(tq, tk, tv, p, stream);
 }

@@ -5,8 +5,12 @@
 //   * Rows of a query tile are (token, head) pairs: the G query heads that
 //     read one key/value head share each K/V tile, so a 128-row tile holds
 //     floor(128 / G) tokens of G heads and K/V is read once for all of them.
-//   * A 128-key tile is gathered page by page: 128 / box_rows TMA boxes, one
-//     issued per lane, each at the (page, row) its page-table entry names.
+//   * A 128-key tile is gathered page by page: 128 / box_rows TMA boxes of 64
+//     head-dim columns, issued by a lane each, at the (page, row) its page-table
+//     entry names.  A TMA instruction costs its warp about 65 cycles, so where
+//     pages are small and rows long (kFine) a box is 8 keys of all of d: the
+//     tile's 8-row groups then lie one after the other, each with its column
+//     blocks of 1 KB, instead of column blocks of 16 KB.
 //   * A tile's key blocks can be shared by `splits` CTAs.  Each leaves its
 //     normalised output and log-sum-exp as a piece, and they are joined:
 //     O = sum_i w_i O_i / sum_i w_i with w_i = exp2(lse2_i - max lse2).  Up to
@@ -52,7 +56,7 @@ __device__ __forceinline__ void find_packed_tile(const SeqLayout& lq, int B, int
     local = x - packed_tile_base(lq, b, tokens);
 }
 
-template <int D, bool kF16, int kTiles>
+template <int D, bool kF16, int kTiles, bool kFine>
 __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
@@ -278,7 +282,10 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                     }
                     if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
                     __syncwarp();
-                    if (box.needed) {
+                    if (kFine && box.needed) {
+                        tma_load_5d(sKV + slot * C::TILE + lane * 8 * C::ROWB, which ? &tmV : &tmK, &full[slot], 0,
+                                    box.row, 0, hk, page_box_checked(p, box));
+                    } else if (box.needed) {
                         const int page = page_box_checked(p, box);
                         uint8_t* dst = sKV + slot * C::TILE + lane * p.box_rows * 128;
                         const CUtensorMap* m = which ? &tmV : &tmK;
@@ -307,25 +314,27 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         if (lane == 0 && nkv > 0) {
             const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t dq1 = sdesc_adv(dq0, C::TILE);
-            const uint64_t dk0 = sdesc_sw128(smem_u32(sKV), 16, 1024);   // K-major, slot 0
-            const uint64_t dv0 = sdesc_sw128(smem_u32(sKV), C::CB_BYTES, 1024);
+            // K-major K and MN-major V of slot 0: 8-row groups 1 KB apart and column
+            // blocks 16 KB, or (kFine) groups a row group's bytes apart, blocks 1 KB
+            const uint64_t dk0 = sdesc_sw128(smem_u32(sKV), 16, kFine ? 8 * C::ROWB : 1024);
+            const uint64_t dv0 = sdesc_sw128(smem_u32(sKV), kFine ? 1024 : C::CB_BYTES, kFine ? 8 * C::ROWB : 1024);
             auto issue_qk = [&](int t, int slot) {
                 const uint32_t d_tmem = tmem + 128u * t;
                 const uint64_t ad = t ? dq1 : dq0;
                 const uint64_t bd = sdesc_adv(dk0, slot * C::TILE);
-                constexpr uint32_t CB = C::CB_BYTES / 16 - 6;
+                constexpr uint32_t CB = C::CB_BYTES / 16 - 6, CK = kFine ? 1024 / 16 - 6 : CB;
                 if constexpr (C::QK_STEPS == 4) {
                     mma4_ss_f16<2, 2, 2, 2, 2, 2>(d_tmem, ad, bd, C::IDESC_QK, 0u);
                 } else {
-                    mma8_ss_f16<2, 2, 2, CB, 2, 2, 2, 2, 2, 2, CB, 2, 2, 2>(d_tmem, ad, bd, C::IDESC_QK, 0u);
+                    mma8_ss_f16<2, 2, 2, CB, 2, 2, 2, 2, 2, 2, CK, 2, 2, 2>(d_tmem, ad, bd, C::IDESC_QK, 0u);
                     if constexpr (C::QK_STEPS == 16)
-                        mma8_ss_f16<2, 2, 2, CB, 2, 2, 2, 2, 2, 2, CB, 2, 2, 2>(
-                            d_tmem, sdesc_adv(ad, 2 * C::CB_BYTES), sdesc_adv(bd, 2 * C::CB_BYTES),
-                            C::IDESC_QK, 1u);
+                        mma8_ss_f16<2, 2, 2, CB, 2, 2, 2, 2, 2, 2, CK, 2, 2, 2>(
+                            d_tmem, sdesc_adv(ad, 2 * C::CB_BYTES),
+                            sdesc_adv(bd, 2 * (kFine ? 1024 : C::CB_BYTES)), C::IDESC_QK, 1u);
                 }
             };
             auto issue_pv = [&](int t, int slot, bool accumulate) {
-                mma_run_ts_f16<8, 8, C::KSTEP * 128 / 16>(tmem + C::O_COL + D * t, tmem + 128u * t,
+                mma_run_ts_f16<8, 8, (kFine ? 2 * 8 * C::ROWB : C::KSTEP * 128) / 16>(tmem + C::O_COL + D * t, tmem + 128u * t,
                                                           sdesc_adv(dv0, slot * C::TILE), C::IDESC_PV,
                                                           accumulate ? 1u : 0u);
             };
@@ -450,7 +459,9 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                 }
                 if (k0 + r < klo || k0 + r >= khi) {
                     for (int cb = 0; cb < C::NCB; ++cb) {
-                        uint4* row = reinterpret_cast<uint4*>(sKV + slot * C::TILE + cb * C::CB_BYTES + r * 128);
+                        const int at = kFine ? (r >> 3) * 8 * C::ROWB + cb * 1024 + (r & 7) * 128
+                                              : cb * C::CB_BYTES + r * 128;
+                        uint4* row = reinterpret_cast<uint4*>(sKV + slot * C::TILE + at);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) row[e] = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -627,11 +638,11 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_DEVICE_TIMEOUT));
 }
 
-template <int D, bool kF16, int kTiles>
+template <int D, bool kF16, int kTiles, bool kFine = false>
 cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PagedParams& p, cudaStream_t stream) {
     using C = FwdCfg<D, false, kF16, false, kTiles>;
-    auto kern = attn_paged_kernel<D, kF16, kTiles>;
+    auto kern = attn_paged_kernel<D, kF16, kTiles, kFine>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;

@@ -38,6 +38,7 @@ struct PagedParams {
     int num_pages, page_size, max_pages;
     unsigned long long page_magic;   // floor(2^62 / page_size) + 1
     int box_rows;               // keys of one TMA box: the power of two dividing page_size, <= 128
+    int fine;                   // tile kernel: boxes of 8 keys and all of d (box_rows = 8)
     int tile_tokens;            // tokens of one 128-row query tile (rows are (token, head of the group))
     int causal, window;
     float scale_log2;           // scale * log2(e)

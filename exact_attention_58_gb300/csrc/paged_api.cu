@@ -128,17 +128,26 @@ attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int
     return ATTN_OK;
 }
 
-// Tensor map over a cache [num_pages][Hkv][page_size][d] with any strides.
+// Tensor map over a cache [num_pages][Hkv][page_size][d] with any strides:
+// boxes of box_rows tokens and 64 columns, or (fine) of 8 tokens and all of d.
 bool make_tmap_cache(CUtensorMap* map, const void* ptr, attn_dtype dtype, int num_pages, int Hkv,
                      int page_size, int d, long long page_stride, long long head_stride,
-                     long long token_stride, int box_rows) {
+                     long long token_stride, int box_rows, bool fine) {
     auto bytes = [&](long long stride, long long extent) {
         return static_cast<cuuint64_t>(extent == 1 ? d : stride) * 2;
     };
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
-                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(num_pages)};
-    const cuuint64_t strides[3] = {bytes(token_stride, page_size), bytes(head_stride, Hkv),
-                                   bytes(page_stride, num_pages)};
+    const cuuint64_t ts = bytes(token_stride, page_size), hs = bytes(head_stride, Hkv),
+                     ps = bytes(page_stride, num_pages);
+    const cuuint64_t pages = static_cast<cuuint64_t>(num_pages), heads = static_cast<cuuint64_t>(Hkv),
+                     rows = static_cast<cuuint64_t>(page_size);
+    if (fine) {
+        const cuuint64_t dims[5] = {64, rows, static_cast<cuuint64_t>(d) / 64, heads, pages};
+        const cuuint64_t strides[4] = {ts, 128, hs, ps};
+        const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d) / 64, 1, 1};
+        return encode_tmap(map, ptr, dtype, 5, dims, strides, box);
+    }
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), rows, heads, pages};
+    const cuuint64_t strides[3] = {ts, hs, ps};
     const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
     return encode_tmap(map, ptr, dtype, 4, dims, strides, box);
 }
@@ -302,6 +311,10 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     p.max_pages = max_pages;
     p.page_magic = (1ull << 62) / static_cast<unsigned long long>(page_size) + 1;
     p.box_rows = std::min(kTileRows, page_size & -page_size);
+    // More than 16 boxes of 64 columns a tile: 16 of 8 keys and all columns
+    // instead (the decode kernel issues K and V from two warps and has the time).
+    p.fine = !t.decode && kTileRows / p.box_rows * (d / 64) > 16;
+    if (p.fine) p.box_rows = 8;
     p.tile_tokens = t.tile_tokens;
     p.causal = causal != 0;
     // a window of 2^30 keys is none: no two positions are that far apart
@@ -316,9 +329,9 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     if (!make_tmap_queries(&tq, Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
                            p.tile_tokens) ||
         !make_tmap_cache(&tk, k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
-                         cache_head_stride, cache_token_stride, p.box_rows) ||
+                         cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
         !make_tmap_cache(&tv, v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
-                         cache_head_stride, cache_token_stride, p.box_rows))
+                         cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
         return ATTN_ERR_CUDA;
     const bool f16 = dtype == ATTN_DTYPE_FP16;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -52,10 +52,11 @@ def test_lengths_and_heads(lens, d, heads, causal, wide):
     check_attention(*run(x, causal, wide=wide), x, causal)
 
 
-@pytest.mark.parametrize("page", [8, 24, 48, 64, 128, 256, 384])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16, 24, 48, 64, 128, 256, 384])
 @pytest.mark.parametrize("q_lens", [[1, 1, 1], [40, 1, 200]], ids=str)
-def test_page_sizes(page, q_lens):
-    x = make_paged(q_lens, [300, 129, 777], 4, 2, 128, page, seed=page, poison=math.inf)
+def test_page_sizes(d, page, q_lens):
+    x = make_paged(q_lens, [300, 129, 777], 4, 2, d, page, seed=page, poison=math.inf)
     check_attention(*run(x, True), x, True)
     check_attention(*run(x, True, wide=True), x, True)
 
