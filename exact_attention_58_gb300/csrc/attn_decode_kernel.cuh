@@ -361,13 +361,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
         __syncwarp();
     };
+    // The boxes of a segment's first tile: asked for before anything else.
+    auto first_box = [&](int b, const Request& r, int blk) {
+        return page_box(p, p.page_table + static_cast<size_t>(b) * p.max_pages, (r.j0 + blk) * kTileRows, r.klo,
+                        r.khi, lane);
+    };
     // The K (or V) tiles of one segment through their ring.
     auto load_tiles = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty,
-                          int slots, int& fills, int b, const Request& r, int hk, int blk, int nblk) {
+                          int slots, int& fills, PageBox box, int b, const Request& r, int hk, int blk,
+                          int nblk) {
         if (r.khi <= r.klo) return true;
         const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
         const int jbeg = r.j0 + blk;
-        PageBox box = page_box(p, table, jbeg * kTileRows, r.klo, r.khi, lane);
         for (int j = jbeg; j < jbeg + nblk; ++j) {
             const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
                                    static_cast<uint32_t>(p.box_rows) * (2 * C::CW);
@@ -402,6 +407,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         bool ok = walk_run(p, at_b, at_u, u0, u1, lane, [&](int b, const Request& r, int hk, int blk, int nblk,
                                                             long long u) {
             const int buf = seg & 1;
+            const PageBox box = first_box(b, r, blk);
             if (seg >= 2 && !mbar_wait_warp_soon(&q_empty[buf], ((seg >> 1) & 1) ^ 1, s_abort)) return false;
             if (lane == 0) {
                 const bool whole = nblk == r.units, none = r.khi <= r.klo;
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             }
             __syncwarp();
             ++seg;
-            return load_tiles(&tmK, sK, k_full, k_empty, C::NK, fills, b, r, hk, blk, nblk);
+            return load_tiles(&tmK, sK, k_full, k_empty, C::NK, fills, box, b, r, hk, blk, nblk);
         });
         // no more segments
         bool told = false;
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         if (lane == 0) tma_prefetch_desc(&tmV);
         int fills = 0;
         walk_run(p, at_b, at_u, u0, u1, lane, [&](int b, const Request& r, int hk, int blk, int nblk, long long) {
-            return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, b, r, hk, blk, nblk);
+            return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk);
         });
         if (lane == 0) drain(v_full, C::NV, fills);
         __syncwarp();

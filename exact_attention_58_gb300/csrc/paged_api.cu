@@ -64,12 +64,14 @@ Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_key
         t.tile_tokens = max_q;
         t.rows = max_q * G <= 16 ? 16 : (max_q * G <= 32 ? 32 : 64);
         const long long all = static_cast<long long>(B) * Hkv;
-        // Few short tiles: the largest clusters that run at once, as long as a
-        // CTA's share is at most 4 blocks more than in equal runs, about what
-        // the second launch and the pieces' way through memory take.
+        // Few short tiles: the largest clusters that run at once.  A cluster
+        // takes as long as its own tile, runs of all tiles as long as the mean
+        // one; with lengths spread evenly up to what the page table holds that is
+        // half the longest, and the second launch and the pieces' way through
+        // memory take about 4 blocks more.
         for (int cs = 8; cs >= 1 && t.cluster == 0; cs /= 2)
             if (all <= kClusters[cs] && (cs == 1 || cs / 2 < blocks) &&
-                (blocks + cs - 1) / cs <= 4 + blocks * all / kSMs)
+                (blocks + cs - 1) / cs <= 4 + blocks * all / (2 * kSMs))
                 t.cluster = cs;
         if (t.cluster > 0) {
             t.tiles = static_cast<int>(all) * t.cluster;
@@ -339,7 +341,9 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
                              : launch_paged_tiles(tq, tk, tv, p, d, f16, s);
     if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
         const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
-        e = launch_paged_join(p, static_cast<int>(t.descs), rows, t.decode ? 4 : 1, d, f16, s);
+        // pieces of a tile in the mean: CTAs by tiles
+        const bool many = t.decode && static_cast<long long>(B) * H_kv <= 16;
+        e = launch_paged_join(p, static_cast<int>(t.descs), rows, many, d, f16, s);
     }
     return from_cuda(e);
 }
