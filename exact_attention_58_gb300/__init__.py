@@ -28,6 +28,8 @@ Serving from a paged key/value cache (bf16 or fp16, grouped query heads):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
@@ -498,9 +500,33 @@ def attn_bwd_varlen(q, k, v, o, do, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_
 # paged key/value cache
 # ---------------------------------------------------------------------------
 # The calls of a decoding step take a few microseconds on the GPU, so the host
-# side is kept short: one pass over each tensor's attributes, plain integers for
-# pointers and streams (a current_stream() object alone costs 3 us), no
-# allocation beyond the outputs.
+# side is kept short.  The ordinary call (all arguments as documented, the
+# current stream and device) is checked and marshalled by csrc/binding.cpp; what
+# that does not take, refusals included, goes on here, with one pass over each
+# tensor's attributes and plain integers for pointers and streams (a
+# current_stream() object alone costs 3 us).
+_native_module = None
+
+
+def _native():
+    """The extension lib/_binding.so.  Raises if it has not been built."""
+    global _native_module
+    if _native_module is None:
+        lib = library()
+        if not os.path.exists(_build.BINDING_PATH):
+            raise RuntimeError(f"{_build.BINDING_PATH} is missing: build it with "
+                               "exact_attention_58_gb300._build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_binding", _build.BINDING_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in
+                      ("attn_page_table", "attn_cache_append", "attn_fwd_paged",
+                       "attn_fwd_paged_workspace_size")))
+        _native_module = module
+    return _native_module
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -598,6 +624,12 @@ def attn_page_table(cached_lens, new_lens, page_table, free_pages, num_free, pag
     free_pages[:num_free], and returns (cu_seqlens_q [B + 1], seq_lens [B],
     slots [max_tokens] int64, -1 behind the last token, pages_taken [1]).  All
     int32 CUDA tensors but slots; see include/gbattn.h."""
+    if stream is None:
+        done = (_native_module or _native()).page_table(
+            cached_lens, new_lens, page_table, free_pages, num_free, page_size, max_tokens,
+            cu_seqlens_q, seq_lens, slots, pages_taken, dev_status)
+        if done is not None:
+            return done
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
@@ -629,6 +661,9 @@ def attn_cache_append(k, v, k_cache, v_cache, slots, *, dev_status=None, stream=
     """Writes k, v ([T, Hkv, d], d innermost, the same strides) into slots
     slots[t] (int64 [T]; -1 skips a token) of the caches ([num_pages, Hkv,
     page_size, d] views of like strides); see include/gbattn.h."""
+    if stream is None and (_native_module or _native()).cache_append(k, v, k_cache, v_cache, slots,
+                                                                     dev_status):
+        return
     shape, strides = _rows("k", k)
     v_shape, v_strides = _rows("v", v)
     T, Hkv, d = shape
@@ -662,6 +697,12 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_
     positions; keys and values in the pages that page_table [B, max_pages]
     names.  Query head h reads key head h // (H // Hkv).  Returns O [total_q,
     H, d] and LSE [H, total_q]; see include/gbattn.h."""
+    if stream is None:
+        done = (_native_module or _native()).fwd_paged(q, k_cache, v_cache, page_table, seq_lens,
+                                                       cu_seqlens_q, max_seqlen_q, causal, window,
+                                                       scale, out, lse, workspace, dev_status)
+        if done is not None:
+            return done
     (total_q, H, d), strides = _rows("q", q)
     pages, Hkv, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, q)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:

@@ -1,8 +1,11 @@
-"""Build libgbattn.so in-tree with nvcc for sm_103a.
+"""Build libgbattn.so in-tree with nvcc for sm_103a, and the Python extension
+that calls it.
 
 Each translation unit under csrc/ is compiled in parallel to an object in
 ``_build/`` and linked (static CUDA runtime) into ``lib/libgbattn.so``.  A
 unit is recompiled only when it or a header is newer than its object.
+``csrc/binding.cpp`` (host code against PyTorch's headers) becomes
+``lib/_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +26,9 @@ BUILD = os.path.join(PKG, "_build", MACHINE)   # objects differ per host archite
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgbattn.so")
 STAMP = LIB_PATH + ".machine"
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_binding.so")
+BINDING_STAMP = BINDING_PATH + ".machine"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -57,13 +64,44 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """lib/_binding.so for this machine, Python and PyTorch."""
+    import torch
+    made_for = " ".join((MACHINE, platform.python_version(), torch.__version__))
+    header = os.path.join(INCLUDE, "gbattn.h")
+    if (os.path.exists(BINDING_PATH) and os.path.exists(BINDING_STAMP)
+            and open(BINDING_STAMP).read().strip() == made_for
+            and os.path.getmtime(BINDING_PATH) >= max(os.path.getmtime(BINDING_SRC),
+                                                      os.path.getmtime(header))):
+        return
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SRC,
+           "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(made_for)
+
+
 def build(verbose_ptxas: bool = False) -> str:
-    """Compile every .cu under csrc/ and link lib/libgbattn.so; returns its path."""
+    """Compile every .cu under csrc/, link lib/libgbattn.so and build the
+    extension; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding.result()
     newest = max(os.path.getmtime(o) for o in objs)
     stamp_ok = os.path.exists(STAMP) and open(STAMP).read().strip() == MACHINE
     if not (stamp_ok and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest):

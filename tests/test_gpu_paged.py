@@ -314,6 +314,40 @@ def test_other_stream_and_graph_with_new_lengths():
         check_attention(out, lse, b, True)
 
 
+def test_both_ways_into_the_library_agree():
+    """The short way through the extension (no stream argument) and the long one
+    through ctypes: same results, outputs given or not; and the same refusals."""
+    x = make_paged([3, 40, 0, 1], [200, 90, 5, 700], 8, 2, 64, 16, seed=40, poison=math.nan)
+    here = torch.cuda.current_stream()
+    a = run(x, True, window=100)
+    out, lse = torch.empty_like(a[0]), torch.empty_like(a[1])
+    for kw in (dict(stream=here), dict(stream=here.cuda_stream or 0), dict(out=out, lse=lse),
+               dict(workspace=torch.empty(100 << 20, dtype=torch.uint8, device="cuda"), scale=0.125)):
+        b = run(x, True, window=100, **kw)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert run(x, True, out=out, lse=lse)[0] is out
+    dev = [t.cuda() for t in (x.q, x.k_cache, x.v_cache, x.page_table, x.seq_lens, x.cu)]
+    for stream in (None, here):
+        for i, bad in ((0, dev[0].float()), (1, dev[1][:, :1]), (3, dev[3].long()), (4, dev[4][:1]),
+                       (5, x.cu), (0, dev[0][:, :, ::2])):
+            with pytest.raises(ValueError):
+                ea.attn_fwd_paged(*dev[:i], bad, *dev[i + 1:], 40, stream=stream)
+        for kw, status in ((dict(scale=-1.0), 1), (dict(workspace=torch.empty(4, device="cuda")), 4)):
+            wide = torch.nn.functional.pad(dev[3], (0, 8000), value=-1)
+            with pytest.raises(ea.AttnError) as e:
+                ea.attn_fwd_paged(*dev[:3], wide, *dev[4:], 40, stream=stream, **kw)
+            assert e.value.status == status
+        with pytest.raises(ValueError):
+            ea.attn_fwd_paged(*dev, 40, out=out.float(), stream=stream)
+        with pytest.raises(ValueError):
+            ea.attn_cache_append(dev[0][:, :2], dev[0][:, :2], dev[1], dev[2],
+                                 torch.zeros(3, dtype=torch.int64, device="cuda"), stream=stream)
+        with pytest.raises(ea.AttnError) as e:   # an output inside an input
+            ea.attn_page_table(dev[4], dev[4], dev[3], dev[5], dev[4][:1], 16, 8, seq_lens=dev[4],
+                               stream=stream)
+        assert e.value.status == 1
+
+
 # ---------------------------------------------------------------------------
 # cache append
 # ---------------------------------------------------------------------------
