@@ -139,19 +139,30 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t t, uint32_t (&r)[N]) {
     else tmem_ld32(t, r);
 }
 
-// Walks a CTA's run [u, end), segment by segment, with the whole warp:
-// body(request index, request, head, first block, blocks, first unit) returns
-// false to stop.  Returns whether the walk came to its end.
+// A CTA's run [u0, u1) of the units of request 0, 1, ... one after the other.
+struct Run {
+    long long all, parts;   // units in all; CTAs that have some
+    long long u0, u1;
+    int b;                  // request that holds u0
+    long long b_unit;       // its first unit
+};
+
+// Walks a CTA's run, segment by segment, with the whole warp: body(request
+// index, request, head, first block, blocks, first unit) returns false to stop.
+// Returns whether the walk came to its end.
 template <typename Body>
-__device__ __forceinline__ bool walk_run(const PagedParams& p, int b, long long b_unit, long long u,
-                                         long long end, int lane, Body&& body) {
+__device__ __forceinline__ bool walk_run(const PagedParams& p, const Run& run, int lane, Body&& body) {
+    if (run.u0 >= run.u1) return true;
+    int b = run.b;
+    long long u = run.u0;
+    const long long end = run.u1;
     // lane x holds request win + x
     auto load = [&](int at) {
         return at + lane < p.B ? request_of(p, at + lane) : Request{0, 0, 0, 0, 0, 0, 0};
     };
     int win = b;
     Request held = load(win);
-    int in_req = static_cast<int>(u - b_unit);   // unit within the request: head * units + block
+    int in_req = static_cast<int>(u - run.b_unit);   // unit within the request: head * units + block
     while (u < end) {
         Request r;
         const int x = b - win;
@@ -232,10 +243,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     int* s_lo = reinterpret_cast<int*>(s_fac + N);         // [N] first key that a row attends,
     uint32_t* s_num = reinterpret_cast<uint32_t*>(s_lo + N);   // [N] and how many from there on
     float* s_lse = reinterpret_cast<float*>(s_num + N);        // [N] of a cluster's piece
-    long long* s_scan = reinterpret_cast<long long*>(s_row);   // set-up only
+    long long* s_scan = reinterpret_cast<long long*>(s_lse + N);   // [18] set-up only
     static_assert(C::NK <= 6 && C::NV <= 6, "ring barriers");
     static_assert(2 * sizeof(Segment) <= 12 * 8, "segments fit their place");
-    static_assert(50 * 8 + 9 * N * 4 <= C::MISC, "row values fit their place");
+    static_assert(50 * 8 + 9 * N * 4 + 18 * 8 <= C::MISC, "row values fit their place");
     constexpr int kFirst = 1, kStop = 2;   // s_kind: O^T starts anew; no more blocks
 
     const int warp = threadIdx.x >> 5;
@@ -291,47 +302,34 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
         return before + incl - x;
     };
-    long long all = 0, parts = 1, u0 = 0, u1 = 0;
-    long long* s_at = s_scan + 16;   // request that holds unit u0, and where it starts
-    if (p.cluster > 0) {
-        // A cluster has one tile and shares its blocks out evenly.
-        const int rank = cta % p.cluster, tile = cta / p.cluster;
-        const int b = tile / p.Hkv, hk = tile - b * p.Hkv;
-        const int units = request_of(p, b).units;
-        const int share = (units + p.cluster - 1) / p.cluster;
-        const int first = min(units, rank * share);
-        u0 = static_cast<long long>(hk) * units + first;
-        u1 = static_cast<long long>(hk) * units + min(units, first + share);
-        if (threadIdx.x == 0) {
-            s_at[0] = b;
-            s_at[1] = 0;
-        }
-    } else {
+    Run run{0, 1, 0, 0, 0, 0};
+    if (p.cluster == 0) {   // a cluster's producers find their share by themselves
+        long long* s_at = s_scan + 16;   // request that holds unit u0, and where it starts
         long long mine = 0, excl = 0;
         for (int b0 = 0; b0 < p.B; b0 += C::THREADS) {
             const int b = b0 + static_cast<int>(threadIdx.x);
             mine = b < p.B ? static_cast<long long>(request_of(p, b).units) * p.Hkv : 0;
             long long total;
             excl = block_scan(mine, total);
-            all += total;
+            run.all += total;
         }
         // No run is empty: the pieces of a tile are in consecutive CTAs.
-        parts = min(all, static_cast<long long>(gridDim.x));
-        u0 = cta < parts ? all * cta / parts : 0;
-        u1 = cta < parts ? all * (cta + 1) / parts : 0;
+        run.parts = min(run.all, static_cast<long long>(gridDim.x));
+        run.u0 = cta < run.parts ? run.all * cta / run.parts : 0;
+        run.u1 = cta < run.parts ? run.all * (cta + 1) / run.parts : 0;
         if (p.B <= C::THREADS) {   // one round: the sums of above
-            if (excl <= u0 && u0 < excl + mine) {
+            if (excl <= run.u0 && run.u0 < excl + mine) {
                 s_at[0] = threadIdx.x;
                 s_at[1] = excl;
             }
         } else {
             long long done = 0;
-            for (int b0 = 0; b0 < p.B && done <= u0; b0 += C::THREADS) {
+            for (int b0 = 0; b0 < p.B && done <= run.u0; b0 += C::THREADS) {
                 const int b = b0 + static_cast<int>(threadIdx.x);
                 mine = b < p.B ? static_cast<long long>(request_of(p, b).units) * p.Hkv : 0;
                 long long total;
                 excl = done + block_scan(mine, total);
-                if (excl <= u0 && u0 < excl + mine) {
+                if (excl <= run.u0 && run.u0 < excl + mine) {
                     s_at[0] = b;
                     s_at[1] = excl;
                 }
@@ -343,9 +341,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const int at_b = u0 < u1 ? static_cast<int>(s_at[0]) : 0;
-    const long long at_u = u0 < u1 ? s_at[1] : 0;
-    __syncthreads();   // s_at shares its place with the row values
+    if (p.cluster == 0 && run.u0 < run.u1) {
+        run.b = static_cast<int>(s_scan[16]);
+        run.b_unit = s_scan[17];
+    }
+
+    // Calls body for every segment of the CTA: those of its run, or its even
+    // share of the cluster's tile.
+    auto each_segment = [&](auto&& body) {
+        if (p.cluster == 0) return walk_run(p, run, lane, body);
+        const int rank = cta % p.cluster, tile = cta / p.cluster;
+        const int b = tile / p.Hkv;
+        const Request r = request_of(p, b);
+        const int share = (r.units + p.cluster - 1) / p.cluster;
+        const int first = rank * share;
+        return first >= r.units || body(b, r, tile - b * p.Hkv, first, min(share, r.units - first), 0ll);
+    };
 
     // One tile's chunk into a ring slot (whole warp).
     auto load_chunk = [&](const CUtensorMap* map, uint8_t* slot, uint64_t* bar, const PageBox& box,
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             tma_prefetch_desc(&tmK);
         }
         int fills = 0, seg = 0;
-        bool ok = walk_run(p, at_b, at_u, u0, u1, lane, [&](int b, const Request& r, int hk, int blk, int nblk,
+        bool ok = each_segment([&](int b, const Request& r, int hk, int blk, int nblk,
                                                             long long u) {
             const int buf = seg & 1;
             const PageBox box = first_box(b, r, blk);
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 s.none = none;
                 if (p.cluster == 0 && !whole && blk == 0) {   // this CTA has the tile's first piece
                     const long long end = u + r.units;
-                    const long long last = (end * parts + all - 1) / all - 1;   // CTA that ends it
+                    const long long last = (end * run.parts + run.all - 1) / run.all - 1;   // CTA that ends it
                     p.desc[cta] = PieceDesc{r.start, 0, r.n, hk, static_cast<int>(last) - cta + 1,
                                             2 * cta + 1, 2 * cta + 2, 2};
                 }
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         // ================= producer of V =================
         if (lane == 0) tma_prefetch_desc(&tmV);
         int fills = 0;
-        walk_run(p, at_b, at_u, u0, u1, lane, [&](int b, const Request& r, int hk, int blk, int nblk, long long) {
+        each_segment([&](int b, const Request& r, int hk, int blk, int nblk, long long) {
             return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk);
         });
         if (lane == 0) drain(v_full, C::NV, fills);
@@ -642,7 +653,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                                   e[2 * i], e[2 * i + 1]);
                     }
                 };
-                bool grows = x == 0;
+                bool grows = false;
                 if (x > 0) {
                     float mx = -INFINITY;
 #pragma unroll
@@ -653,7 +664,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     }
                     grows = mx > kRescaleThreshold;
                 }
-                if (named_barrier_or(bar, 128, grows)) {
+                if (x == 0 || named_barrier_or(bar, 128, grows)) {
                     // new reference maxima: over the warp's keys, then over the four warps
                     float mine_max = -INFINITY;
 #pragma unroll
@@ -818,13 +829,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
 
     // ---- a cluster's pieces become its tile's result ----
     if (p.cluster > 1) {
-        // pieces without a key, for CTAs that had no block
-        if (u0 >= u1 && threadIdx.x < N) s_lse[threadIdx.x] = -INFINITY;
-        cluster_sync();
         const int rank = cta % p.cluster, tile = cta / p.cluster;
         const int b = tile / p.Hkv, hk = tile - b * p.Hkv;
         const Request r = request_of(p, b);
-        const bool whole = (r.units + p.cluster - 1) / p.cluster >= r.units;   // written by rank 0
+        const int share = (r.units + p.cluster - 1) / p.cluster;
+        const bool whole = share >= r.units;   // written by rank 0
+        // pieces without a key, for CTAs that had no block
+        if (rank * share >= r.units && threadIdx.x < N) s_lse[threadIdx.x] = -INFINITY;
+        cluster_sync();
         for (int n = rank * (C::THREADS / 32) + warp; n < r.n * p.G && !whole;
              n += p.cluster * (C::THREADS / 32)) {
             float w = lane < p.cluster ? ld_cluster(&s_lse[n], lane) : -INFINITY;
