@@ -1,5 +1,6 @@
 // attn_paged.cu — launches of the paged attention kernel (attn_paged_kernel.cuh)
-// at head dims 64 and 128, and the kernel that joins pieces.
+// at head dim 64, and the kernel that joins pieces; head dims 128 and 256 compile
+// beside it in attn_paged_d128.cu and attn_paged_d256.cu.
 #include "attn_paged_kernel.cuh"
 
 namespace gbattn {
@@ -133,13 +134,8 @@ cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, bool ma
 cudaError_t launch_paged_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedParams& p, int d, bool f16, cudaStream_t stream) {
     switch (d) {
-        case 64: return f16 ? launch_paged_t<64, true, 2>(tq, tk, tv, p, stream)
-                            : launch_paged_t<64, false, 2>(tq, tk, tv, p, stream);
-        case 128:
-            if (p.fine) return f16 ? launch_paged_t<128, true, 2, true>(tq, tk, tv, p, stream)
-                                   : launch_paged_t<128, false, 2, true>(tq, tk, tv, p, stream);
-            return f16 ? launch_paged_t<128, true, 2>(tq, tk, tv, p, stream)
-                       : launch_paged_t<128, false, 2>(tq, tk, tv, p, stream);
+        case 64: return launch_paged_f<64, 2, false>(tq, tk, tv, p, f16, stream);
+        case 128: return launch_paged_tiles_d128(tq, tk, tv, p, f16, stream);
         case 256: return launch_paged_tiles_d256(tq, tk, tv, p, f16, stream);
     }
     return cudaErrorInvalidValue;

@@ -56,7 +56,7 @@ __device__ __forceinline__ void find_packed_tile(const SeqLayout& lq, int B, int
     local = x - packed_tile_base(lq, b, tokens);
 }
 
-template <int D, bool kF16, int kTiles, bool kFine>
+template <int D, bool kF16, int kTiles, bool kFine, bool kLoop>
 __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
     uint64_t* bar_p = bar_s + 2;          // [2]
     uint64_t* bar_o = bar_p + 2;          // [2]
     uint64_t* bar_fin = bar_o + 2;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_fin + 1);
+    uint64_t* q_free = bar_fin + 1;       // (kLoop) a tile's last S has read the queries
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_free + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -87,59 +88,81 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
     // ---- which tokens of which request, which key/value head, which keys ----
     const int G = p.G;
     const int TT = p.tile_tokens;
-    const int split = static_cast<int>(blockIdx.x) % p.splits;
-    const int hk = static_cast<int>(blockIdx.x) / p.splits % p.Hkv;
-    // the last tiles of a causal request see the most keys: they start first
-    const int tile = p.tiles - 1 - static_cast<int>(blockIdx.x) / p.splits / p.Hkv;
-    int b, local;
-    if (p.uniform_tiles > 0) {
-        b = tile / p.uniform_tiles;
-        local = tile - b * p.uniform_tiles;
-    } else {
-        find_packed_tile(p.lq, p.B, C::TILES * TT, tile, b, local);
-    }
-    const SeqSpan sq = seq_span(p.lq, b, nullptr, false);
-    const int N = sq.len;
-    const int tok0 = local * C::TILES * TT;
-    const int L = paged_keys(p, b);
-    const int off = L - N;   // query i stands at key position i + off
-    const bool live = local >= 0 && tok0 < N;
-    const int ntok = live ? min(C::TILES * TT, N - tok0) : 0;
-    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
-
-    // Key blocks [jlo(t), jhi(t)) that tile t needs, and the key range
-    // [klo, khi) of the whole CTA.
-    int jlo0 = 0, jlo1 = 0, jhi0 = 0, jhi1 = 0, klo = 0, khi = 0;
-#pragma unroll
-    for (int t = 0; t < C::TILES; ++t) {
-        const int first = tok0 + t * TT;
-        int lo = 0, hi = 0;
-        if (live && first < N) key_range(p, first, min(first + TT - 1, N - 1), off, L, lo, hi);
-        if (hi > lo) {
-            klo = khi > klo ? min(klo, lo) : lo;
-            khi = max(khi, hi);
+    // Unit x: a tile of a request and a key/value head (kLoop: a CTA takes one unit
+    // of every round of as many as there are CTAs, rounds going up and down the CTAs
+    // in turn; else one unit to the p.splits CTAs of a group).  The last tiles of a
+    // causal request see the most keys: units are in falling order where all
+    // requests have as many tiles, so that a CTA's units weigh the same in sum (4
+    // x 16 x 4096 queries, d 128: 7 rounds within 2% of the mean; request by request
+    // in equal strides the longest CTA had 23% more).
+    const int units = p.tiles * p.Hkv;
+    const int split = kLoop ? 0 : static_cast<int>(blockIdx.x) % p.splits;
+    const int unit = kLoop ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) / p.splits;
+    struct TilePlan {
+        int b, start, N, L;           // the request: first packed row, queries (0: no such tile), keys
+        int tok0, hk;                 // first token of the tile; key/value head
+        int jlo0, jhi0, jlo1, jhi1;   // key blocks of the query tiles
+        int klo, khi;                 // keys that the tile's queries attend between them
+        int pieces;
+    };
+    auto plan_of = [&](int x) {
+        TilePlan t;
+        const int order = x / p.Hkv;
+        const int tile = p.tiles - 1 - order;
+        t.hk = x - order * p.Hkv;
+        int local;
+        if (p.uniform_tiles > 0) {
+            local = tile / p.B;
+            t.b = tile - local * p.B;
+        } else {
+            find_packed_tile(p.lq, p.B, C::TILES * TT, tile, t.b, local);
         }
-        const int bl = lo / kTileRows, bh = (hi + kTileRows - 1) / kTileRows;
-        if (t == 0) { jlo0 = bl; jhi0 = bh; } else { jlo1 = bl; jhi1 = bh; }
+        const SeqSpan sq = seq_span(p.lq, t.b, nullptr, false);
+        t.start = sq.start;
+        t.N = sq.len;
+        t.L = paged_keys(p, t.b);
+        t.tok0 = local * C::TILES * TT;
+        if (local < 0 || t.tok0 >= t.N) t.N = t.tok0 = 0;
+        const int off = t.L - t.N;   // query i stands at key position i + off
+        t.jlo0 = t.jhi0 = t.jlo1 = t.jhi1 = t.klo = t.khi = 0;
+#pragma unroll
+        for (int i = 0; i < C::TILES; ++i) {
+            const int first = t.tok0 + i * TT;
+            int lo = 0, hi = 0;
+            if (first < t.N) key_range(p, first, min(first + TT, t.N) - 1, off, t.L, lo, hi);
+            if (hi > lo) {
+                t.klo = t.khi > t.klo ? min(t.klo, lo) : lo;
+                t.khi = max(t.khi, hi);
+            }
+            const int bl = lo / kTileRows, bh = (hi + kTileRows - 1) / kTileRows;
+            if (i == 0) { t.jlo0 = bl; t.jhi0 = bh; } else { t.jlo1 = bl; t.jhi1 = bh; }
+        }
+        t.pieces = 1;
+        if (!kLoop) {   // this CTA's share of the blocks
+            const int all_lo = t.klo / kTileRows, all_hi = (t.khi + kTileRows - 1) / kTileRows;
+            const int share = (all_hi - all_lo + p.splits - 1) / p.splits;
+            if (share > 0) t.pieces = (all_hi - all_lo + share - 1) / share;
+            if (t.pieces > 1) {
+                const int s0 = all_lo + split * share, s1 = min(all_hi, s0 + share);
+                t.jlo0 = max(t.jlo0, s0); t.jhi0 = min(t.jhi0, s1);
+                t.jlo1 = max(t.jlo1, s0); t.jhi1 = min(t.jhi1, s1);
+                if (t.jhi0 <= t.jlo0) t.jlo0 = t.jhi0 = 0;
+                if (t.jhi1 <= t.jlo1) t.jlo1 = t.jhi1 = 0;
+            }
+        }
+        return t;
+    };
+    TilePlan pl = plan_of(unit);
+    const int pieces = pl.pieces;
+    const bool joined = !kLoop && pieces > 1;
+    if (!kLoop) {
+        const int ntok = pl.N > 0 ? min(C::TILES * TT, pl.N - pl.tok0) : 0;
+        if (threadIdx.x == 0 && split == 0 && p.splits > 1 && p.cluster == 0)
+            p.desc[unit] = PieceDesc{pl.start, pl.tok0, ntok, pl.hk, joined ? pieces : 0,
+                                     unit * p.splits, unit * p.splits + 1, 1};
     }
-    // this CTA's share of the blocks
-    const int all_lo = klo / kTileRows, all_hi = (khi + kTileRows - 1) / kTileRows;
-    const int share = (all_hi - all_lo + p.splits - 1) / p.splits;
-    const int pieces = share > 0 ? (all_hi - all_lo + share - 1) / share : 1;
-    if (pieces > 1) {
-        const int s0 = all_lo + split * share, s1 = min(all_hi, s0 + share);
-        jlo0 = max(jlo0, s0); jhi0 = min(jhi0, s1);
-        jlo1 = max(jlo1, s0); jhi1 = min(jhi1, s1);
-        if (jhi0 <= jlo0) jlo0 = jhi0 = 0;
-        if (jhi1 <= jlo1) jlo1 = jhi1 = 0;
-    }
-    const bool joined = pieces > 1;
-    const int unit = tile * p.Hkv + hk;
-    if (threadIdx.x == 0 && split == 0 && p.splits > 1 && p.cluster == 0)
-        p.desc[unit] = PieceDesc{sq.start, tok0, ntok, hk, live && joined ? pieces : 0,
-                                 unit * p.splits, unit * p.splits + 1, 1};
     if (blockIdx.x == 0) paged_report(p);
-    if (!live) return;
+    if (!kLoop && pl.N == 0) return;
 
     // A cluster's pieces, where the K/V ring and the queries were: rows of D
     // floats in 16-byte groups, group c of row r at c ^ r (mod the groups of a
@@ -154,6 +177,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
     auto join_cluster = [&]() {
         cluster_sync();
         constexpr int WARPS = C::THREADS / 32;
+        const int ntok = min(C::TILES * TT, pl.N - pl.tok0);
         for (int u = split * WARPS + warp; u < ntok * G; u += p.splits * WARPS) {
             const int ut = u / G, g = u - ut * G;
             const int row = ut / TT * kTileRows + (ut % TT) * G + g;
@@ -168,9 +192,9 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             sum = __shfl_sync(0xffffffffu, sum, 0);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int head = hk * G + g;
+            const int head = pl.hk * G + g;
             uint2* dst = reinterpret_cast<uint2*>(
-                static_cast<uint16_t*>(p.O) + ((static_cast<size_t>(sq.start) + tok0 + ut) * p.lq.H + head) * D);
+                static_cast<uint16_t*>(p.O) + ((static_cast<size_t>(pl.start) + pl.tok0 + ut) * p.lq.H + head) * D);
             for (int c = lane; c < GROUPS; c += 32) {
                 // all pieces' loads before the first is used
                 constexpr unsigned LANES = GROUPS < 32 ? (1u << (GROUPS & 31)) - 1u : 0xffffffffu;
@@ -192,12 +216,12 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             }
             __syncwarp();
             if (lane == 0)
-                p.LSE[static_cast<size_t>(head) * p.lq.total + sq.start + tok0 + ut] =
+                p.LSE[static_cast<size_t>(head) * p.lq.total + pl.start + pl.tok0 + ut] =
                     sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
         }
         cluster_sync();   // no CTA leaves while another reads its piece
     };
-    if (split >= pieces) {   // no blocks left for this CTA
+    if (!kLoop && split >= pieces) {   // no blocks left for this CTA
         if (p.cluster > 0 && joined) {
             for (int r = threadIdx.x; r < C::TILES * kTileRows; r += C::THREADS) s_lse[r] = -INFINITY;
             join_cluster();
@@ -205,13 +229,20 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         return;
     }
 
-    auto jlo = [&](int t) { return t ? jlo1 : jlo0; };
-    auto jhi = [&](int t) { return t ? jhi1 : jhi0; };
-    auto nkv_t = [&](int t) { return jhi(t) - jlo(t); };
-    const int jbeg = (nkv_t(0) > 0) ? jlo0 : jlo1;
-    const int jend = max(jhi0, jhi1);
-    const int nkv = (nkv_t(0) > 0 || nkv_t(1) > 0) ? jend - jbeg : 0;
-    auto edge = [&](int j) { return j * kTileRows < klo || (j + 1) * kTileRows > khi; };
+    // blocks the CTA walks for a plan: tile A's window starts no later than tile B's
+    auto first_block = [](const TilePlan& t) { return t.jhi0 > t.jlo0 ? t.jlo0 : t.jlo1; };
+    auto num_blocks = [&](const TilePlan& t) { return max(0, max(t.jhi0, t.jhi1) - first_block(t)); };
+    // the next unit's plan, or false
+    int round = 0;
+    auto next_unit = [&]() {
+        if (!kLoop) return false;
+        const int n = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+        ++round;
+        const int x = round * n + ((round & 1) ? n - 1 - c : c);
+        if (x >= units) return false;   // only in the last round
+        pl = plan_of(x);
+        return true;
+    };
 
     // ---- set-up ----
     if (threadIdx.x == 0) {
@@ -227,6 +258,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             mbar_init(&bar_o[t], 1);
         }
         mbar_init(bar_fin, 1);
+        mbar_init(q_free, 1);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -241,36 +273,47 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
 
     if (warp == C::PRODUCER_WARP) {
         // ================= TMA producer =================
-        if (nkv > 0) {
-            if (lane == 0) {
-                tma_prefetch_desc(&tmQ);
-                tma_prefetch_desc(&tmK);
-                tma_prefetch_desc(&tmV);
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        int seq = 0;                        // ring fills so far
+        int tiles = 0, q_n0 = 0, q_n1 = 0;  // units with blocks; loads of each query tile
+        bool ok = true;
+        do {
+            const int jbeg = first_block(pl), nkv = num_blocks(pl);
+            if (nkv == 0) continue;
+            const int32_t* table = p.page_table + static_cast<size_t>(pl.b) * p.max_pages;
+            PageBox box = page_box(p, table, jbeg * kTileRows, pl.klo, pl.khi, lane);
+            if (tiles > 0 && !mbar_wait_warp(q_free, (tiles - 1) & 1, s_abort)) {
+                ok = false;
+                break;
             }
-            const int ntiles = (nkv_t(1) > 0) ? 2 : 1;
-            if (lane == 0) {
-                for (int t = 0; t < ntiles; ++t) {
+            ++tiles;
+            for (int t = 0; t < C::TILES; ++t) {
+                const bool used = t ? pl.jhi1 > pl.jlo1 : pl.jhi0 > pl.jlo0;
+                if (used && lane == 0) {
                     mbar_arrive_expect_tx(&bar_q[t], static_cast<uint32_t>(TT * G) * C::ROWB);
                     for (int cb = 0; cb < C::NCB; ++cb)
                         tma_load_3d(sQ + t * C::TILE + cb * C::CB_BYTES, &tmQ, &bar_q[t],
-                                    cb * C::BOXW, hk * G, sq.start + tok0 + t * TT);
+                                    cb * C::BOXW, pl.hk * G, pl.start + pl.tok0 + t * TT);
                 }
             }
-            int seq = 0;
-            bool ok = true;
-            PageBox box = page_box(p, table, jbeg * kTileRows, klo, khi, lane);
+            q_n0 += pl.jhi0 > pl.jlo0;
+            q_n1 += pl.jhi1 > pl.jlo1;
             for (int j = jbeg; j < jbeg + nkv && ok; ++j) {
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
                                        static_cast<uint32_t>(p.box_rows) * C::ROWB;
                 // the next tile's table entries arrive while this tile waits
                 PageBox next = box;
-                if (j + 1 < jbeg + nkv) next = page_box(p, table, (j + 1) * kTileRows, klo, khi, lane);
+                if (j + 1 < jbeg + nkv) next = page_box(p, table, (j + 1) * kTileRows, pl.klo, pl.khi, lane);
                 for (int which = 0; which < 2; ++which) {
                     const int slot = seq % C::NSLOT;
                     const uint32_t ph = (seq / C::NSLOT) & 1;
                     bool free_ok;
                     if constexpr (kBlockRelease) {
-                        const int bi = j - jbeg;
+                        const int bi = seq / 2;
                         const int wb = which == 0 ? bi - kPairs : bi - kPairs + 1;
                         free_ok = bi < kPairs || mbar_wait_warp(&empty[wb % kPairs], (wb / kPairs) & 1, s_abort);
                     } else {
@@ -284,34 +327,35 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                     __syncwarp();
                     if (kFine && box.needed) {
                         tma_load_5d(sKV + slot * C::TILE + lane * 8 * C::ROWB, which ? &tmV : &tmK, &full[slot], 0,
-                                    box.row, 0, hk, page_box_checked(p, box));
+                                    box.row, 0, pl.hk, page_box_checked(p, box));
                     } else if (box.needed) {
                         const int page = page_box_checked(p, box);
                         uint8_t* dst = sKV + slot * C::TILE + lane * p.box_rows * 128;
                         const CUtensorMap* m = which ? &tmV : &tmK;
                         for (int cb = 0; cb < C::NCB; ++cb)
                             tma_load_4d(dst + cb * C::CB_BYTES, m, &full[slot], cb * C::BOXW, box.row,
-                                        hk, page);
+                                        pl.hk, page);
                     }
                     __syncwarp();
                     ++seq;
                 }
                 box = next;
             }
-            // Drain: every load this warp issued has landed before teardown.
-            if (lane == 0) {
-                volatile int no_abort = 0;
-                for (int t = 0; t < ntiles; ++t) mbar_wait(&bar_q[t], 0, &no_abort);
-                for (int s = 0; s < C::NSLOT && s < seq; ++s) {
-                    const int uses = (seq - s + C::NSLOT - 1) / C::NSLOT;
-                    mbar_wait(&full[s], (uses - 1) & 1, &no_abort);
-                }
+        } while (ok && next_unit());
+        // Drain: every load this warp issued has landed before teardown.
+        if (lane == 0) {
+            volatile int no_abort = 0;
+            if (q_n0 > 0) mbar_wait(&bar_q[0], (q_n0 - 1) & 1, &no_abort);
+            if (q_n1 > 0) mbar_wait(&bar_q[1], (q_n1 - 1) & 1, &no_abort);
+            for (int s = 0; s < C::NSLOT && s < seq; ++s) {
+                const int uses = (seq - s + C::NSLOT - 1) / C::NSLOT;
+                mbar_wait(&full[s], (uses - 1) & 1, &no_abort);
             }
         }
         __syncwarp();
     } else if (warp == C::MMA_WARP) {
         // ================= MMA issuer =================
-        if (lane == 0 && nkv > 0) {
+        {
             const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t dq1 = sdesc_adv(dq0, C::TILE);
             // K-major K and MN-major V of slot 0: 8-row groups 1 KB apart and column
@@ -339,85 +383,110 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                                                           accumulate ? 1u : 0u);
             };
             bool ok = true;
-            bool q_ready[2] = {false, false};
-            int seq = 0;
-            int v_slot = 0;
-            uint32_t v_phase = 0;
-            bool v_ready = false;
-            for (int j = jbeg; j < jbeg + nkv && ok; ++j) {
-                const int kslot = seq % C::NSLOT;
-                const uint32_t kph = (seq / C::NSLOT) & 1;
-                ++seq;
-                const int next_v_slot = seq % C::NSLOT;
-                const uint32_t next_v_phase = (seq / C::NSLOT) & 1;
-                ++seq;
-                bool k_ready = false;
-                constexpr bool kEarlyVRelease = C::NSLOT == 2;   // see attn_fwd_kernel
-                int v_last = -1;
-                for (int t = 0; t < C::TILES; ++t)
-                    if (kEarlyVRelease && j - 1 >= jlo(t) && j - 1 < jhi(t)) v_last = t;
-                for (int t = 0; t < C::TILES && ok; ++t) {
-                    const bool qk = j >= jlo(t) && j < jhi(t);
-                    const bool prev = j - 1 >= jlo(t) && j - 1 < jhi(t);
-                    const bool last_pv = prev && j == jhi(t);
-                    if (prev) {   // O_t += P_t(j-1) V_{j-1}
-                        ok = mbar_wait(&bar_p[t], (j - 1 - jlo(t)) & 1, s_abort);
+            uint32_t g = 0;                   // K/V blocks of the units before
+            uint32_t q_n0 = 0, q_n1 = 0;      // units in which a query tile had blocks
+            uint32_t p_n0 = 0, p_n1 = 0;      // blocks of a query tile in them
+            do {
+                const int jlo0 = pl.jlo0, jhi0 = pl.jhi0, jlo1 = pl.jlo1, jhi1 = pl.jhi1;
+                auto jlo = [&](int t) { return t ? jlo1 : jlo0; };
+                auto jhi = [&](int t) { return t ? jhi1 : jhi0; };
+                const int jbeg = first_block(pl), nkv = num_blocks(pl);
+                if (nkv == 0) continue;
+                if (lane == 0) {
+                    // parity of P of block j of query tile t: (p_base(t) + j) & 1
+                    const uint32_t p_b0 = p_n0 - jlo0, p_b1 = p_n1 - jlo1;
+                    auto p_parity = [&](int t, int j) { return ((t ? p_b1 : p_b0) + j) & 1u; };
+                    bool q_ready[2] = {false, false};
+                    uint32_t seq = 2 * g;
+                    int v_slot = 0;
+                    uint32_t v_phase = 0;
+                    bool v_ready = false;
+                    for (int j = jbeg; j < jbeg + nkv && ok; ++j) {
+                        const int kslot = seq % C::NSLOT;
+                        const uint32_t kph = (seq / C::NSLOT) & 1;
+                        ++seq;
+                        const int next_v_slot = seq % C::NSLOT;
+                        const uint32_t next_v_phase = (seq / C::NSLOT) & 1;
+                        ++seq;
+                        bool k_ready = false;
+                        constexpr bool kEarlyVRelease = C::NSLOT == 2;   // see attn_fwd_kernel
+                        int v_last = -1;
+                        for (int t = 0; t < C::TILES; ++t)
+                            if (kEarlyVRelease && j - 1 >= jlo(t) && j - 1 < jhi(t)) v_last = t;
+                        for (int t = 0; t < C::TILES && ok; ++t) {
+                            const bool qk = j >= jlo(t) && j < jhi(t);
+                            const bool prev = j - 1 >= jlo(t) && j - 1 < jhi(t);
+                            const bool last_pv = prev && j == jhi(t);
+                            if (prev) {   // O_t += P_t(j-1) V_{j-1}
+                                ok = mbar_wait(&bar_p[t], p_parity(t, j - 1), s_abort);
+                                if (!ok) break;
+                                tc_fence_after();
+                                if (!v_ready) {
+                                    ok = mbar_wait(&full[v_slot], v_phase, s_abort);
+                                    v_ready = true;
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                }
+                                issue_pv(t, v_slot, j - 1 > jlo(t));
+                                if (last_pv) tc_commit(&bar_o[t]);
+                                if (t == v_last) tc_commit(&empty[v_slot]);
+                            }
+                            if (qk) {     // S_t = Q_t K_j^T
+                                if (!q_ready[t]) {
+                                    ok = mbar_wait(&bar_q[t], (t ? q_n1 : q_n0) & 1, s_abort);
+                                    q_ready[t] = true;
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                }
+                                if (!k_ready) {
+                                    ok = mbar_wait(&full[kslot], kph, s_abort);
+                                    k_ready = true;
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                }
+                                issue_qk(t, kslot);
+                                tc_commit(&bar_s[t]);
+                            }
+                        }
                         if (!ok) break;
-                        tc_fence_after();
-                        if (!v_ready) {
+                        if constexpr (kBlockRelease) {
+                            tc_commit(&empty[kslot / 2]);   // pair (seq / 2) % kPairs
+                        } else {
+                            tc_commit(&empty[kslot]);
+                            if (j > jbeg && v_last < 0) tc_commit(&empty[v_slot]);
+                        }
+                        v_slot = next_v_slot;
+                        v_phase = next_v_phase;
+                        v_ready = false;
+                    }
+                    if (kLoop && ok) tc_commit(q_free);
+                    for (int t = 0; t < C::TILES && ok; ++t) {   // tiles whose last block is the unit's last
+                        if (jhi(t) == jlo(t) || jhi(t) != jbeg + nkv) continue;
+                        ok = mbar_wait(&bar_p[t], p_parity(t, jhi(t) - 1), s_abort);
+                        if (ok && !v_ready) {
                             ok = mbar_wait(&full[v_slot], v_phase, s_abort);
                             v_ready = true;
-                            if (!ok) break;
-                            tc_fence_after();
                         }
-                        issue_pv(t, v_slot, j - 1 > jlo(t));
-                        if (last_pv) tc_commit(&bar_o[t]);
-                        if (t == v_last) tc_commit(&empty[v_slot]);
-                    }
-                    if (qk) {     // S_t = Q_t K_j^T
-                        if (!q_ready[t]) {
-                            ok = mbar_wait(&bar_q[t], 0, s_abort);
-                            q_ready[t] = true;
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        if (!k_ready) {
-                            ok = mbar_wait(&full[kslot], kph, s_abort);
-                            k_ready = true;
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        issue_qk(t, kslot);
-                        tc_commit(&bar_s[t]);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(t, v_slot, jhi(t) - 1 > jlo(t));
+                        tc_commit(&bar_o[t]);
+                        if (!kBlockRelease) tc_commit(&empty[v_slot]);   // (one query tile)
                     }
                 }
-                if (!ok) break;
-                if constexpr (kBlockRelease) {
-                    tc_commit(&empty[(j - jbeg) % kPairs]);
-                } else {
-                    tc_commit(&empty[kslot]);
-                    if (j > jbeg && v_last < 0) tc_commit(&empty[v_slot]);
-                }
-                v_slot = next_v_slot;
-                v_phase = next_v_phase;
-                v_ready = false;
-            }
-            for (int t = 0; t < C::TILES && ok; ++t) {   // tiles whose last block is the CTA's last
-                if (nkv_t(t) == 0 || jhi(t) != jbeg + nkv) continue;
-                ok = mbar_wait(&bar_p[t], (jhi(t) - 1 - jlo(t)) & 1, s_abort);
-                if (ok && !v_ready) {
-                    ok = mbar_wait(&full[v_slot], v_phase, s_abort);
-                    v_ready = true;
-                }
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(t, v_slot, jhi(t) - 1 > jlo(t));
-                tc_commit(&bar_o[t]);
-            }
+                g += nkv;
+                p_n0 += jhi0 - jlo0;
+                p_n1 += jhi1 - jlo1;
+                q_n0 += jhi0 > jlo0;
+                q_n1 += jhi1 > jlo1;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            } while (ok && next_unit());
             // Drain: no MMA of this CTA is in flight at teardown.
-            tc_commit(bar_fin);
-            volatile int no_abort = 0;
-            mbar_wait(bar_fin, 0, &no_abort);
+            if (lane == 0) {
+                tc_commit(bar_fin);
+                volatile int no_abort = 0;
+                mbar_wait(bar_fin, 0, &no_abort);
+            }
         }
         __syncwarp();
     } else {
@@ -425,24 +494,28 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         const int t = warp >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
-        const int tl = r / G;                       // token within the tile
-        const int first_tok = tok0 + t * TT;
-        const int tok = first_tok + tl;
-        const bool row_ok = tl < TT && tok < N;
-        const int head = hk * G + (r - tl * G);
-        const int pos = tok + off;
-        const int first_pos = first_tok + off, last_pos = first_pos + TT - 1;
-        const int ntile = nkv_t(t);
+        const int tl = r / G;                       // token within the query tile
+        const int rg = r - tl * G;                  // head within the group
         const int W = p.window;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t t_S = t_lane + 128u * t;
         const uint32_t t_O = t_lane + C::O_COL + D * t;
+        int g = 0;       // K/V blocks of the units before
+        int s_n = 0;     // blocks of this query tile in them
+        int o_n = 0;     // of them with blocks of this query tile
+        bool ok = true;
+        do {
+        const int L = pl.L, klo = pl.klo, khi = pl.khi;
+        const int jlo = t ? pl.jlo1 : pl.jlo0, jhi = t ? pl.jhi1 : pl.jhi0;
+        const int first_pos = pl.tok0 + t * TT + L - pl.N, last_pos = first_pos + TT - 1;
+        const int pos = first_pos + tl;
+        const int fill0 = 2 * (g - first_block(pl)) + 1;   // ring fill of V_j: fill0 + 2 j
+        const int s_b = s_n - jlo;                         // parity of S_j: (s_b + j) & 1
         float m_ref = -INFINITY;   // reference max, log2 units of scaled scores
         float l = 0.f;
-        bool ok = true;
-        for (int j = jlo(t); j < jhi(t); ++j) {
+        for (int j = jlo; j < jhi; ++j) {
             const int k0 = j * kTileRows;
-            if (!mbar_wait_warp(&bar_s[t], (j - jlo(t)) & 1, s_abort)) {
+            if (!mbar_wait_warp(&bar_s[t], (s_b + j) & 1, s_abort)) {
                 ok = false;
                 break;
             }
@@ -450,10 +523,10 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             // V rows outside [klo, khi) become zero.  Only after S_j: by then
             // every earlier fill of V_j's slot has been waited for, so that
             // the parity below can only mean this one.
-            if (edge(j)) {
-                const int vseq = 2 * (j - jbeg) + 1;
-                const int slot = vseq % C::NSLOT;
-                if (!mbar_wait_warp(&full[slot], (vseq / C::NSLOT) & 1, s_abort)) {
+            if (k0 < klo || k0 + kTileRows > khi) {
+                const int fill = fill0 + 2 * j;
+                const int slot = fill % C::NSLOT;
+                if (!mbar_wait_warp(&full[slot], (fill / C::NSLOT) & 1, s_abort)) {
                     ok = false;
                     break;
                 }
@@ -549,7 +622,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                 rowsum = (a0 + a1) + (a2 + a3);
             }
             l = l * alpha + rowsum;
-            if (warp_rescale && j > jlo(t)) {   // O row *= alpha (PV of block j-1 is complete)
+            if (warp_rescale && j > jlo) {   // O row *= alpha (PV of block j-1 is complete)
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -566,22 +639,29 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             mbar_arrive_warp(&bar_p[t]);
         }
         // ---- epilogue: O = acc / l and the log-sum-exp, or a piece of them ----
-        if (ok && ntile > 0) {
-            ok = mbar_wait_warp(&bar_o[t], 0, s_abort);
+        const bool any = jhi > jlo;
+        if (ok && any) {
+            ok = mbar_wait_warp(&bar_o[t], o_n & 1, s_abort);
             tc_fence_after();
         }
         if (joined && p.cluster > 0)   // the ring and the queries are free once every product is done
             ok = mbar_wait_warp(bar_fin, 0, s_abort) && ok;
+        g += num_blocks(pl);
+        s_n += jhi - jlo;
+        o_n += any;
         if (ok) {
+            const int tok = pl.tok0 + t * TT + tl;
+            const bool row_ok = tl < TT && tok < pl.N;
+            const int head = pl.hk * G + rg;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t piece_row =
                 (static_cast<size_t>(unit) * p.splits + split) * p.slot_rows + t * kTileRows + r;
-            const size_t out_row = (static_cast<size_t>(sq.start) + tok) * p.lq.H + head;
+            const size_t out_row = (static_cast<size_t>(pl.start) + tok) * p.lq.H + head;
             uint32_t o[32];
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 __syncwarp();   // rows past the tile's end skip the stores below
-                if (ntile > 0) {
+                if (any) {
                     tmem_ld32(t_O + 32 * c, o);
                     tmem_ld_wait();
                     reg_fence(o);
@@ -620,9 +700,13 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                 s_lse[t * kTileRows + r] = lse2;
             } else if (row_ok) {
                 if (joined) p.part_lse[piece_row] = lse2;
-                else p.LSE[static_cast<size_t>(head) * p.lq.total + sq.start + tok] = lse2 * kLn2;
+                else p.LSE[static_cast<size_t>(head) * p.lq.total + pl.start + tok] = lse2 * kLn2;
             }
         }
+        // O_t is read: the next unit's first P V, which overwrites it, waits for P of
+        // these threads.
+        tc_fence_before();
+        } while (ok && next_unit());
     }
 
     if (joined && p.cluster > 0) {
@@ -638,16 +722,28 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_DEVICE_TIMEOUT));
 }
 
-template <int D, bool kF16, int kTiles, bool kFine = false>
+template <int D, bool kF16, int kTiles, bool kFine, bool kLoop>
 cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PagedParams& p, cudaStream_t stream) {
     using C = FwdCfg<D, false, kF16, false, kTiles>;
-    auto kern = attn_paged_kernel<D, kF16, kTiles, kFine>;
+    auto kern = attn_paged_kernel<D, kF16, kTiles, kFine, kLoop>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(p.tiles) * static_cast<unsigned>(p.Hkv * p.splits);
+    const unsigned units = static_cast<unsigned>(p.tiles) * static_cast<unsigned>(p.Hkv);
+    const unsigned grid = kLoop ? (units < kSMs ? units : kSMs) : units * static_cast<unsigned>(p.splits);
     return launch_overlapped_cluster(kern, grid, C::THREADS, C::SMEM, p.cluster, stream, tq, tk, tv, p);
+}
+
+// One unit per CTA or group of CTAs, or (p.splits = 1) a persistent CTA per SM.
+template <int D, int kTiles, bool kFine>
+cudaError_t launch_paged_f(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const PagedParams& p, bool f16, cudaStream_t s) {
+    if (p.splits == 1)
+        return f16 ? launch_paged_t<D, true, kTiles, kFine, true>(tq, tk, tv, p, s)
+                   : launch_paged_t<D, false, kTiles, kFine, true>(tq, tk, tv, p, s);
+    return f16 ? launch_paged_t<D, true, kTiles, kFine, false>(tq, tk, tv, p, s)
+               : launch_paged_t<D, false, kTiles, kFine, false>(tq, tk, tv, p, s);
 }
 
 }  // namespace

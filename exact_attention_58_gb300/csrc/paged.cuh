@@ -135,6 +135,9 @@ inline void carve_pieces(PagedParams& p, void* ws, size_t slots, int rows, size_
 // Launches (validated arguments only).
 cudaError_t launch_paged_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedParams& p, int d, bool f16, cudaStream_t stream);
+cudaError_t launch_paged_tiles_d128(const CUtensorMap& tq, const CUtensorMap& tk,
+                                    const CUtensorMap& tv, const PagedParams& p, bool f16,
+                                    cudaStream_t stream);
 cudaError_t launch_paged_tiles_d256(const CUtensorMap& tq, const CUtensorMap& tk,
                                     const CUtensorMap& tv, const PagedParams& p, bool f16,
                                     cudaStream_t stream);
