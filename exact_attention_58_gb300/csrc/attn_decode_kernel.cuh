@@ -147,6 +147,24 @@ struct Run {
     long long b_unit;       // its first unit
 };
 
+// Cuts all units into equal runs, one per CTA of the grid, as far as they go
+// round (no run in between is empty: the pieces of a tile are in consecutive
+// CTAs): boundary i is at floor(all i / parts).  Code that runs once costs its
+// fetching, and a wide division is long: the ordinary case does without.
+__device__ __forceinline__ void cut_run(Run& r) {
+    const uint32_t i = blockIdx.x;
+    r.parts = min(r.all, static_cast<long long>(gridDim.x));
+    if (i >= r.parts) return;
+    if (r.all < (1ll << 24)) {   // times gridDim.x < 2^8: in 32 bits
+        const uint32_t n = static_cast<uint32_t>(r.parts), all = static_cast<uint32_t>(r.all);
+        r.u0 = all * i / n;
+        r.u1 = all * (i + 1) / n;
+    } else {
+        r.u0 = r.all * i / r.parts;
+        r.u1 = r.all * (i + 1) / r.parts;
+    }
+}
+
 // Walks a CTA's run, segment by segment, with the whole warp: body(request
 // index, request, head, first block, blocks, first unit) returns false to stop.
 // Returns whether the walk came to its end.
@@ -303,7 +321,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         return before + incl - x;
     };
     Run run{0, 1, 0, 0, 0, 0};
-    if (p.cluster == 0) {   // a cluster's producers find their share by themselves
+    // A cluster's producers find their share by themselves, and so do those of up
+    // to 32 requests their run, one request per lane (a microsecond less).
+    const bool alone = p.cluster > 0 || p.B <= 32;
+    if (!alone) {
         long long* s_at = s_scan + 16;   // request that holds unit u0, and where it starts
         long long mine = 0, excl = 0;
         for (int b0 = 0; b0 < p.B; b0 += C::THREADS) {
@@ -313,10 +334,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             excl = block_scan(mine, total);
             run.all += total;
         }
-        // No run is empty: the pieces of a tile are in consecutive CTAs.
-        run.parts = min(run.all, static_cast<long long>(gridDim.x));
-        run.u0 = cta < run.parts ? run.all * cta / run.parts : 0;
-        run.u1 = cta < run.parts ? run.all * (cta + 1) / run.parts : 0;
+        cut_run(run);
         if (p.B <= C::THREADS) {   // one round: the sums of above
             if (excl <= run.u0 && run.u0 < excl + mine) {
                 s_at[0] = threadIdx.x;
@@ -341,7 +359,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    if (p.cluster == 0 && run.u0 < run.u1) {
+    if (!alone && run.u0 < run.u1) {
         run.b = static_cast<int>(s_scan[16]);
         run.b_unit = s_scan[17];
     }
@@ -407,6 +425,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         }
     };
 
+    if (p.cluster == 0 && alone && (warp == C::K_WARP || warp == C::V_WARP)) {
+        const long long mine = lane < p.B ? static_cast<long long>(request_of(p, lane).units) * p.Hkv : 0;
+        long long incl = mine;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        run.all = __shfl_sync(0xffffffffu, incl, 31);
+        cut_run(run);
+        const unsigned past = __ballot_sync(0xffffffffu, incl > run.u0);
+        run.b = past != 0 ? __ffs(past) - 1 : 0;
+        run.b_unit = __shfl_sync(0xffffffffu, incl - mine, run.b);
+    }
+
     if (warp == C::K_WARP) {
         // ================= producer of segments, Q and K =================
         if (lane == 0) {
@@ -436,7 +469,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 s.none = none;
                 if (p.cluster == 0 && !whole && blk == 0) {   // this CTA has the tile's first piece
                     const long long end = u + r.units;
-                    const long long last = (end * run.parts + run.all - 1) / run.all - 1;   // CTA that ends it
+                    // CTA that ends it: the first whose boundary is at or past `end`
+                    const long long last = run.all < (1ll << 24)
+                                               ? (static_cast<uint32_t>(end) * static_cast<uint32_t>(run.parts) +
+                                                  static_cast<uint32_t>(run.all) - 1) /
+                                                         static_cast<uint32_t>(run.all) - 1
+                                               : (end * run.parts + run.all - 1) / run.all - 1;
                     p.desc[cta] = PieceDesc{r.start, 0, r.n, hk, static_cast<int>(last) - cta + 1,
                                             2 * cta + 1, 2 * cta + 2, 2};
                 }
