@@ -203,6 +203,9 @@ attn_status attn_page_table(const int32_t* cached_lens, const int32_t* new_lens,
     for (const auto& o : outs)
         for (const auto& i : ins)
             if (overlap(o.ptr, o.bytes, i.ptr, i.bytes)) return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].ptr, outs[i].bytes, outs[j].ptr, outs[j].bytes)) return ATTN_ERR_INVALID_ARG;
     for (int i = 0; i < 4; ++i)   // page_table is an output too
         if (overlap(page_table, nb * max_pages, ins[i].ptr, ins[i].bytes)) return ATTN_ERR_INVALID_ARG;
     TableParams p{};

@@ -289,7 +289,8 @@ attn_status attn_bwd_varlen(const void* Q, const void* K, const void* V, const v
  *                              its end, request by request: the i-th taken is
  *                              free_pages[num_free - 1 - i].  The caller lowers
  *                              num_free by pages_taken.
- * Outputs other than page_table must not overlap inputs.  Clamped and reported
+ * Outputs must not overlap inputs or one another (ATTN_ERR_INVALID_ARG), page_table
+ * apart, which is both.  B, max_pages, max_tokens, free_capacity >= 1.  Clamped and reported
  * as ATTN_ERR_INVALID_ARG through dev_status: negative lengths (to 0),
  * requests longer than max_pages pages (their new tokens are cut), new tokens
  * past max_tokens (cut), num_free outside [0, free_capacity].  When the free
@@ -309,7 +310,7 @@ attn_status attn_page_table(const int32_t* cached_lens, const int32_t* new_lens,
  * -1 is skipped; any other slot outside [0, num_pages * page_size) is skipped
  * and reported as ATTN_ERR_INVALID_ARG through dev_status.  Slots must differ
  * from one another: what a slot named twice holds is unspecified.  K and V
- * must not overlap the caches.  bf16 or fp16, d in {64, 128, 256}.  One launch.
+ * must not overlap the caches.  T >= 1; bf16 or fp16, d in {64, 128, 256}.  One launch.
  */
 attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void* v_cache,
                               const int64_t* slots, int T, int H_kv, int d, attn_dtype dtype,
@@ -337,7 +338,7 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
  * ATTN_ERR_INVALID_ARG through dev_status: bad cu_seqlens_q as in
  * attn_fwd_varlen, seq_lens outside [0, max_pages * page_size], and page ids
  * outside [0, num_pages) (zeros are read for their keys).
- * bf16 or fp16, d in {64, 128, 256}.  The workspace holds
+ * total_q, max_seqlen_q, B >= 1; bf16 or fp16, d in {64, 128, 256}.  The workspace holds
  * attn_fwd_paged_workspace_size(...) bytes (16-byte aligned, contents on entry
  * do not matter; may be NULL when that is 0); calls that may overlap on the
  * GPU need one each.  One or two launches.

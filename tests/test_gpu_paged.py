@@ -132,11 +132,12 @@ def test_many_requests():
     check_attention(*run(x, True), x, True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("q_len", [1, 4, 150])
-def test_strided_views(q_len):
-    """Queries as a slice of a fused projection; token-major pages; K and V side
-    by side in one array."""
-    H, Hkv, d, page = 4, 2, 128, 16
+def test_strided_views(q_len, d):
+    """Queries as a slice of a fused projection, or heads first; token-major
+    pages; K and V side by side in one array."""
+    H, Hkv, page = 4, 2, 16
     x = make_paged([q_len, 1], [500, 77], H, Hkv, d, page, seed=q_len, poison=math.nan)
     T = q_len + 1
     fused = torch.full((T, H + 2 * Hkv, d), math.nan, dtype=BF16)
@@ -150,6 +151,9 @@ def test_strided_views(q_len):
         assert not kc.is_contiguous()
         o, lse = run(x, True, q=fused.cuda()[:, :H], k_cache=kc, v_cache=vc)
         assert torch.equal(o, base[0]) and torch.equal(lse, base[1])
+    heads_first = x.q.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    o, lse = run(x, True, q=heads_first)
+    assert o.is_contiguous() and torch.equal(o, base[0]) and torch.equal(lse, base[1])
 
 
 @pytest.mark.parametrize("q_lens", [[1, 1, 0], [40, 1, 130]], ids=str)
@@ -169,6 +173,54 @@ def test_max_seqlen_is_only_a_bound(q_len):
     x = make_paged([q_len, 1], [700, 300], 4, 2, 128, 16, seed=2, poison=math.nan)
     run(x, True, max_q=1000)
     check_attention(*run(x, True, max_q=1000), x, True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_tiles(d):
+    """Several rounds of query tiles per CTA: uniform and ragged requests, empty
+    ones among them, with and without a window."""
+    for q_lens, k_lens in (([130] * 40, [200] * 40),
+                           ([0, 300, 1, 77] * 10, [50, 350, 400, 90] * 10)):
+        x = make_paged(q_lens, k_lens, 8, 8, d, 16, seed=d, poison=math.nan)
+        check_attention(*run(x, True), x, True)
+        check_attention(*run(x, False, 60), x, False, 60)
+
+
+@pytest.mark.parametrize("q_len", [1, 100])
+def test_guard_bands(q_len):
+    """Nothing is written outside O and LSE, nor beside the caches' slots."""
+    x = make_paged([q_len, 1, 7], [300, 90, 40], 4, 2, 64, 16, seed=3, poison=math.nan)
+    n = x.q.numel()
+    band = 4096
+    buf = torch.full((n + 2 * band,), 3.0, dtype=BF16, device="cuda")
+    lbuf = torch.full((4 * x.q.shape[0] + 2 * band,), 3.0, device="cuda")
+    out = buf[band:band + n].view(x.q.shape)
+    lse = lbuf[band:-band].view(4, -1)
+    for wide in (False, True):
+        run(x, True, out=out, lse=lse, wide=wide)
+        check_attention(out, lse, x, True)
+        for b in (buf, lbuf):
+            assert bool((b[:band] == 3).all()) and bool((b[-band:] == 3).all())
+
+
+def test_two_streams_at_once():
+    """Calls with a workspace each, on two streams at the same time."""
+    a = make_paged([1] * 5, [3000, 100, 900, 2000, 50], 8, 2, 128, 16, seed=50)
+    b = make_paged([300, 40], [1300, 700], 8, 2, 128, 16, seed=51)
+    ref = [run(x, True, wide=True) for x in (a, b)]
+    dev = [[t.cuda() for t in (x.q, x.k_cache, x.v_cache,
+                               torch.nn.functional.pad(x.page_table, (0, 8000), value=-1),
+                               x.seq_lens, x.cu)] for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i, x in enumerate((a, b)):
+            got[i].append(ea.attn_fwd_paged(*dev[i], x.max_q, causal=True, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, ref[i][0]) and torch.equal(lse, ref[i][1])
 
 
 def test_scale_and_dirty_workspace():

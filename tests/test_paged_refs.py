@@ -88,7 +88,7 @@ def table(lib, **kw):
     (dict(cached=0x1002), 3), (dict(slots=0x8004), 3), (dict(taken=0x9001), 3),
     # outputs inside inputs
     (dict(seq=0x1000), 1), (dict(cu=0x1000 - 16), 1), (dict(taken=0x5000), 1),
-    (dict(slots=0x4000 - 8), 1), (dict(seq=0x3000 + 4 * 31), 1), (dict(table=0x1008), 1),
+    (dict(slots=0x4000 - 8), 1), (dict(seq=0x6004), 1), (dict(taken=0x8000), 1), (dict(seq=0x3000 + 4 * 31), 1), (dict(table=0x1008), 1),
 ])
 def test_table_refusals(lib, kw, expected):
     assert table(lib, **kw) == expected
