@@ -13,15 +13,15 @@ namespace {
 // dependent loads: each warp asks for the O_i of up to kBatch pieces before it
 // knows their weights.  A row takes one warp, or (kPerRow) the eight of a CTA,
 // which share its pieces: for few tiles, where one long context can be in as many
-// pieces as there are CTAs (76 pieces a row: 9 -> 6 us).  The order of the sums is
+// pieces as there are CTAs (76 pieces a row: 9 -> 6 us).  Where there are only a
+// few pieces a row, kBatch = 4 leaves registers for more CTAs at a time.  The order of the sums is
 // fixed either way.  Most CTAs find nothing to join and leave, so there should
 // not be many of them: 6000 took 15 us to come and go.
-template <int D, bool kF16, int kPerRow>
+template <int D, bool kF16, int kPerRow, int kBatch>
 __global__ void __launch_bounds__(kPerRow > 1 ? 32 * kPerRow : 128) paged_join_kernel(const PagedParams p) {
     grid_dep_wait();
     grid_dep_launch_dependents();
     constexpr int PER = D / 32;   // floats of a lane
-    constexpr int kBatch = 10;
     constexpr int kWarps = kPerRow > 1 ? kPerRow : 4;
     __shared__ float s_acc[kPerRow][D];
     __shared__ float s_sum[kPerRow];
@@ -101,17 +101,21 @@ __global__ void __launch_bounds__(kPerRow > 1 ? 32 * kPerRow : 128) paged_join_k
 }
 
 template <int D, bool kF16>
-cudaError_t launch_join_t(cudaLaunchConfig_t& cfg, int descs, int rows, bool many, const PagedParams& p) {
-    const int groups = many ? rows : (rows + 3) / 4;
+cudaError_t launch_join_t(cudaLaunchConfig_t& cfg, int descs, int rows, JoinKind kind, const PagedParams& p) {
+    const int groups = kind == kJoinFewRows ? rows : (rows + 3) / 4;
     cfg.gridDim = dim3(static_cast<unsigned>(descs), static_cast<unsigned>(groups < 16 ? groups : 16));
-    cfg.blockDim = dim3(many ? 256 : 128);
-    return many ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, 8>, p)
-                : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, 1>, p);
+    cfg.blockDim = dim3(kind == kJoinFewRows ? 256 : 128);
+    switch (kind) {
+        case kJoinFewRows: return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, 8, 10>, p);
+        case kJoinFewPieces: return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, 1, 4>, p);
+        case kJoinMany: return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kF16, 1, 10>, p);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, bool many, int d, bool f16,
+cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, JoinKind kind, int d, bool f16,
                               cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
@@ -121,12 +125,12 @@ cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, bool ma
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (d) {
-        case 64: return f16 ? launch_join_t<64, true>(cfg, descs, rows, many, p)
-                            : launch_join_t<64, false>(cfg, descs, rows, many, p);
-        case 128: return f16 ? launch_join_t<128, true>(cfg, descs, rows, many, p)
-                             : launch_join_t<128, false>(cfg, descs, rows, many, p);
-        case 256: return f16 ? launch_join_t<256, true>(cfg, descs, rows, many, p)
-                             : launch_join_t<256, false>(cfg, descs, rows, many, p);
+        case 64: return f16 ? launch_join_t<64, true>(cfg, descs, rows, kind, p)
+                            : launch_join_t<64, false>(cfg, descs, rows, kind, p);
+        case 128: return f16 ? launch_join_t<128, true>(cfg, descs, rows, kind, p)
+                             : launch_join_t<128, false>(cfg, descs, rows, kind, p);
+        case 256: return f16 ? launch_join_t<256, true>(cfg, descs, rows, kind, p)
+                             : launch_join_t<256, false>(cfg, descs, rows, kind, p);
     }
     return cudaErrorInvalidValue;
 }

@@ -148,9 +148,13 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tk, co
 cudaError_t launch_paged_decode_d256(const CUtensorMap& tq, const CUtensorMap& tk,
                                      const CUtensorMap& tv, const PagedParams& p, bool f16,
                                      cudaStream_t stream);
-// Joins the pieces of p.desc[0, descs), up to `rows` rows each; `many`: eight
-// warps share a row, for results in many pieces.
-cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, bool many, int d, bool f16,
+// Joins the pieces of p.desc[0, descs), up to `rows` rows each.
+enum JoinKind {
+    kJoinFewPieces,   // a few pieces a row
+    kJoinFewRows,     // few rows in many pieces each
+    kJoinMany,        // many rows and pieces
+};
+cudaError_t launch_paged_join(const PagedParams& p, int descs, int rows, JoinKind kind, int d, bool f16,
                               cudaStream_t stream);
 
 }  // namespace gbattn

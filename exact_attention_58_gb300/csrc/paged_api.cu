@@ -345,8 +345,9 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
         const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
         // pieces of a tile in the mean: CTAs by tiles
-        const bool many = t.decode && static_cast<long long>(B) * H_kv <= 16;
-        e = launch_paged_join(p, static_cast<int>(t.descs), rows, many, d, f16, s);
+        const JoinKind kind = !t.decode ? kJoinMany
+                              : static_cast<long long>(B) * H_kv <= 16 ? kJoinFewRows : kJoinFewPieces;
+        e = launch_paged_join(p, static_cast<int>(t.descs), rows, kind, d, f16, s);
     }
     return from_cuda(e);
 }
