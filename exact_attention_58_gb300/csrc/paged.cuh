@@ -39,6 +39,8 @@ struct PagedParams {
     unsigned long long page_magic;   // floor(2^62 / page_size) + 1
     int box_rows;               // keys of one TMA box: the power of two dividing page_size, <= 128
     int fine;                   // tile kernel: boxes of 8 keys and all of d (box_rows = 8)
+    int few;                    // > 0: requests of up to this many tokens are the decode kernel's, the
+                                // others the tile kernel's; 0: all are the launched kernel's
     int tile_tokens;            // tokens of one 128-row query tile (rows are (token, head of the group))
     int causal, window;
     float scale_log2;           // scale * log2(e)
@@ -48,6 +50,7 @@ struct PagedParams {
     PieceDesc* desc;
     int slot_rows;              // rows of a slot
     int tiles;                  // query tiles of the grid (per key/value head)
+    int tile_div;               // tokens per tile index (packed_tile_base)
     int uniform_tiles;          // > 0: every request has this many tiles; 0: tiles follow the packed offsets
     int splits;                 // CTAs that share one tile's keys
     int cluster;                // > 0: CTAs of a cluster, which takes one tile and joins its pieces itself

@@ -46,7 +46,7 @@ attn_status check_cache(int Hkv, int d, attn_dtype dtype, int num_pages, int pag
 struct Plan {
     bool decode;           // attn_decode_kernel: few query rows per request
     int tile_tokens;       // tokens of a query tile
-    int tiles, uniform, splits, cluster;
+    int tiles, tile_div, uniform, splits, cluster;
     size_t slots, descs;   // pieces and joined tiles that the workspace holds
     int rows;              // rows of a slot
 };
@@ -55,7 +55,8 @@ struct Plan {
 // SMs are not all of one size).
 constexpr int kClusters[9] = {0, kSMs, 76, 46, 36, 28, 23, 15, 15};
 
-Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d) {
+// few > 0: requests of up to that many tokens are another launch's.
+Plan plan_one(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d, int few) {
     Plan t{};
     const int G = H / Hkv;
     const long long blocks = (max_keys + kTileRows - 1) / kTileRows;
@@ -88,28 +89,72 @@ Plan plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_key
     t.tile_tokens = kTileRows / G;
     const int cta_tokens = t.tile_tokens * per_cta;
     const long long per_request = (max_q + cta_tokens - 1) / cta_tokens;
-    const long long packed = total_q / cta_tokens + static_cast<long long>(B);
-    const bool uniform = per_request * B <= packed;
+    t.tile_div = few > 0 ? std::min(few + 1, std::max(1, cta_tokens / 2)) : cta_tokens;
+    const long long packed = total_q / t.tile_div + (few > 0 ? 1ll : static_cast<long long>(B));
+    const bool uniform = few == 0 && per_request * B <= packed;
     t.tiles = static_cast<int>(std::min(uniform ? per_request * B : packed, 0x7fffffffll));
     t.uniform = uniform ? static_cast<int>(per_request) : 0;
     // With fewer CTAs than SMs the keys of a tile are shared out, as far as
     // all CTAs still run at once: over a cluster, or over more CTAs where that
     // saves more blocks than joining in a second launch costs (4, about 8 us).
-    const long long ctas = static_cast<long long>(t.tiles) * Hkv;
+    // Where most requests have no tile, as far as one long request's do.
+    const long long ctas = (few > 0 ? total_q / cta_tokens + 1ll : t.tiles) * Hkv;
     t.splits = static_cast<int>(std::max(1ll, std::min(kSMs / ctas, blocks)));
     int cs = 8;
     while (cs > 1 && (ctas > kClusters[cs] || cs > blocks)) --cs;
-    if (t.splits > 1 && cs > 1 && (blocks + cs - 1) / cs <= (blocks + t.splits - 1) / t.splits + 4) {
+    if (t.splits > 1 && cs > 1 &&
+        (few > 0 || (blocks + cs - 1) / cs <= (blocks + t.splits - 1) / t.splits + 4)) {
         t.splits = t.cluster = cs;
         t.rows = per_cta * kTileRows;
         return t;
     }
     t.rows = per_cta * kTileRows;
+    if (few > 0) t.splits = 1;   // (no cluster fits: the pieces' place is the other launch's)
     if (t.splits > 1) {
         t.descs = static_cast<size_t>(ctas);
         t.slots = t.descs * t.splits;
     }
     return t;
+}
+
+// The launches of a call.  Where most requests are short beside the longest (a
+// step of decoding with a prompt's chunk in it: the mean at most a quarter of the
+// longest), requests of up to `few` tokens go to the decode kernel and the others
+// to the tile kernel, if the page table holds at least 48 key blocks a request: a
+// single token's tile is one CTA's in the tile kernel, however long its context.
+// 32/8 heads, d = 128: 15 tokens over up to 30000 keys beside a chunk of 512, 563
+// -> 255 us; 63 over up to 8000, 341 -> 303 us; but 63 over up to 2000, 135 -> 144
+// us, hence the 48 blocks (the tile kernel's grid has to have room for more tiles
+// than there are, and the empty ones cost it up to 25 us).
+struct Plans {
+    int count, few;
+    Plan plan[2];
+};
+
+Plans plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_keys, int d) {
+    Plans t{};
+    const int G = H / Hkv;
+    const int few = G <= 64 ? std::max(1, 16 / G) : 0;   // at most 16 rows where one token has no more
+    if (max_q * static_cast<long long>(G) > 64 && few >= 1 && max_keys >= 48 * kTileRows &&
+        4ll * total_q <= static_cast<long long>(B) * max_q) {
+        t.count = 2;
+        t.few = few;
+        t.plan[0] = plan_one(B, H, Hkv, total_q, max_q, max_keys, d, few);
+        t.plan[1] = plan_one(B, H, Hkv, total_q, few, max_keys, d, 0);
+    } else {
+        t.count = 1;
+        t.plan[0] = plan_one(B, H, Hkv, total_q, max_q, max_keys, d, 0);
+    }
+    return t;
+}
+
+// Workspace bytes: at most one of the launches leaves pieces.
+size_t plans_bytes(const Plans& t, int d) {
+    size_t bytes = 0;
+    for (int i = 0; i < t.count; ++i)
+        if (t.plan[i].slots > 0)
+            bytes = std::max(bytes, pieces_bytes(t.plan[i].slots, t.plan[i].rows, d, t.plan[i].descs));
+    return bytes;
 }
 
 attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int max_pages,
@@ -124,9 +169,11 @@ attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int
     // key blocks of all heads of a request, counted in 32 bits on the device
     if ((static_cast<long long>(max_pages) * page_size / kTileRows + 1) * Hkv >= (1ll << 31))
         return ATTN_ERR_UNSUPPORTED;
-    const Plan t = plan_paged(B, H, Hkv, total_q, std::min(max_q, total_q),
-                              static_cast<long long>(max_pages) * page_size, d);
-    if (static_cast<long long>(t.tiles) * Hkv * t.splits >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+    const Plans t = plan_paged(B, H, Hkv, total_q, std::min(max_q, total_q),
+                               static_cast<long long>(max_pages) * page_size, d);
+    for (int i = 0; i < t.count; ++i)
+        if (static_cast<long long>(t.plan[i].tiles) * Hkv * t.plan[i].splits >= (1ll << 31))
+            return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -265,9 +312,9 @@ size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int ma
                                      int max_pages, int page_size, int d) {
     if (check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d) != ATTN_OK)
         return 0;
-    const Plan t = plan_paged(B, H, H_kv, total_q, std::min(max_seqlen_q, total_q),
-                                  static_cast<long long>(max_pages) * page_size, d);
-    return t.slots == 0 ? 0 : pieces_bytes(t.slots, t.rows, d, t.descs);
+    return plans_bytes(plan_paged(B, H, H_kv, total_q, std::min(max_seqlen_q, total_q),
+                                  static_cast<long long>(max_pages) * page_size, d),
+                       d);
 }
 
 attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cache, void* O,
@@ -293,15 +340,14 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
         !aligned(page_table, 4))
         return ATTN_ERR_MISALIGNED;
     const int max_q = std::min(max_seqlen_q, total_q);
-    const Plan t = plan_paged(B, H, H_kv, total_q, max_q,
-                                  static_cast<long long>(max_pages) * page_size, d);
-    PagedParams p{};
-    if (t.slots > 0) {
-        if (workspace == nullptr || workspace_bytes < pieces_bytes(t.slots, t.rows, d, t.descs))
-            return ATTN_ERR_WORKSPACE;
+    const Plans plans = plan_paged(B, H, H_kv, total_q, max_q,
+                                   static_cast<long long>(max_pages) * page_size, d);
+    const size_t need = plans_bytes(plans, d);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
-        carve_pieces(p, workspace, t.slots, t.rows, t.descs);
     }
+    PagedParams p{};
     p.O = O;
     p.LSE = LSE;
     p.seq_lens = seq_lens;
@@ -311,43 +357,55 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
     p.B = B;
     p.Hkv = H_kv;
     p.G = H / H_kv;
+    p.few = plans.few;
     p.num_pages = num_pages;
     p.page_size = page_size;
     p.max_pages = max_pages;
     p.page_magic = (1ull << 62) / static_cast<unsigned long long>(page_size) + 1;
-    p.box_rows = std::min(kTileRows, page_size & -page_size);
-    // More than 16 boxes of 64 columns a tile: 16 of 8 keys and all columns
-    // instead (the decode kernel issues K and V from two warps and has the time).
-    p.fine = !t.decode && kTileRows / p.box_rows * (d / 64) > 16;
-    if (p.fine) p.box_rows = 8;
-    p.tile_tokens = t.tile_tokens;
     p.causal = causal != 0;
     // a window of 2^30 keys is none: no two positions are that far apart
     p.window = window > 0 && window < kMaxPagedKeys ? window : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.tiles = t.tiles;
-    p.uniform_tiles = t.uniform;
-    p.splits = t.splits;
-    p.cluster = t.cluster;
-    p.slot_rows = t.rows;
-    CUtensorMap tq, tk, tv;
-    if (!make_tmap_queries(&tq, Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
-                           p.tile_tokens) ||
-        !make_tmap_cache(&tk, k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
-                         cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
-        !make_tmap_cache(&tv, v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
-                         cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
-        return ATTN_ERR_CUDA;
     const bool f16 = dtype == ATTN_DTYPE_FP16;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = t.decode ? launch_paged_decode(tq, tk, tv, p, d, f16, s)
-                             : launch_paged_tiles(tq, tk, tv, p, d, f16, s);
-    if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
-        const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
-        // pieces of a tile in the mean: CTAs by tiles
-        const JoinKind kind = !t.decode ? kJoinMany
-                              : static_cast<long long>(B) * H_kv <= 16 ? kJoinFewRows : kJoinFewPieces;
-        e = launch_paged_join(p, static_cast<int>(t.descs), rows, kind, d, f16, s);
+    CUtensorMap tq[2], tk[2], tv[2];
+    PagedParams params[2];
+    for (int i = 0; i < plans.count; ++i) {   // all maps before the first launch
+        const Plan& t = plans.plan[i];
+        if (t.slots > 0) carve_pieces(p, workspace, t.slots, t.rows, t.descs);
+        p.box_rows = std::min(kTileRows, page_size & -page_size);
+        // More than 16 boxes of 64 columns a tile: 16 of 8 keys and all columns
+        // instead (the decode kernel issues K and V from two warps and has the time).
+        p.fine = !t.decode && kTileRows / p.box_rows * (d / 64) > 16;
+        if (p.fine) p.box_rows = 8;
+        p.tile_tokens = t.tile_tokens;
+        p.tiles = t.tiles;
+        p.tile_div = t.tile_div;
+        p.uniform_tiles = t.uniform;
+        p.splits = t.splits;
+        p.cluster = t.cluster;
+        p.slot_rows = t.rows;
+        params[i] = p;
+        if (!make_tmap_queries(&tq[i], Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
+                               p.tile_tokens) ||
+            !make_tmap_cache(&tk[i], k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+                             cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
+            !make_tmap_cache(&tv[i], v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+                             cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
+            return ATTN_ERR_CUDA;
+    }
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < plans.count && e == cudaSuccess; ++i) {
+        const Plan& t = plans.plan[i];
+        e = t.decode ? launch_paged_decode(tq[i], tk[i], tv[i], params[i], d, f16, s)
+                     : launch_paged_tiles(tq[i], tk[i], tv[i], params[i], d, f16, s);
+        if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
+            const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
+            // pieces of a tile in the mean: CTAs by tiles
+            const JoinKind kind = !t.decode ? kJoinMany
+                                  : static_cast<long long>(B) * H_kv <= 16 ? kJoinFewRows : kJoinFewPieces;
+            e = launch_paged_join(params[i], static_cast<int>(t.descs), rows, kind, d, f16, s);
+        }
     }
     return from_cuda(e);
 }

@@ -186,6 +186,24 @@ def test_many_tiles(d):
         check_attention(*run(x, False, 60), x, False, 60)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(4, 4), (8, 2), (64, 1), (65, 1)], ids=str)
+def test_single_tokens_beside_a_chunk(d, heads):
+    """Most requests short beside the longest: they and the long ones go to a
+    kernel each, and every row is written once."""
+    group = heads[0] // heads[1]
+    q_lens = [1] * 14 + [150] + [16 // group, 0, 16 // group + 1, 64 // group + 1] + [2] * 6
+    k_lens = [37 * i + q + 5 for i, q in enumerate(q_lens)]
+    k_lens[3], k_lens[20] = 0, 1
+    x = make_paged(q_lens, k_lens, *heads, d, 16, seed=d, poison=math.nan, extra_rows=3)
+    for wide in (False, True):
+        out = torch.full(x.q.shape, 7.0, dtype=BF16, device="cuda")
+        lse = torch.full((heads[0], x.q.shape[0]), 7.0, device="cuda")
+        run(x, True, 90, wide=wide, out=out, lse=lse)
+        check_attention(out, lse, x, True, 90)
+        assert bool((out[-3:] == 7).all()) and bool((lse[:, -3:] == 7).all())
+
+
 @pytest.mark.parametrize("q_len", [1, 100])
 def test_guard_bands(q_len):
     """Nothing is written outside O and LSE, nor beside the caches' slots."""

@@ -100,6 +100,8 @@ def test_workspace_sizes(lib):
     assert size(1, 8, 2, 1, 1, 100, 16, 128) == 0         # among a cluster, if they are few
     assert size(1, 8, 2, 200, 200, 10000, 16, 128) > 0 == size(1, 8, 2, 200, 200, 100, 16, 128)
     assert size(4, 16, 16, 4 * 4096, 4096, 32, 128, 128) == 0   # enough tiles without
+    # single tokens beside a chunk: the pieces of the single tokens'
+    assert size(64, 32, 8, 575, 512, 800, 16, 128) == size(64, 32, 8, 64, 4, 800, 16, 128) > 0
     for bad in (dict(B=0), dict(H=7), dict(d=96), dict(max_pages=0)):
         a = dict(B=1, H=8, Hkv=2, total_q=1, max_seqlen_q=1, max_pages=100, page_size=16, d=128)
         a.update(bad)
