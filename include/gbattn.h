@@ -341,7 +341,7 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
  * total_q, max_seqlen_q, B >= 1; bf16 or fp16, d in {64, 128, 256}.  The workspace holds
  * attn_fwd_paged_workspace_size(...) bytes (16-byte aligned, contents on entry
  * do not matter; may be NULL when that is 0); calls that may overlap on the
- * GPU need one each.  One or two launches.
+ * GPU need one each.  One to three launches.
  */
 attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cache, void* O,
                            float* LSE, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
