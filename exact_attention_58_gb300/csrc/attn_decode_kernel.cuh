@@ -56,7 +56,7 @@ struct DecodeCfg {
     static constexpr int QCB_BYTES = N * 128;                // Q: column blocks of N rows
     static constexpr int Q_BYTES = (D / 64) * QCB_BYTES;
     static constexpr int P_BYTES = kTileRows * 128;          // P^T: 128 keys of up to 64 rows
-    static constexpr int MISC = 3072;                        // barriers, segments, row values
+    static constexpr int MISC = 2944;                        // barriers, segments, row values
     static constexpr int AVAIL = 232448 - MISC - 2 * Q_BYTES - 2 * P_BYTES;
     static constexpr int NSLOT = AVAIL / SLOT < 11 ? AVAIL / SLOT : 11;
     static constexpr int NK = (NSLOT + 1) / 2, NV = NSLOT / 2;   // K and V rings

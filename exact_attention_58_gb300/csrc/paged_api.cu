@@ -135,7 +135,9 @@ Plans plan_paged(int B, int H, int Hkv, int total_q, int max_q, long long max_ke
     Plans t{};
     const int G = H / Hkv;
     const int few = G <= 64 ? std::max(1, 16 / G) : 0;   // at most 16 rows where one token has no more
-    if (max_q * static_cast<long long>(G) > 64 && few >= 1 && max_keys >= 48 * kTileRows &&
+    // (2^27: tokens of a tile are at most 15.1 times tile_div, and a tile's number
+    // times its tokens, of rows behind the last request too, has to fit 32 bits)
+    if (max_q * static_cast<long long>(G) > 64 && few >= 1 && max_keys >= 48 * kTileRows && total_q < (1 << 27) &&
         4ll * total_q <= static_cast<long long>(B) * max_q) {
         t.count = 2;
         t.few = few;
@@ -165,14 +167,15 @@ attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int
     if (H / Hkv > kTileRows) return ATTN_ERR_UNSUPPORTED;
     if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<long long>(max_pages) * page_size > kMaxPagedKeys) return ATTN_ERR_UNSUPPORTED;
-    if (total_q > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    if (total_q > (1 << 30) || B > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
     // key blocks of all heads of a request, counted in 32 bits on the device
     if ((static_cast<long long>(max_pages) * page_size / kTileRows + 1) * Hkv >= (1ll << 31))
         return ATTN_ERR_UNSUPPORTED;
     const Plans t = plan_paged(B, H, Hkv, total_q, std::min(max_q, total_q),
                                static_cast<long long>(max_pages) * page_size, d);
+    // a persistent CTA's next unit, up to two rounds past the last, fits 32 bits
     for (int i = 0; i < t.count; ++i)
-        if (static_cast<long long>(t.plan[i].tiles) * Hkv * t.plan[i].splits >= (1ll << 31))
+        if (static_cast<long long>(t.plan[i].tiles) * Hkv * t.plan[i].splits >= (1ll << 31) - 2 * kSMs)
             return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }

@@ -280,7 +280,9 @@ attn_status attn_bwd_varlen(const void* Q, const void* K, const void* V, const v
  *   page_table    in/out       the pages that request b holds, entries [0,
  *                              ceil(cached_lens[b] / page_size)), are read; the
  *                              pages its new tokens need beyond them are
- *                              entered behind; nothing else is written
+ *                              entered behind; nothing else is written.  Requests
+ *                              that get new tokens may share full pages, not the
+ *                              one that their cached tokens end in
  *   slots         out int64 [max_tokens]  slot of each packed new token; -1
  *                              from the last token on
  *   pages_taken   out [1]      free pages used
@@ -338,7 +340,9 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
  * ATTN_ERR_INVALID_ARG through dev_status: bad cu_seqlens_q as in
  * attn_fwd_varlen, seq_lens outside [0, max_pages * page_size], and page ids
  * outside [0, num_pages) (zeros are read for their keys).
- * total_q, max_seqlen_q, B >= 1; bf16 or fp16, d in {64, 128, 256}.  The workspace holds
+ * 1 <= B, total_q <= 2^30, max_seqlen_q >= 1; bf16 or fp16, d in {64, 128, 256}.
+ * Requests may share pages.  O, LSE and the workspace must not overlap the
+ * inputs or one another.  The workspace holds
  * attn_fwd_paged_workspace_size(...) bytes (16-byte aligned, contents on entry
  * do not matter; may be NULL when that is 0); calls that may overlap on the
  * GPU need one each.  One to three launches.

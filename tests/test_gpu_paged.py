@@ -204,6 +204,32 @@ def test_single_tokens_beside_a_chunk(d, heads):
         assert bool((out[-3:] == 7).all()) and bool((lse[:, -3:] == 7).all())
 
 
+@pytest.mark.parametrize("longest,max_q", [(200, 200), (2, 200), (0, 200), (2, 2), (0, 2)])
+@pytest.mark.parametrize("B", [8, 40])
+def test_mostly_empty_batches(longest, max_q, B):
+    """Calls with room for more than they hold: few requests have queries, or
+    none, whichever kernels the sizes choose."""
+    q_lens = ([0, 0, longest] + [0] * 5) * (B // 8)
+    rows = sum(q_lens) + 9
+    x = make_paged(q_lens, [500 + q for q in q_lens], 4, 2, 64, 16, seed=1, poison=math.nan, extra_rows=9)
+    for wide in (False, True):
+        out = torch.full((rows, 4, 64), 7.0, dtype=BF16, device="cuda")
+        lse = torch.full((4, rows), 7.0, device="cuda")
+        run(x, True, max_q=max_q, wide=wide, out=out, lse=lse)
+        check_attention(out, lse, x, True)
+        assert bool((out[-9:] == 7).all()) and bool((lse[:, -9:] == 7).all())
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_requests_share_pages(q_len):
+    """The same page in several requests: a prompt that they begin with."""
+    x = make_paged([q_len] * 3, [400, 400, 400], 4, 2, 128, 16, seed=5, poison=math.nan)
+    x.page_table[1:, :20] = x.page_table[0, :20]
+    for b in (1, 2):
+        x.keys[b][:320], x.values[b][:320] = x.keys[0][:320], x.values[0][:320]
+    check_attention(*run(x, True), x, True)
+
+
 @pytest.mark.parametrize("q_len", [1, 100])
 def test_guard_bands(q_len):
     """Nothing is written outside O and LSE, nor beside the caches' slots."""

@@ -39,7 +39,8 @@ def paged(lib, **kw):
     (dict(scale=math.nan), 1), (dict(scale=math.inf), 1),
     (dict(d=96), 2), (dict(d=32), 2), (dict(dtype=1), 2), (dict(dtype=3), 2), (dict(page=12), 2),
     (dict(H=258), 2), (dict(width=1 << 27), 2), (dict(pages=1 << 28), 2),
-    (dict(total=(1 << 30) + 1), 2),
+    (dict(total=(1 << 30) + 1), 2), (dict(B=(1 << 30) + 1), 2),
+    (dict(B=(1 << 30) - 100, H=2, total=65, max_q=65), 2),   # 2^31 - 200 tiles
     (dict(Q=FAKE + 8), 3), (dict(kc=FAKE + 2), 3), (dict(O=FAKE + 4), 3), (dict(LSE=FAKE + 4), 3),
     (dict(cu=FAKE + 2), 3), (dict(seq=FAKE + 1), 3), (dict(table=FAKE + 2), 3),
     (dict(qt=1020), 3), (dict(qh=0), 3), (dict(sp=-8), 3), (dict(sh=12), 3), (dict(st=1 << 40), 3),
@@ -102,6 +103,8 @@ def test_workspace_sizes(lib):
     assert size(4, 16, 16, 4 * 4096, 4096, 32, 128, 128) == 0   # enough tiles without
     # single tokens beside a chunk: the pieces of the single tokens'
     assert size(64, 32, 8, 575, 512, 800, 16, 128) == size(64, 32, 8, 64, 4, 800, 16, 128) > 0
+    # ... whose tiles' numbers fit 32 bits: 2^27 rows and more go to one kernel
+    assert size(64, 1, 1, (1 << 27) - 1, 1 << 27, 800, 16, 64) > 0 == size(64, 1, 1, 1 << 27, 1 << 27, 800, 16, 64)
     for bad in (dict(B=0), dict(H=7), dict(d=96), dict(max_pages=0)):
         a = dict(B=1, H=8, Hkv=2, total_q=1, max_seqlen_q=1, max_pages=100, page_size=16, d=128)
         a.update(bad)
