@@ -22,7 +22,8 @@
 // replaced by -inf before use, and their V rows, whose product with P = 0
 // would still be NaN for a NaN or infinite V, are zeroed in shared memory.
 //
-// Two query tiles per CTA share each K/V block (one tile at head dim 256).
+// Two query tiles per CTA share each K/V block (at head dim 256 one tile, whose
+// rows have two softmax threads each).
 //
 // Bound, like attn_fwd_kernel, by the softmax warps' issue and the chain of
 // products per key block (about 2 us for 256 rows x 128 keys at d = 128): whole
@@ -64,12 +65,31 @@ __device__ __forceinline__ void find_packed_tile(const PagedParams& p, int x, in
     local = x - packed_tile_base(p, b);
 }
 
+template <int D, bool kF16, int kTiles>
+struct PagedCfg : FwdCfg<D, false, kF16, false, kTiles> {
+    using Base = FwdCfg<D, false, kF16, false, kTiles>;
+    // Softmax threads of a row, which share its keys.  One query tile alone has
+    // nothing to run while its softmax does: two threads a row halve that (8
+    // chunks of 33 to 65 tokens, d = 256: 27.4 -> 25.4 us).  Two tiles fill in for
+    // one another, and the barrier per block costs more than it gives (4 x 16 x
+    // 4096, d = 128: 245 -> 264 us; d = 64 chunks with a window: 46.9 -> 51.3).
+    static constexpr int PARTS = kTiles == 1 ? 2 : 1;
+    static constexpr int NC = kTileRows / PARTS;      // keys of a thread
+    static constexpr int DC = D / PARTS;              // output columns of a thread
+    static constexpr int ROW_THREADS = kTileRows * PARTS;
+    static constexpr int THREADS = kTiles * ROW_THREADS + 64;
+    static constexpr int PRODUCER_WARP = kTiles * ROW_THREADS / 32;
+    static constexpr int MMA_WARP = PRODUCER_WARP + 1;
+    static constexpr int ROW_FLOATS = kTiles * ROW_THREADS;   // one per softmax thread
+    static constexpr int SMEM = Base::SMEM + (PARTS > 1 ? 3 * ROW_FLOATS * 4 : 0);   // maxima; sums of two units
+};
+
 template <int D, bool kF16, int kTiles, bool kFine, bool kLoop>
-__global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS, 1)
+__global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-    using C = FwdCfg<D, false, kF16, false, kTiles>;
+    using C = PagedCfg<D, kF16, kTiles>;
     grid_dep_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -89,6 +109,8 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
     uint64_t* q_free = bar_fin + 1;       // (kLoop) a tile's last S has read the queries
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_free + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    float* s_max = reinterpret_cast<float*>(bars + 128);   // (PARTS = 2) [tile][part][row]
+    float* s_sum = s_max + C::ROW_FLOATS;                  // and [unit & 1][tile][part][row]
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -262,7 +284,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar_s[t], 1);
-            mbar_init(&bar_p[t], kTileRows);
+            mbar_init(&bar_p[t], C::ROW_THREADS);
             mbar_init(&bar_o[t], 1);
         }
         mbar_init(bar_fin, 1);
@@ -498,20 +520,27 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         }
         __syncwarp();
     } else {
-        // ================= softmax (one thread per row) =================
-        const int t = warp >> 2;
+        // ================= softmax (one or two threads per row) =================
+        const int t = warp / (C::ROW_THREADS / 32);
+        const int part = C::PARTS == 1 ? 0 : (warp >> 2) % C::PARTS;   // keys c0 .. c0 + NC, output columns likewise
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
+        const int c0 = part * C::NC;
         const int tl = r / G;                       // token within the query tile
         const int rg = r - tl * G;                  // head within the group
         const int W = p.window;
+        const int bar = 1 + t;                      // hardware barrier of the tile's softmax threads
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint32_t t_S = t_lane + 128u * t;
-        const uint32_t t_O = t_lane + C::O_COL + D * t;
+        const uint32_t t_S = t_lane + 128u * t + c0;
+        const uint32_t t_P = t_lane + 128u * t + c0 / 2;
+        const uint32_t t_O = t_lane + C::O_COL + D * t + part * C::DC;
+        float* const x_mine = s_max + (t * C::PARTS + part) * kTileRows + r;
+        float* const x_other = s_max + (t * C::PARTS + (part ^ 1)) * kTileRows + r;
         int g = 0;       // K/V blocks of the units before
         int s_n = 0;     // blocks of this query tile in them
         int o_n = 0;     // of them with blocks of this query tile
-        bool ok = true;
+        int u_n = 0;     // units before
+        bool ok = true;  // of the warp; a tile's warps agree on it at a unit's end
         do {
         const int L = pl.L, klo = pl.klo, khi = pl.khi;
         const int jlo = t ? pl.jlo1 : pl.jlo0, jhi = t ? pl.jhi1 : pl.jhi0;
@@ -520,13 +549,13 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         const int fill0 = 2 * (g - first_block(pl)) + 1;   // ring fill of V_j: fill0 + 2 j
         const int s_b = s_n - jlo;                         // parity of S_j: (s_b + j) & 1
         float m_ref = -INFINITY;   // reference max, log2 units of scaled scores
-        float l = 0.f;
+        float l = 0.f;             // of this thread's keys
+        // A failed wait leaves the results unspecified.  Where a tile's warps meet
+        // at barriers the warp goes on to the unit's end all the same.
         for (int j = jlo; j < jhi; ++j) {
             const int k0 = j * kTileRows;
-            if (!mbar_wait_warp(&bar_s[t], (s_b + j) & 1, s_abort)) {
-                ok = false;
-                break;
-            }
+            ok = ok && mbar_wait_warp(&bar_s[t], (s_b + j) & 1, s_abort);
+            if (C::PARTS == 1 && !ok) break;
             tc_fence_after();
             // V rows outside [klo, khi) become zero.  Only after S_j: by then
             // every earlier fill of V_j's slot has been waited for, so that
@@ -534,12 +563,10 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             if (k0 < klo || k0 + kTileRows > khi) {
                 const int fill = fill0 + 2 * j;
                 const int slot = fill % C::NSLOT;
-                if (!mbar_wait_warp(&full[slot], (fill / C::NSLOT) & 1, s_abort)) {
-                    ok = false;
-                    break;
-                }
-                if (k0 + r < klo || k0 + r >= khi) {
-                    for (int cb = 0; cb < C::NCB; ++cb) {
+                ok = ok && mbar_wait_warp(&full[slot], (fill / C::NSLOT) & 1, s_abort);
+                if (C::PARTS == 1 && !ok) break;
+                if (ok && (k0 + r < klo || k0 + r >= khi)) {
+                    for (int cb = part; cb < C::NCB; cb += C::PARTS) {
                         const int at = kFine ? (r >> 3) * 8 * C::ROWB + cb * 1024 + (r & 7) * 128
                                               : cb * C::CB_BYTES + r * 128;
                         uint4* row = reinterpret_cast<uint4*>(sKV + slot * C::TILE + at);
@@ -553,47 +580,64 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                                          (!p.causal && k0 + kTileRows - 1 > first_pos + W - 1));
             const bool tile_mask = k0 + kTileRows > L ||
                                    (p.causal && k0 + kTileRows - 1 > first_pos) || wmask;
-            // columns >= lim and < lo of this row are masked (only on masked tiles)
-            int lim = tile_mask ? (p.causal ? min(L, pos + 1) : L) - k0 : kTileRows;
+            // keys >= lim and < lo of this thread's are masked (only on masked tiles)
+            int lim = tile_mask ? (p.causal ? min(L, pos + 1) : L) - k0 - c0 : C::NC;
             int lo = 0;
             if (wmask) {
-                lo = pos - W + 1 - k0;
-                if (!p.causal) lim = min(lim, pos + W - k0);
+                lo = pos - W + 1 - k0 - c0;
+                if (!p.causal) lim = min(lim, pos + W - k0 - c0);
             }
 
             // ---- row max ----
             float mx;
-            uint32_t sr[4][32];
+            uint32_t sr[C::NC / 32][32];
             {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(t_S + 32 * c, sr[c]);
+                for (int c = 0; c < C::NC / 32; ++c) tmem_ld32(t_S + 32 * c, sr[c]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) reg_fence(sr[c]);
+                for (int c = 0; c < C::NC / 32; ++c) reg_fence(sr[c]);
                 if (tile_mask) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
+                    for (int c = 0; c < C::NC; ++c)
                         if (c >= lim || c < lo) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
                 }
                 float mp[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 128; c += 2)
+                for (int c = 0; c < C::NC; c += 2)
                     mp[(c >> 1) & 7] = max3f(mp[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
                                              __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-                mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]),
-                           fmaxf(mp[6], mp[7]));
+                mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
             }
-            const float m_new = fmaxf(m_ref, mx * p.scale_log2);
-            const bool want = (m_ref != -INFINITY) && (m_new > m_ref + kRescaleThreshold);
-            const bool warp_rescale = __any_sync(0xffffffffu, want);
+            float m_new = fmaxf(m_ref, mx * p.scale_log2);
             float alpha = 1.f;
-            if (m_ref == -INFINITY) {
-                m_ref = m_new;   // O and l are still zero: adopt without rescaling
-            } else if (warp_rescale) {
-                alpha = ex2_approx(m_ref - m_new);
-                m_ref = m_new;
+            bool warp_rescale = false;
+            auto adopt = [&]() {
+                const bool want = (m_ref != -INFINITY) && (m_new > m_ref + kRescaleThreshold);
+                warp_rescale = __any_sync(0xffffffffu, want);
+                if (m_ref == -INFINITY) {
+                    m_ref = m_new;   // O and l are still zero: adopt without rescaling
+                } else if (warp_rescale) {
+                    alpha = ex2_approx(m_ref - m_new);
+                    m_ref = m_new;
+                }
+            };
+            if constexpr (C::PARTS == 1) {
+                adopt();
+            } else {
+                // The barrier that asks whether any row of the tile needs a new
+                // reference (its first keys, or a score 2^8 above the old one)
+                // is also what lets P overwrite S: all of it is read.
+                tc_fence_before();
+                if (named_barrier_or(bar, C::ROW_THREADS, m_new > m_ref + kRescaleThreshold)) {
+                    *x_mine = m_new;
+                    named_barrier_sync(bar, C::ROW_THREADS);
+                    m_new = fmaxf(m_new, *x_other);
+                    adopt();
+                }
+                tc_fence_after();
             }
             const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
 
@@ -605,7 +649,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc2[k] = f2_pack(0.f, 0.f);
 #pragma unroll
-            for (int c8 = 0; c8 < 8; ++c8) {   // 16 keys, 8 packed words
+            for (int c8 = 0; c8 < C::NC / 16; ++c8) {   // 16 keys, 8 packed words
                 uint32_t pk[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -620,7 +664,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                     pk[e] = pack_h2<kF16>(x0, x1);
                     acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(x0, x1));
                 }
-                tmem_st8(t_S + 8 * c8, pk);
+                tmem_st8(t_P + 8 * c8, pk);
             }
             float rowsum;
             {
@@ -632,7 +676,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             l = l * alpha + rowsum;
             if (warp_rescale && j > jlo) {   // O row *= alpha (PV of block j-1 is complete)
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < C::DC / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(t_O + 32 * c, o);
                     tmem_ld_wait();
@@ -654,6 +698,13 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
         }
         if (joined && p.cluster > 0)   // the ring and the queries are free once every product is done
             ok = mbar_wait_warp(bar_fin, 0, s_abort) && ok;
+        if constexpr (C::PARTS > 1) {   // the sum over all keys of the row
+            float* const sums = s_sum + (u_n & 1) * C::ROW_FLOATS + t * C::ROW_THREADS + r;
+            sums[part * kTileRows] = l;
+            ok = !named_barrier_or(bar, C::ROW_THREADS, !ok);
+            l = sums[0] + sums[kTileRows];
+            ++u_n;
+        }
         g += num_blocks(pl);
         s_n += jhi - jlo;
         o_n += any;
@@ -667,7 +718,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             const size_t out_row = (static_cast<size_t>(pl.start) + tok) * p.lq.H + head;
             uint32_t o[32];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < C::DC / 32; ++c) {
                 __syncwarp();   // rows past the tile's end skip the stores below
                 if (any) {
                     tmem_ld32(t_O + 32 * c, o);
@@ -680,18 +731,18 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
                 if (joined && p.cluster > 0) {
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
-                        *reinterpret_cast<float4*>(piece_group(t * kTileRows + r, 8 * c + v)) =
+                        *reinterpret_cast<float4*>(piece_group(t * kTileRows + r, part * (C::DC / 4) + 8 * c + v)) =
                             make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
                                         __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
                 } else if (row_ok && joined) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + piece_row * D + 32 * c);
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + piece_row * D + part * C::DC + 32 * c);
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
                         dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
                                              __uint_as_float(o[4 * v + 2]) * inv,
                                              __uint_as_float(o[4 * v + 3]) * inv);
                 } else if (row_ok) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + out_row * D + 32 * c);
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + out_row * D + part * C::DC + 32 * c);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint32_t w[4];
@@ -705,8 +756,8 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
             }
             const float lse2 = l == 0.f ? -INFINITY : m_ref + log2f(l);
             if (joined && p.cluster > 0) {
-                s_lse[t * kTileRows + r] = lse2;
-            } else if (row_ok) {
+                if (part == 0) s_lse[t * kTileRows + r] = lse2;
+            } else if (row_ok && part == 0) {
                 if (joined) p.part_lse[piece_row] = lse2;
                 else p.LSE[static_cast<size_t>(head) * p.lq.total + pl.start + tok] = lse2 * kLn2;
             }
@@ -733,7 +784,7 @@ __global__ void __launch_bounds__(FwdCfg<D, false, kF16, false, kTiles>::THREADS
 template <int D, bool kF16, int kTiles, bool kFine, bool kLoop>
 cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PagedParams& p, cudaStream_t stream) {
-    using C = FwdCfg<D, false, kF16, false, kTiles>;
+    using C = PagedCfg<D, kF16, kTiles>;
     auto kern = attn_paged_kernel<D, kF16, kTiles, kFine, kLoop>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
