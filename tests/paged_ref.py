@@ -79,6 +79,7 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None):
     Hkv = x.k_cache.shape[1]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     u = torch.finfo(x.q.dtype).eps / 2
+    tiny = torch.finfo(x.q.dtype).smallest_normal * u   # half a step below the normal numbers
     O = torch.zeros(T, H, d, dtype=torch.float64)
     tol = torch.zeros(T, H, d, dtype=torch.float64)
     lse = torch.full((H, T), -math.inf, dtype=torch.float64)
@@ -111,10 +112,15 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None):
             bound = (q.abs() @ k.abs().T * scale).masked_fill(~valid, 0.0).amax(1)
             e_s = (d + 8) * 2.0**-24 * bound + 2.0**-21
             # P rounds to the storage type for the product with V (u), fp32
-            # sums over L keys, O rounds once (u).
+            # sums over L keys, O rounds once (u).  Below the type's normal
+            # numbers (fp16: 2^-14) a rounding is off by up to half a step of
+            # the subnormals (2^-25), not by u of the value: of O once, of P for
+            # each attended key, whose sum it is divided by is at least 1 (the
+            # row's largest weight: a reference never exceeds the maximum).
+            below = tiny * (1 + valid.double() @ v.abs())
             e_o = u + 2 * e_s + (L + 64) * 2.0**-23
             O[t0:t1, h], lse[h, t0:t1] = o, z
-            tol[t0:t1, h] = A * (e_o * (1 + u))[:, None] + u * o.abs() + 2.0**-24 * u
+            tol[t0:t1, h] = A * (e_o * (1 + u))[:, None] + u * o.abs() + below
             lse_tol[h, t0:t1] = e_s + (L + 64) * 2.0**-24 + z.abs().nan_to_num(0, 0, 0) * 2.0**-22
     return O, lse, tol, lse_tol
 
