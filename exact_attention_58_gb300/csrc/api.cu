@@ -237,11 +237,12 @@ attn_status pre_impl(const void* O, const void* dO, const float* LSE, int B, con
                                     static_cast<cudaStream_t>(stream)));
 }
 
+// behind_preprocess: pre_impl was called just before on the same stream.
 attn_status main_impl(const void* Q, const void* K, const void* V, const void* dO, void* dK,
                       void* dV, int B, const SeqLayout& lq, const SeqLayout& lk, int d,
                       attn_dtype dtype, float scale, int causal, int window,
                       const int32_t* key_lens, float dropout_p, uint64_t seed, void* workspace,
-                      int* dev_status, void* stream) {
+                      bool behind_preprocess, int* dev_status, void* stream) {
     attn_status st = check_math(scale, dropout_p);
     if (st != ATTN_OK) return st;
     if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(dO) || !aligned16(dK) ||
@@ -278,13 +279,13 @@ attn_status main_impl(const void* Q, const void* K, const void* V, const void* d
     p.window = window > 0 ? window : 0;
     p.lq = lq;
     p.lk = lk;
+    const MainStream at{static_cast<cudaStream_t>(stream), behind_preprocess};
     if (d == 256)
         return from_cuda(launch_bwd_main_d256(tq, tk, tv, tdo, tdk, tdv, p,
                                               dtype == ATTN_DTYPE_FP16, causal != 0,
-                                              dropout_p > 0.f, static_cast<cudaStream_t>(stream)));
+                                              dropout_p > 0.f, at));
     return from_cuda(launch_bwd_main(tq, tk, tv, tdo, tdk, tdv, p, d, dtype == ATTN_DTYPE_FP16,
-                                     causal != 0, dropout_p > 0.f,
-                                     static_cast<cudaStream_t>(stream)));
+                                     causal != 0, dropout_p > 0.f, at));
 }
 
 attn_status convert_impl(void* dQ, int B, const SeqLayout& lq, int d, attn_dtype dtype,
@@ -311,7 +312,7 @@ attn_status bwd_impl(const void* Q, const void* K, const void* V, const void* O,
         return ATTN_ERR_MISALIGNED;
     if ((st = pre_impl(O, dO, LSE, B, lq, d, dtype, workspace, stream)) != ATTN_OK) return st;
     if ((st = main_impl(Q, K, V, dO, dK, dV, B, lq, lk, d, dtype, scale, causal, window, key_lens,
-                        dropout_p, seed, workspace, dev_status, stream)) != ATTN_OK)
+                        dropout_p, seed, workspace, true, dev_status, stream)) != ATTN_OK)
         return st;
     return convert_impl(dQ, B, lq, d, dtype, scale, workspace, stream);
 }
@@ -393,7 +394,7 @@ attn_status attn_bwd_main(const void* Q, const void* K, const void* V, const voi
     if ((st = check_keys(B, H, Nk, d)) != ATTN_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, B, H, N, d)) != ATTN_OK) return st;
     return main_impl(Q, K, V, dO, dK, dV, B, dense(H, N), dense(H, Nk), d, dtype, scale, causal,
-                     window, key_lens, dropout_p, seed, workspace, dev_status, stream);
+                     window, key_lens, dropout_p, seed, workspace, false, dev_status, stream);
 }
 
 attn_status attn_bwd_dq_convert(void* dQ, int B, int H, int N, int d, attn_dtype dtype,

@@ -194,7 +194,7 @@ cudaError_t launch_bwd_dq_convert(void* dQ, const float* dq_acc, int BH, const S
 cudaError_t launch_bwd_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
                             const BwdParams& p, int d, bool f16, bool causal, bool dropout,
-                            cudaStream_t stream) {
+                            MainStream stream) {
     if (p.lq.cu != nullptr)
         return launch_bwd_main_packed(tq, tk, tv, tdo, tdk, tdv, p, d, f16, causal, dropout, stream);
     if (d == 64)

@@ -9,7 +9,7 @@ cudaError_t launch_bwd_main_d256(const CUtensorMap& tq64, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const CUtensorMap& tdo64,
                                  const CUtensorMap& tdk, const CUtensorMap& tdv,
                                  const BwdParams& p, bool f16, bool causal, bool dropout,
-                                 cudaStream_t stream) {
+                                 MainStream stream) {
     if (p.lq.cu != nullptr)
         return f16 ? dispatch_bwd_d256<true, true>(tq64, tk, tv, tdo64, tdk, tdv, p, causal, dropout, stream)
                    : dispatch_bwd_d256<false, true>(tq64, tk, tv, tdo64, tdk, tdv, p, causal, dropout, stream);

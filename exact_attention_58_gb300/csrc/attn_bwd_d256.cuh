@@ -544,20 +544,21 @@ __global__ void __launch_bounds__(448, 1)
 template <bool kF16, bool kCausal, bool kDropout, bool kWindow, bool kPacked>
 cudaError_t launch_bwd_d256_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const CUtensorMap& tdk,
-                              const CUtensorMap& tdv, const BwdParams& p, cudaStream_t stream) {
+                              const CUtensorMap& tdv, const BwdParams& p, MainStream stream) {
     using C = Bwd256Cfg<kF16>;
     auto kern = attn_bwd_d256_kernel<kF16, kCausal, kDropout, kWindow, kPacked>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
     const unsigned grid = 2u * static_cast<unsigned>(p.nkb) * static_cast<unsigned>(p.B * p.H);
-    return launch_overlapped(kern, grid, C::THREADS, C::SMEM, stream, tq, tk, tv, tdo, tdk, tdv, p);
+    return launch_overlapped_cluster(kern, grid, C::THREADS, C::SMEM, 1, stream.behind_preprocess, stream.stream,
+                                     tq, tk, tv, tdo, tdk, tdv, p);
 }
 
 template <bool kF16, bool kPacked, bool kWindow>
 cudaError_t dispatch_bwd_d256_w(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                                const BwdParams& p, bool causal, bool dropout, cudaStream_t s) {
+                                const BwdParams& p, bool causal, bool dropout, MainStream s) {
     if (causal)
         return dropout ? launch_bwd_d256_t<kF16, true, true, kWindow, kPacked>(tq, tk, tv, tdo, tdk, tdv, p, s)
                        : launch_bwd_d256_t<kF16, true, false, kWindow, kPacked>(tq, tk, tv, tdo, tdk, tdv, p, s);
@@ -568,7 +569,7 @@ cudaError_t dispatch_bwd_d256_w(const CUtensorMap& tq, const CUtensorMap& tk, co
 template <bool kF16, bool kPacked>
 cudaError_t dispatch_bwd_d256(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                              const BwdParams& p, bool causal, bool dropout, cudaStream_t s) {
+                              const BwdParams& p, bool causal, bool dropout, MainStream s) {
     return p.window > 0
                ? dispatch_bwd_d256_w<kF16, kPacked, true>(tq, tk, tv, tdo, tdk, tdv, p, causal, dropout, s)
                : dispatch_bwd_d256_w<kF16, kPacked, false>(tq, tk, tv, tdo, tdk, tdv, p, causal, dropout, s);

@@ -746,20 +746,21 @@ __global__ void __launch_bounds__(448, 1)
 template <int D, bool kF16, bool kCausal, bool kDropout, bool kWindow, bool kPacked>
 cudaError_t launch_bwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                         const BwdParams& p, cudaStream_t stream) {
+                         const BwdParams& p, MainStream stream) {
     using C = BwdCfg<D, kF16>;
     auto kern = attn_bwd_kernel<D, kF16, kCausal, kDropout, kWindow, kPacked>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(p.nkb) * static_cast<unsigned>(p.B * p.H);
-    return launch_overlapped(kern, grid, C::THREADS, C::SMEM, stream, tq, tk, tv, tdo, tdk, tdv, p);
+    return launch_overlapped_cluster(kern, grid, C::THREADS, C::SMEM, 1, stream.behind_preprocess, stream.stream,
+                                     tq, tk, tv, tdo, tdk, tdv, p);
 }
 
 template <int D, bool kF16, bool kPacked, bool kWindow>
 cudaError_t dispatch_bwd_w(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                           const BwdParams& p, bool causal, bool dropout, cudaStream_t s) {
+                           const BwdParams& p, bool causal, bool dropout, MainStream s) {
     if (causal)
         return dropout ? launch_bwd_t<D, kF16, true, true, kWindow, kPacked>(tq, tk, tv, tdo, tdk, tdv, p, s)
                        : launch_bwd_t<D, kF16, true, false, kWindow, kPacked>(tq, tk, tv, tdo, tdk, tdv, p, s);
@@ -770,7 +771,7 @@ cudaError_t dispatch_bwd_w(const CUtensorMap& tq, const CUtensorMap& tk, const C
 template <int D, bool kF16, bool kPacked>
 cudaError_t dispatch_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                         const BwdParams& p, bool causal, bool dropout, cudaStream_t s) {
+                         const BwdParams& p, bool causal, bool dropout, MainStream s) {
     return p.window > 0
                ? dispatch_bwd_w<D, kF16, kPacked, true>(tq, tk, tv, tdo, tdk, tdv, p, causal, dropout, s)
                : dispatch_bwd_w<D, kF16, kPacked, false>(tq, tk, tv, tdo, tdk, tdv, p, causal, dropout, s);

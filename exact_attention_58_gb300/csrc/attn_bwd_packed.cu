@@ -9,7 +9,7 @@ cudaError_t launch_bwd_main_packed(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const CUtensorMap& tv, const CUtensorMap& tdo,
                                    const CUtensorMap& tdk, const CUtensorMap& tdv,
                                    const BwdParams& p, int d, bool f16, bool causal, bool dropout,
-                                   cudaStream_t stream) {
+                                   MainStream stream) {
     if (d == 64)
         return f16 ? dispatch_bwd<64, true, true>(tq, tk, tv, tdo, tdk, tdv, p, causal, dropout, stream)
                    : dispatch_bwd<64, false, true>(tq, tk, tv, tdo, tdk, tdv, p, causal, dropout, stream);

@@ -948,7 +948,7 @@ cudaError_t launch_decode_t(const CUtensorMap& tq, const CUtensorMap& tk, const 
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
-    return launch_overlapped_cluster(kern, static_cast<unsigned>(p.tiles), C::THREADS, C::SMEM, p.cluster, stream,
+    return launch_overlapped_cluster(kern, static_cast<unsigned>(p.tiles), C::THREADS, C::SMEM, p.cluster, true, stream,
                                      tq, tk, tv, p);
 }
 

@@ -791,7 +791,7 @@ cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
     if (e != cudaSuccess) return e;
     const unsigned units = static_cast<unsigned>(p.tiles) * static_cast<unsigned>(p.Hkv);
     const unsigned grid = kLoop ? (units < kSMs ? units : kSMs) : units * static_cast<unsigned>(p.splits);
-    return launch_overlapped_cluster(kern, grid, C::THREADS, C::SMEM, p.cluster, stream, tq, tk, tv, p);
+    return launch_overlapped_cluster(kern, grid, C::THREADS, C::SMEM, p.cluster, true, stream, tq, tk, tv, p);
 }
 
 // One unit per CTA or group of CTAs, or (p.splits = 1) a persistent CTA per SM.

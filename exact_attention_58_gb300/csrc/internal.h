@@ -89,9 +89,10 @@ cudaError_t enable_smem_per_device(Kernel kern, int bytes, std::atomic<unsigned 
 // Launch on `stream` with programmatic stream serialization, so that the
 // kernel's CTAs may start (and run up to their grid_dep_wait()) while the
 // kernel before it finishes; in clusters of `cluster` CTAs if that is > 1.
+// overlap = false: an ordinary launch, behind all that the stream holds.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_overlapped_cluster(void (*kern)(KArgs...), unsigned grid, unsigned block,
-                                      size_t smem, int cluster, cudaStream_t stream,
+                                      size_t smem, int cluster, bool overlap, cudaStream_t stream,
                                       Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -100,7 +101,7 @@ cudaError_t launch_overlapped_cluster(void (*kern)(KArgs...), unsigned grid, uns
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = overlap;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = 1;
@@ -112,7 +113,7 @@ cudaError_t launch_overlapped_cluster(void (*kern)(KArgs...), unsigned grid, uns
 template <typename... KArgs, typename... Args>
 cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
                               cudaStream_t stream, Args&&... args) {
-    return launch_overlapped_cluster(kern, grid, block, smem, 1, stream, std::forward<Args>(args)...);
+    return launch_overlapped_cluster(kern, grid, block, smem, 1, true, stream, std::forward<Args>(args)...);
 }
 
 // Tensor map of `rank` dimensions (innermost first; strides in bytes, one
@@ -164,6 +165,17 @@ cudaError_t launch_fwd_packed_1tile(const CUtensorMap& tq, const CUtensorMap& tk
                                     attn_dtype dtype, bool causal, bool dropout,
                                     cudaStream_t stream);
 
+// Where the backward's main kernel is launched.  It reads its inputs before
+// its grid_dep_wait(), which is safe right behind the preprocess (let in after
+// the preprocess's own wait) but not behind any kernel: one that writes those
+// inputs may let it in before its stores.  Called as a stage it is therefore
+// launched without overlap (forward and three stages: 2 x 2 x 200, d = 64, 16.1
+// -> 17.4 us; 4 x 16 x 4096, d = 128, 960 -> 956 us; attn_bwd as it was).
+struct MainStream {
+    cudaStream_t stream;
+    bool behind_preprocess;
+};
+
 // Backward launches (validated arguments only).
 // f16: the 16-bit tensors are IEEE half (else bf16).
 // lq: placement of the query rows (O, dO, LSE); the workspace is
@@ -175,20 +187,20 @@ cudaError_t launch_bwd_pre(const void* O, const void* dO, const float* LSE, floa
 cudaError_t launch_bwd_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
                             const BwdParams& p, int d, bool f16, bool causal, bool dropout,
-                            cudaStream_t stream);
+                            MainStream stream);
 // The main launch for packed sequences (p.lq.cu != nullptr).
 cudaError_t launch_bwd_main_packed(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const CUtensorMap& tv, const CUtensorMap& tdo,
                                    const CUtensorMap& tdk, const CUtensorMap& tdv,
                                    const BwdParams& p, int d, bool f16, bool causal, bool dropout,
-                                   cudaStream_t stream);
+                                   MainStream stream);
 // The main launch at head dim 256 (dense or packed by p.lq.cu): Q and dO maps
 // with 64-row boxes, the others with 128-row boxes.
 cudaError_t launch_bwd_main_d256(const CUtensorMap& tq64, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const CUtensorMap& tdo64,
                                  const CUtensorMap& tdk, const CUtensorMap& tdv,
                                  const BwdParams& p, bool f16, bool causal, bool dropout,
-                                 cudaStream_t stream);
+                                 MainStream stream);
 cudaError_t launch_bwd_dq_convert(void* dQ, const float* dq_acc, int BH, const SeqLayout& lq,
                                   int Npad, int d, bool f16, float scale, cudaStream_t stream);
 

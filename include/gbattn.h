@@ -74,8 +74,9 @@
  *             resident before the work ahead of it in the stream has
  *             finished, but no kernel touches a buffer before every earlier
  *             piece of work that may use it has finished (griddepcontrol
- *             .wait); the three backward stages overlap one another's
- *             start-up.
+ *             .wait).  Inside attn_bwd the main stage loads its inputs
+ *             while the preprocess runs; called by itself it starts behind all
+ *             work ahead of it.
  *  Errors     Argument errors are returned before anything is enqueued, with
  *             the outputs untouched.  A failed launch returns ATTN_ERR_CUDA.
  *             Errors detected on the device (a bounded wait that expired, an
