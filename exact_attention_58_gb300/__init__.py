@@ -527,9 +527,6 @@ def _native():
     return _native_module
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _int_tensor(name: str, t, dtype, shape, ref: torch.Tensor) -> int:
     """Pointer of a contiguous index tensor of the given type and shape on
     ref's device."""
@@ -574,7 +571,7 @@ def _call(fn, where: str, device: int, stream, *args):
     """fn(*args, stream) with `device` current: the library runs on the current
     device, and stream None is that device's current stream."""
     if stream is None:
-        handle = _raw_stream(device)
+        handle = torch._C._cuda_getCurrentRawStream(device)
     elif isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream
     else:
