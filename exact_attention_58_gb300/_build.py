@@ -86,6 +86,9 @@ def _build_binding() -> None:
            "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
+        for stale in (BINDING_STAMP, BINDING_PATH):   # of an older header, perhaps
+            if os.path.exists(stale):
+                os.remove(stale)
         raise RuntimeError(f"g++ failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING_PATH)
     with open(BINDING_STAMP, "w") as f:
@@ -94,14 +97,15 @@ def _build_binding() -> None:
 
 def build(verbose_ptxas: bool = False) -> str:
     """Compile every .cu under csrc/, link lib/libgbattn.so and build the
-    extension; returns the library's path."""
+    extension; returns the library's path.  An extension that does not compile
+    raises too, but only once the library stands: all but the paged-cache
+    functions work without it."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding.result()
     newest = max(os.path.getmtime(o) for o in objs)
     stamp_ok = os.path.exists(STAMP) and open(STAMP).read().strip() == MACHINE
     if not (stamp_ok and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest):
@@ -113,6 +117,7 @@ def build(verbose_ptxas: bool = False) -> str:
         os.replace(tmp, LIB_PATH)
         with open(STAMP, "w") as f:
             f.write(MACHINE)
+    binding.result()
     return LIB_PATH
 
 
