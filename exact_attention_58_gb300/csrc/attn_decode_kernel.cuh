@@ -10,8 +10,8 @@
 //     one key and N exponentials (not one row and 128 of them, of which only
 //     n / 128 would count), and O^T = V^T P^T keeps the head dim on the lanes.
 //     K and V are the 128-row operands, read from shared memory as they come.
-//   * The row maximum runs over lanes.  A row keeps its reference maximum
-//     until a score exceeds it by 2^8, which one barrier with a vote finds
+//   * The row maximum runs over lanes.  A row keeps its reference (its first
+//     block's maximum, for fp16 less 7) until a weight exceeds 2^8 (2^15), which one barrier with a vote finds
 //     out; only then are maxima reduced and O rescaled.  Row sums stay in
 //     each thread and are reduced once at the end.
 //   * One persistent CTA per SM.  The key blocks of all requests and heads, in
@@ -707,10 +707,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                         exponents(c, e);
                         mx = max3f(max3f(e[0], e[1], e[2]), max3f(e[3], e[4], e[5]), max3f(e[6], e[7], mx));
                     }
-                    grows = mx > kRescaleThreshold;
+                    grows = mx > kRescaleThreshold + kWeightShift<kF16>;
                 }
                 if (x == 0 || named_barrier_or(bar, 128, grows)) {
-                    // new reference maxima: over the warp's keys, then over the four warps
+                    // new references, from the maxima over the warp's keys, then over the four warps
                     float mine_max = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
@@ -721,8 +721,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     named_barrier_sync(bar, 128);
                     if (tid < NC) {
                         const float old = x > 0 ? -g_negm[tid] : kNoMax;
-                        const float mt = fmaxf(old, sc * fmaxf(fmaxf(g_row[tid], g_row[N + tid]),
-                                                               fmaxf(g_row[2 * N + tid], g_row[3 * N + tid])));
+                        const float mx = fmaxf(fmaxf(g_row[tid], g_row[N + tid]),
+                                               fmaxf(g_row[2 * N + tid], g_row[3 * N + tid]));
+                        const float mt = fmaxf(old, sc * mx - kWeightShift<kF16>);
                         g_negm[tid] = tid < rows ? -mt : -INFINITY;
                         g_fac[tid] = tid < rows ? ex2_approx(old - mt) : 0.f;
                     }

@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
         const int pos = first_pos + tl;
         const int fill0 = 2 * (g - first_block(pl)) + 1;   // ring fill of V_j: fill0 + 2 j
         const int s_b = s_n - jlo;                         // parity of S_j: (s_b + j) & 1
-        float m_ref = -INFINITY;   // reference max, log2 units of scaled scores
+        float m_ref = -INFINITY;   // reference, log2 units of scaled scores: a maximum less kWeightShift
         float l = 0.f;             // of this thread's keys
         // A failed wait leaves the results unspecified.  Where a tile's warps meet
         // at barriers the warp goes on to the unit's end all the same.
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
                                              __uint_as_float(sr[c >> 5][(c & 31) + 1]));
                 mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
             }
-            float m_new = fmaxf(m_ref, mx * p.scale_log2);
+            float m_new = fmaxf(m_ref, mx * p.scale_log2 - kWeightShift<kF16>);
             float alpha = 1.f;
             bool warp_rescale = false;
             auto adopt = [&]() {

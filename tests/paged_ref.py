@@ -72,9 +72,11 @@ def make_paged(q_lens, k_lens, H, Hkv, d, page, *, dtype=torch.bfloat16, seed=0,
                        max(1, max(q_lens)), keys, values)
 
 
-def ref_attention(x: PagedInputs, causal, window=0, scale=None):
+def ref_attention(x: PagedInputs, causal, window=0, scale=None, least=None):
     """O, LSE in 64 bits and the largest error that a kernel may have in each
-    element, for inputs that are exact in the storage type."""
+    element, for inputs that are exact in the storage type.  `least`: how far a
+    small weight may be off, relative to its row's largest (None: half a step
+    below the storage type's normal numbers, over a sum of weights of 1)."""
     T, H, d = x.q.shape
     Hkv = x.k_cache.shape[1]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
@@ -118,6 +120,9 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None):
             # each attended key, whose sum it is divided by is at least 1 (the
             # row's largest weight: a reference never exceeds the maximum).
             below = tiny * (1 + valid.double() @ v.abs())
+            if least is not None:   # over the sum of weights relative to the largest
+                share = torch.exp(S.amax(1, keepdim=True) - z[:, None]).nan_to_num(0.0)
+                below = tiny + least * share * (valid.double() @ v.abs())
             e_o = u + 2 * e_s + (L + 64) * 2.0**-23
             O[t0:t1, h], lse[h, t0:t1] = o, z
             tol[t0:t1, h] = A * (e_o * (1 + u))[:, None] + u * o.abs() + below
@@ -125,8 +130,8 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None):
     return O, lse, tol, lse_tol
 
 
-def check_attention(o, lse, x: PagedInputs, causal, window=0, scale=None):
-    O, L, tol, lse_tol = ref_attention(x, causal, window, scale)
+def check_attention(o, lse, x: PagedInputs, causal, window=0, scale=None, least=None):
+    O, L, tol, lse_tol = ref_attention(x, causal, window, scale, least)
     T = int(x.cu[-1])
     o, lse = o.detach().cpu().double(), lse.detach().cpu().double()
     over = (o - O).abs()[:T] - tol[:T]
@@ -137,3 +142,36 @@ def check_attention(o, lse, x: PagedInputs, causal, window=0, scale=None):
     assert torch.equal(none, lse[:, :T] == -math.inf), "rows without a key differ"
     d = torch.where(none, 0.0, lse[:, :T] - L[:, :T]).abs() - lse_tol[:, :T]
     assert bool((d <= 0).all()), f"LSE out of tolerance by {float(d.nan_to_num(9e9).max()):.3e}"
+
+
+# fp16 weights are rounded as multiples of 2^-7 of their row's largest and more:
+# the largest is at least 2^7, half a step of the subnormals 2^-25.
+FP16_LEAST = 2.0**-32
+
+
+def put_keys(x: PagedInputs, b, k, v):
+    """Gives request b other keys and values ([L, Hkv, d]), in cache and reference."""
+    page = x.k_cache.shape[2]
+    k, v = k.to(x.q.dtype), v.to(x.q.dtype)
+    x.keys[b], x.values[b] = k.double(), v.double()
+    for c in range(-(-k.shape[0] // page)):
+        m = min(page, k.shape[0] - c * page)
+        pg = int(x.page_table[b, c])
+        x.k_cache[pg, :, :m] = k[c * page:c * page + m].transpose(0, 1)
+        x.v_cache[pg, :, :m] = v[c * page:c * page + m].transpose(0, 1)
+
+
+def heavy_tail(n, L, heads, d, page, nats, *, every=128, seed=0, dtype=torch.float16):
+    """One request in which each `every`-th key outweighs the others by about `nats`
+    nats and has the value 0, theirs being 1: O is what the small weights add up
+    to, and the bound is relative to that."""
+    x = make_paged([n], [L], heads, 1, d, page, dtype=dtype, seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    sign = torch.randint(0, 2, (d,), generator=g) * 2.0 - 1.0
+    x.q = (sign + 0.02 * torch.randn(n, heads, d, generator=g)).to(dtype)
+    k = torch.randn(L, 1, d, generator=g) * 0.7
+    k[::every] = sign * (nats / math.sqrt(d))     # q . k / sqrt(d) = nats
+    v = torch.ones(L, 1, d)
+    v[::every] = 0.0
+    put_keys(x, 0, k, v)
+    return x
