@@ -97,7 +97,10 @@ Plan plan_one(int B, int H, int Hkv, int total_q, int max_q, long long max_keys,
     // With fewer CTAs than SMs the keys of a tile are shared out, as far as
     // all CTAs still run at once: over a cluster, or over more CTAs where that
     // saves more blocks than joining in a second launch costs (4, about 8 us).
-    // Where most requests have no tile, as far as one long request's do.
+    // Where most requests have no tile, as far as one long request's do, and always
+    // over a cluster (two CTAs a tile fit, and there are 48 blocks and more): the
+    // pieces' place in the workspace is the other launch's.
+    static_assert(kClusters[2] >= kSMs / 2, "tiles that could be split fit clusters of two");
     const long long ctas = (few > 0 ? total_q / cta_tokens + 1ll : t.tiles) * Hkv;
     t.splits = static_cast<int>(std::max(1ll, std::min(kSMs / ctas, blocks)));
     int cs = 8;
@@ -109,7 +112,6 @@ Plan plan_one(int B, int H, int Hkv, int total_q, int max_q, long long max_keys,
         return t;
     }
     t.rows = per_cta * kTileRows;
-    if (few > 0) t.splits = 1;   // (no cluster fits: the pieces' place is the other launch's)
     if (t.splits > 1) {
         t.descs = static_cast<size_t>(ctas);
         t.slots = t.descs * t.splits;
