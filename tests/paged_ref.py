@@ -79,22 +79,23 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None, least=None):
     below the storage type's normal numbers, over a sum of weights of 1)."""
     T, H, d = x.q.shape
     Hkv = x.k_cache.shape[1]
+    dev = x.keys[0].device
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     u = torch.finfo(x.q.dtype).eps / 2
     tiny = torch.finfo(x.q.dtype).smallest_normal * u   # half a step below the normal numbers
-    O = torch.zeros(T, H, d, dtype=torch.float64)
-    tol = torch.zeros(T, H, d, dtype=torch.float64)
-    lse = torch.full((H, T), -math.inf, dtype=torch.float64)
-    lse_tol = torch.zeros(H, T, dtype=torch.float64)
+    O = torch.zeros(T, H, d, dtype=torch.float64, device=dev)
+    tol = torch.zeros(T, H, d, dtype=torch.float64, device=dev)
+    lse = torch.full((H, T), -math.inf, dtype=torch.float64, device=dev)
+    lse_tol = torch.zeros(H, T, dtype=torch.float64, device=dev)
     cu = x.cu.tolist()
     for b, (K, V) in enumerate(zip(x.keys, x.values)):
         t0, t1 = cu[b], cu[b + 1]
         n, L = t1 - t0, K.shape[0]
         if n == 0 or L == 0:
             continue
-        p = torch.arange(n)[:, None] + L - n
-        j = torch.arange(L)[None, :]
-        valid = torch.ones(n, L, dtype=torch.bool)
+        p = torch.arange(n, device=dev)[:, None] + L - n
+        j = torch.arange(L, device=dev)[None, :]
+        valid = torch.ones(n, L, dtype=torch.bool, device=dev)
         if causal:
             valid &= j <= p
         if window > 0:
@@ -102,7 +103,7 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None, least=None):
             if not causal:
                 valid &= j - p < window
         for h in range(H):
-            q, k, v = x.q[t0:t1, h].double(), K[:, h // (H // Hkv)], V[:, h // (H // Hkv)]
+            q, k, v = x.q[t0:t1, h].double().to(dev), K[:, h // (H // Hkv)], V[:, h // (H // Hkv)]
             S = (q @ k.T * scale).masked_fill(~valid, -math.inf)
             z = torch.logsumexp(S, 1)
             P = torch.exp(S - torch.where(z == -math.inf, 0.0, z)[:, None])
@@ -133,7 +134,7 @@ def ref_attention(x: PagedInputs, causal, window=0, scale=None, least=None):
 def check_attention(o, lse, x: PagedInputs, causal, window=0, scale=None, least=None):
     O, L, tol, lse_tol = ref_attention(x, causal, window, scale, least)
     T = int(x.cu[-1])
-    o, lse = o.detach().cpu().double(), lse.detach().cpu().double()
+    o, lse = o.detach().to(O.device).double(), lse.detach().to(O.device).double()
     over = (o - O).abs()[:T] - tol[:T]
     assert bool((over <= 0).all()), (
         f"O off by {float((o - O).abs()[:T].nan_to_num(9e9).max()):.3e}, "
@@ -173,5 +174,25 @@ def heavy_tail(n, L, heads, d, page, nats, *, every=128, seed=0, dtype=torch.flo
     k[::every] = sign * (nats / math.sqrt(d))     # q . k / sqrt(d) = nats
     v = torch.ones(L, 1, d)
     v[::every] = 0.0
+    put_keys(x, 0, k, v)
+    return x
+
+
+def spread_keys(n, L, H, Hkv, d, page, *, seed=0, dtype=torch.bfloat16):
+    """One request whose every 128 keys hold one that some query row gives a large
+    share of its weight: with n x H / Hkv rows of a key head and L / 128 such keys
+    dealt out to them, losing or misplacing any 128 keys shows in a row."""
+    x = make_paged([n], [L], H, Hkv, d, page, dtype=dtype, seed=seed, sigma=0.3)
+    g = torch.Generator().manual_seed(seed + 1)
+    x.q = torch.randn(n, H, d, generator=g).to(dtype)
+    k, v = x.keys[0].clone(), x.values[0].clone()
+    G = H // Hkv
+    top = math.log(L) + 4     # in sum the other keys weigh e^-4 of one of these
+    for j in range(-(-L // 128)):
+        at = min(128 * j + int(torch.randint(0, 128, (1,), generator=g)), L - 1)
+        row = j % (n * G)
+        for hk in range(Hkv):
+            q = x.q[row // G, hk * G + row % G].double()
+            k[at, hk] = q * (top * math.sqrt(d) / float(q @ q))
     put_keys(x, 0, k, v)
     return x
