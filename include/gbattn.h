@@ -347,6 +347,9 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
  * attn_fwd_paged_workspace_size(...) bytes (16-byte aligned, contents on entry
  * do not matter; may be NULL when that is 0); calls that may overlap on the
  * GPU need one each.  One to three launches.
+ * Kernel and split are chosen from these sizes alone (so that a captured call
+ * can be replayed with other lengths), and max_pages * page_size stands for the
+ * longest context there: the result does not depend on it, the time can.
  */
 attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cache, void* O,
                            float* LSE, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
