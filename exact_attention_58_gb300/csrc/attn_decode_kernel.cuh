@@ -11,7 +11,8 @@
 //     n / 128 would count), and O^T = V^T P^T keeps the head dim on the lanes.
 //     K and V are the 128-row operands, read from shared memory as they come.
 //   * The row maximum runs over lanes.  A row keeps its reference (its first
-//     block's maximum, for fp16 less 7) until a weight exceeds 2^8 (2^15), which one barrier with a vote finds
+//     block's maximum, for fp16 less 7) until a weight exceeds 2^8 (2^15),
+//     which one barrier with a vote finds
 //     out; only then are maxima reduced and O rescaled.  Row sums stay in
 //     each thread and are reduced once at the end.
 //   * One persistent CTA per SM.  The key blocks of all requests and heads, in

@@ -29,8 +29,8 @@
 // products per key block (about 2 us for 256 rows x 128 keys at d = 128): whole
 // prompts of 4 x 16 x 4096, causal, d = 128, 246 us with other inputs from call to
 // call (1118 TFLOP/s; 233 to 240 us over and over on the same ones; the dense kernel
-// 225 to 233 either way); a chunk of 512 over 16100 keys, 16 heads, 72 us (950 TFLOP/s, 128 CTAs
-// of 33 blocks on 152 SMs).
+// 225 to 233 either way); a chunk of 512 over 16100 keys, 16 heads, 72 us (950
+// TFLOP/s, 128 CTAs of 33 blocks on 152 SMs).
 #pragma once
 
 #include "attn_fwd_kernel.cuh"

@@ -16,12 +16,12 @@ constexpr int kSMs = 152;
 constexpr long long kMaxPagedKeys = 1ll << 30;
 
 // Weights exp2(s - m) are rounded to the storage type for the product with V, m a
-// row's reference.  fp16 holds 2^-24 to just under 2^16, so m is put this far below the
-// row's maximum: with the 2^8 that a score may exceed a reference by, weights reach
-// 2^15, and the smallest that still count go from 2^-25 of the largest to 2^-32.  (Without it
-// 131072 keys 17 nats below the largest lost 0.4% of O: zero in the product, but not
-// in the sum, which takes weights unrounded.)  The factor cancels in O / l; LSE = m +
-// log2 l.  bf16 has the exponents of fp32 and needs none.
+// row's reference.  fp16 holds 2^-24 to just under 2^16, so m is put this far below
+// the row's maximum: with the 2^8 that a score may exceed a reference by, weights
+// reach 2^15, and the smallest that still count go from 2^-25 of the largest to
+// 2^-32.  (Without it 131072 keys 17 nats below the largest lost 0.4% of O: zero in
+// the product, but not in the sum, which takes weights unrounded.)  The factor
+// cancels in O / l; LSE = m + log2 l.  bf16 has the exponents of fp32 and needs none.
 template <bool kF16>
 constexpr float kWeightShift = kF16 ? 7.f : 0.f;   // log2 units
 

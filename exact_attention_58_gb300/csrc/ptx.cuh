@@ -195,12 +195,12 @@ __device__ __forceinline__ void bulk_wait_group_read_all() {
 // first access to memory a preceding kernel may still write or read.  Only
 // the backward's main kernel reads anything (its inputs) before that wait: it
 // is launched this way only right behind the preprocess, which signals its
-// dependents after its own wait.  The main and dQ-conversion
-// kernels signal at their start; the page-table, cache-append, decode and join
-// kernels after their wait and before they store anything; the forward and the
-// paged tile kernel not at all.  A signal says nothing about the signalling
-// kernel's stores, so whatever reads them has to wait first.  Without the
-// launch attribute both are no-ops.
+// dependents after its own wait.  The main and dQ-conversion kernels signal at
+// their start; the page-table, cache-append, decode and join kernels after
+// their wait and before they store anything; the forward and the paged tile
+// kernel not at all.  A signal says nothing about the signalling kernel's
+// stores, so whatever reads them has to wait first.  Without the launch
+// attribute both are no-ops.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

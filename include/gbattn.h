@@ -349,7 +349,8 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
  * GPU need one each.  One to three launches.
  * Kernel and split are chosen from these sizes alone (so that a captured call
  * can be replayed with other lengths), and max_pages * page_size stands for the
- * longest context there: the result does not depend on it, the time can.
+ * longest context there: the result depends on it by rounding only, the time
+ * can do so by much.
  */
 attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cache, void* O,
                            float* LSE, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
