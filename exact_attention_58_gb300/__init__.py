@@ -24,6 +24,16 @@ Serving from a paged key/value cache (bf16 or fp16, grouped query heads):
     ea.attn_cache_append(k, v, k_cache, v_cache, slots)
     o, lse = ea.attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu, max_seqlen_q,
                                causal=True)
+
+With rotary positions the step's append rotates too, and a cache of e4m3 values
+(torch.float8_e4m3fn) has float32 scales per page and head, powers of two:
+
+    q = ea.attn_cache_append_rope(q, k, v, k_cache, v_cache, slots, inv_freq,
+                                  cu_seqlens_q=cu, seq_lens=seq_lens)
+    q, k = ea.attn_rope(q, k, inv_freq, positions)
+    ea.attn_cache_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slots)
+    o, lse = ea.attn_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
+                                   cu, max_seqlen_q, causal=True)
 """
 from __future__ import annotations
 
@@ -43,7 +53,8 @@ __all__ = [
     "AttnError", "attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_preprocess",
     "attn_bwd_main", "attn_bwd_dq_convert", "attn_bwd_noalloc", "attn_fwd_varlen",
     "attn_bwd_varlen", "attn_page_table", "attn_cache_append", "attn_fwd_paged",
-    "attn_fwd_paged_workspace_size", "attn_selftest_wait", "attn_selftest_fwd_withheld", "attn_status_string",
+    "attn_fwd_paged_workspace_size", "attn_rope", "attn_rope_frequencies",
+    "attn_cache_append_rope", "attn_cache_append_fp8", "attn_fwd_paged_fp8", "attn_selftest_wait", "attn_selftest_fwd_withheld", "attn_status_string",
     "attn_version", "library",
     "LIB_PATH", "STATUS",
 ]
@@ -117,9 +128,17 @@ def library():
                                               [i64] * 3 + [vp, vp])
             lib.attn_fwd_paged.argtypes = ([vp] * 8 + [ip] * 10 + [i64] * 5 +
                                            [f, ip, ip, vp, sz, vp, vp])
+            lib.attn_rope.argtypes = [vp] * 6 + [ip] * 7 + [i64] * 13 + [f, ip, ip, vp]
+            lib.attn_cache_append_rope.argtypes = ([vp] * 11 + [ip] * 7 + [i64] * 6 + [ip] * 2 +
+                                                   [i64] * 3 + [f, ip, vp, vp])
+            lib.attn_cache_append_fp8.argtypes = ([vp] * 7 + [ip] * 4 + [i64] * 2 + [ip] * 2 +
+                                                  [i64] * 3 + [vp, vp])
+            lib.attn_fwd_paged_fp8.argtypes = ([vp] * 10 + [ip] * 10 + [i64] * 5 +
+                                               [f, ip, ip, vp, sz, vp, vp])
             lib.attn_fwd_paged_workspace_size.argtypes = [ip] * 8
             lib.attn_fwd_paged_workspace_size.restype = sz
-            for fn in ("attn_page_table", "attn_cache_append", "attn_fwd_paged",
+            for fn in ("attn_page_table", "attn_cache_append", "attn_fwd_paged", "attn_rope",
+                       "attn_cache_append_rope", "attn_cache_append_fp8", "attn_fwd_paged_fp8",
                        "attn_fwd", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main",
                        "attn_bwd_dq_convert", "attn_bwd_noalloc", "attn_fwd_varlen",
                        "attn_bwd_varlen"):
@@ -522,7 +541,8 @@ def _native():
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in
                       ("attn_page_table", "attn_cache_append", "attn_fwd_paged",
-                       "attn_fwd_paged_workspace_size")))
+                       "attn_fwd_paged_workspace_size", "attn_rope", "attn_cache_append_rope",
+                       "attn_cache_append_fp8", "attn_fwd_paged_fp8")))
         _native_module = module
     return _native_module
 
@@ -537,13 +557,14 @@ def _int_tensor(name: str, t, dtype, shape, ref: torch.Tensor) -> int:
     return t.data_ptr()
 
 
-def _cache_pair(k_cache, v_cache, d: int, ref: torch.Tensor):
+def _cache_pair(k_cache, v_cache, d: int, ref: torch.Tensor, dtype=None):
     """Sizes and strides of the caches: [num_pages, Hkv, page_size, d] views of
-    ref's dtype and device, d innermost, laid out alike."""
+    the given dtype (None: ref's) on ref's device, d innermost, laid out alike."""
+    dtype = ref.dtype if dtype is None else dtype
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if (not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype is not ref.dtype
+        if (not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype is not dtype
                 or t.get_device() != ref.get_device()):
-            raise ValueError(f"{name} must be [num_pages, Hkv, page_size, d], {ref.dtype}, on "
+            raise ValueError(f"{name} must be [num_pages, Hkv, page_size, d], {dtype}, on "
                              f"{ref.device}")
     shape, strides = k_cache.shape, k_cache.stride()
     if shape[3] != d or strides[3] != 1:
@@ -565,6 +586,17 @@ def _rows(name: str, t):
     if strides[2] != 1:
         raise ValueError(f"{name} must have d innermost (stride 1)")
     return t.shape, strides
+
+
+def _new_rows(k, v):
+    """Shape and strides of a step's k and v rows, which have to be laid out alike."""
+    shape, strides = _rows("k", k)
+    v_shape, v_strides = _rows("v", v)
+    if (v_shape != shape or v.dtype is not k.dtype or v.get_device() != k.get_device()
+            or (v_strides != strides
+                and any(n > 1 and x != y for n, x, y in zip(shape, strides, v_strides)))):
+        raise ValueError("v must match k in shape, strides, dtype and device")
+    return shape, strides
 
 
 def _call(fn, where: str, device: int, stream, *args):
@@ -661,13 +693,7 @@ def attn_cache_append(k, v, k_cache, v_cache, slots, *, dev_status=None, stream=
     if stream is None and (_native_module or _native()).cache_append(k, v, k_cache, v_cache, slots,
                                                                      dev_status):
         return
-    shape, strides = _rows("k", k)
-    v_shape, v_strides = _rows("v", v)
-    T, Hkv, d = shape
-    if (v_shape != shape or v.dtype is not k.dtype or v.get_device() != k.get_device()
-            or (v_strides != strides
-                and any(n > 1 and x != y for n, x, y in zip(shape, strides, v_strides)))):
-        raise ValueError("v must match k in shape, strides, dtype and device")
+    (T, Hkv, d), strides = _new_rows(k, v)
     pages, heads, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, k)
     if heads != Hkv:
         raise ValueError("the caches must have k's number of heads")
@@ -700,8 +726,18 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_
                                                        scale, out, lse, workspace, dev_status)
         if done is not None:
             return done
+    return _fwd_paged("attn_fwd_paged", q, k_cache, v_cache, None, page_table, seq_lens,
+                      cu_seqlens_q, max_seqlen_q, causal, window, scale, out, lse, workspace,
+                      dev_status, stream)
+
+
+def _fwd_paged(where, q, k_cache, v_cache, scales, page_table, seq_lens, cu_seqlens_q, max_seqlen_q,
+               causal, window, scale, out, lse, workspace, dev_status, stream):
+    """attn_fwd_paged, or with the scales of a cache of e4m3 attn_fwd_paged_fp8."""
     (total_q, H, d), strides = _rows("q", q)
-    pages, Hkv, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, q)
+    pages, Hkv, page_size, sp, sh, st = _cache_pair(
+        k_cache, v_cache, d, q, None if scales is None else torch.float8_e4m3fn)
+    scale_ptrs = () if scales is None else _scale_pair(*scales, pages, Hkv, q)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
     B, max_pages = page_table.shape
@@ -734,12 +770,217 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_
     else:
         _check_workspace(workspace, q)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _call(lib.attn_fwd_paged, "attn_fwd_paged", dev.index, stream, q.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), cu, lens, table, B, H, Hkv, total_q,
-          max_seqlen_q, pages, page_size, max_pages, d, _dtype_code(q), strides[0], strides[1], sp,
+    _call(getattr(lib, where), where, dev.index, stream, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), *scale_ptrs, out.data_ptr(), lse.data_ptr(), cu, lens, table, B, H, Hkv,
+          total_q, max_seqlen_q, pages, page_size, max_pages, d, _dtype_code(q), strides[0], strides[1], sp,
           sh, st, float(scale), int(bool(causal)), window, _ptr(workspace), ws_bytes,
           _ptr(dev_status))
     return out, lse
+
+
+def _scale_pair(k_scale, v_scale, pages: int, Hkv: int, ref: torch.Tensor):
+    """Pointers of the scales of a cache of e4m3."""
+    return tuple(_int_tensor(name, t, torch.float32, (pages, Hkv), ref)
+                 for name, t in (("k_scale", k_scale), ("v_scale", v_scale)))
+
+
+def attn_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens_q,
+                       max_seqlen_q: int, *, causal: bool = False, window: int = 0,
+                       scale: Optional[float] = None, out=None, lse=None, workspace=None,
+                       dev_status=None, stream=None):
+    """attn_fwd_paged over a cache of 8 bits: torch.float8_e4m3fn caches, whose
+    page and head stand for their values times k_scale and v_scale (float32 [num_pages,
+    Hkv], powers of two).  q and O are bf16 or fp16; see include/gbattn.h."""
+    if stream is None:
+        done = (_native_module or _native()).fwd_paged_fp8(
+            q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal, window,
+            scale, out, lse, workspace, dev_status, k_scale, v_scale)
+        if done is not None:
+            return done
+    return _fwd_paged("attn_fwd_paged_fp8", q, k_cache, v_cache, (k_scale, v_scale), page_table,
+                      seq_lens, cu_seqlens_q, max_seqlen_q, causal, window, scale, out, lse,
+                      workspace, dev_status, stream)
+
+
+def attn_cache_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slots, *, dev_status=None,
+                          stream=None):
+    """attn_cache_append into a cache of 8 bits (see attn_fwd_paged_fp8): each
+    page and head gets the smallest scale that holds its rows, and rows that it held
+    before are rounded again where that grows; see include/gbattn.h."""
+    if stream is None and (_native_module or _native()).cache_append_fp8(
+            k, v, k_cache, v_cache, slots, dev_status, k_scale, v_scale):
+        return
+    (T, Hkv, d), strides = _new_rows(k, v)
+    pages, heads, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, k, torch.float8_e4m3fn)
+    if heads != Hkv:
+        raise ValueError("the caches must have k's number of heads")
+    scales = _scale_pair(k_scale, v_scale, pages, Hkv, k)
+    at = _int_tensor("slots", slots, torch.int64, (T,), k)
+    _check_status(dev_status, k)
+    _on_gpu(k)
+    _call(library().attn_cache_append_fp8, "attn_cache_append_fp8", k.get_device(), stream,
+          k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *scales, at, T, Hkv, d,
+          _dtype_code(k), strides[0], strides[1], pages, page_size, sp, sh, st, _ptr(dev_status))
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def attn_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0,
+                          method: str = "linear", original_len: int = 0, fast: float = 32.0,
+                          slow: float = 1.0, device=None):
+    """(inv_freq, scaling) for attn_rope: float32 [rotary_dim / 2] and a number.
+    Frequencies base^(-2i / rotary_dim); for contexts `factor` times as long as
+    the original_len positions that a model was trained on they are
+      "linear"  divided by factor (positions interpolated);
+      "base"    those of the base times factor^(rotary_dim / (rotary_dim - 2)): the
+                highest stays, the lowest is divided by factor;
+      "parts"   kept where original_len positions make `fast` turns or more, divided
+                by factor where they make `slow` or fewer, and in between mixed
+                linearly over i; cosines and sines times 0.1 ln(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2 != 0:
+        raise ValueError("rotary_dim must be even and positive")
+    if not (base > 1.0 and math.isfinite(base) and factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    scaling = 1.0
+    if method == "base":
+        if rotary_dim < 4:
+            raise ValueError("the base method needs two frequencies")
+        base *= factor ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** (-i / rotary_dim)
+    if method == "linear":
+        freq = freq / factor
+    elif method == "parts":
+        if original_len < 1 or not fast > slow > 0.0:
+            raise ValueError("the parts method needs original_len and fast > slow > 0")
+        # index whose frequency makes `turns` turns in original_len positions
+        def index(turns):
+            return rotary_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotary_dim // 2 - 1)
+        mix = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        freq = freq * (1.0 - mix) + freq / factor * mix
+        scaling = 0.1 * math.log(factor) + 1.0
+    elif method != "base":
+        raise ValueError(f"unknown method {method!r}")
+    return freq.float().to(device), scaling
+
+
+def _rope_rows(name: str, t, ref: torch.Tensor):
+    """(B, heads, N, d) and the strides of batch, head and token of [B, heads, N,
+    d] or packed [tokens, heads, d] rows, d innermost."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4) or t.dim() != ref.dim():
+        raise ValueError(f"{name} must be [B, heads, N, d] or [tokens, heads, d], as q")
+    if t.dtype is not ref.dtype or t.get_device() != ref.get_device():
+        raise ValueError(f"{name} must match q in dtype and device")
+    n, s = t.shape, t.stride()
+    if s[-1] != 1:
+        raise ValueError(f"{name} must have d innermost (stride 1)")
+    if t.dim() == 3:
+        return (1, n[1], n[0], n[2]), (0, s[1], s[0])
+    return tuple(n), s[:3]
+
+
+def _rope_out(name: str, out, like: torch.Tensor, stream):
+    """The output given, or None's new tensor, and its strides."""
+    if out is None:
+        _on_gpu(like)
+        out = _empty(tuple(like.shape), like.dtype, like.device, stream)
+    elif not isinstance(out, torch.Tensor) or out.shape != like.shape:
+        raise ValueError(f"{name} must have its input's shape")
+    return out, _rope_rows(name, out, like)[1]
+
+
+def _inv_freq(t, ref: torch.Tensor):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError("inv_freq must be a float32 [rotary_dim / 2] tensor")
+    return _int_tensor("inv_freq", t, torch.float32, t.shape, ref), 2 * t.shape[0]
+
+
+def attn_rope(q, k, inv_freq, positions=None, *, interleaved: bool = False, inverse: bool = False,
+              scaling: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions: q [B, H, N, d] and k [B, Hk, N, d] (or packed [T, H, d] and
+    [T, Hk, d]; k may be None), d innermost, other strides free.  inv_freq: float32
+    [rotary_dim / 2]; positions: int32 [N], [B, N] or, packed, [T]; None: 0 .. N - 1
+    (not for packed rows).  inverse=True is the transposed map: gradients of q and k from those of
+    the results.  Returns (q_out, k_out); q_out=q works in place.  See include/gbattn.h."""
+    if stream is None:
+        done = (_native_module or _native()).rope(q, k, inv_freq, positions, interleaved, inverse,
+                                                  scaling, q_out, k_out)
+        if done is not None:
+            return done
+    if not isinstance(q, torch.Tensor):
+        raise ValueError("q must be a tensor")
+    (B, H, N, d), qs = _rope_rows("q", q, q)
+    freq, rotary_dim = _inv_freq(inv_freq, q)
+    Hk, ks = 0, (0, 0, 0)
+    if k is not None:
+        (kB, Hk, kN, kd), ks = _rope_rows("k", k, q)
+        if (kB, kN, kd) != (B, N, d):
+            raise ValueError("k must match q in all but the number of heads")
+        if Hk < 1:
+            raise ValueError("k has no heads")
+    pos, pos_batch = None, 0
+    if positions is not None:
+        rows = q.dim() == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 2
+        pos = _int_tensor("positions", positions, torch.int32, (B, N) if rows else (N,), q)
+        pos_batch = N if rows else 0
+    elif q.dim() == 3:
+        raise ValueError("packed rows need positions")
+    q_out, qo = _rope_out("q_out", q_out, q, stream)
+    ko = (0, 0, 0)
+    if k is not None:
+        k_out, ko = _rope_out("k_out", k_out, k, stream)
+    _on_gpu(q)
+    _call(library().attn_rope, "attn_rope", q.get_device(), stream, q.data_ptr(),
+          None if k is None else k.data_ptr(), q_out.data_ptr(),
+          None if k is None else k_out.data_ptr(), freq, pos, B, H, Hk, N, d, rotary_dim,
+          _dtype_code(q), *qs, *ks, *qo, *ko, pos_batch, float(scaling), int(bool(interleaved)),
+          int(bool(inverse)))
+    return q_out, (None if k is None else k_out)
+
+
+def attn_cache_append_rope(q, k, v, k_cache, v_cache, slots, inv_freq, positions=None, *,
+                           cu_seqlens_q=None, seq_lens=None, interleaved: bool = False,
+                           scaling: float = 1.0, q_out=None, dev_status=None, stream=None):
+    """attn_cache_append with rotary positions on the way: the rotated k ([T, Hkv, d])
+    and v go into the caches, and the rotated q ([T, H, d]) is returned (q_out=q works
+    in place).  positions: int32 [T], or cu_seqlens_q and seq_lens as attn_page_table
+    gives them.  See include/gbattn.h."""
+    if stream is None:
+        done = (_native_module or _native()).cache_append_rope(
+            q, k, v, k_cache, v_cache, slots, inv_freq, positions, cu_seqlens_q, seq_lens,
+            interleaved, scaling, q_out, dev_status)
+        if done is not None:
+            return done
+    (T, Hkv, d), strides = _new_rows(k, v)
+    (q_T, H, q_d), qs = _rows("q", q)
+    if q_T != T or q_d != d or q.dtype is not k.dtype or q.get_device() != k.get_device():
+        raise ValueError("q must match k in all but the number of heads")
+    pages, heads, page_size, sp, sh, st = _cache_pair(k_cache, v_cache, d, k)
+    if heads != Hkv:
+        raise ValueError("the caches must have k's number of heads")
+    at = _int_tensor("slots", slots, torch.int64, (T,), k)
+    freq, rotary_dim = _inv_freq(inv_freq, k)
+    pos = cu = lens = None
+    B = 0
+    if positions is not None:
+        pos = _int_tensor("positions", positions, torch.int32, (T,), k)
+    else:
+        if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+            raise ValueError("positions, or cu_seqlens_q and seq_lens, are needed")
+        B = seq_lens.shape[0]
+        lens = _int_tensor("seq_lens", seq_lens, torch.int32, (B,), k)
+        cu = _int_tensor("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), k)
+    _check_status(dev_status, k)
+    q_out, qo = _rope_out("q_out", q_out, q, stream)
+    _on_gpu(k)
+    _call(library().attn_cache_append_rope, "attn_cache_append_rope", k.get_device(), stream,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), at, freq, pos, cu, lens, B, T, H, Hkv, d, rotary_dim, _dtype_code(k),
+          qs[0], qs[1], strides[0], strides[1], qo[2], qo[1], pages, page_size, sp, sh, st,
+          float(scaling), int(bool(interleaved)), _ptr(dev_status))
+    return q_out
 
 
 def attn_selftest_wait(dev_status, *, arrive: bool, stream=None):

@@ -1,0 +1,39 @@
+// fp8.cuh — e4m3 values and the power-of-two scales of a cache that holds them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace gbattn {
+
+// Scales are 2^-48 to 2^48 (a float whose mantissa is zero): wide enough for any
+// activation, and weights of two blocks can be added up in fp32 whatever their scales.
+constexpr int kLeastScale = -48, kMostScale = 48;
+
+// Two e4m3 values (low byte first) to two fp16, which hold every e4m3 exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+    return r;
+}
+
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Exponent of a scale given by its bits (sign and mantissa ignored), within the range.
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+    return min(max(static_cast<int>((bits >> 23) & 0xffu) - 127, kLeastScale), kMostScale);
+}
+// A float that is not a power of two (or zero, as a cache never written to has).
+__device__ __forceinline__ bool bad_scale(uint32_t bits) {
+    return (bits & 0x807fffffu) != 0 || bits == 0x7f800000u;
+}
+
+// The smallest exponent e in range with x <= 448 2^e, x >= 0 given by its bits:
+// 448 = 1.75 x 2^8, so one more than x's own exponent less 8 where its mantissa exceeds 1.75.
+__device__ __forceinline__ int fit_exponent(uint32_t bits) {
+    return min(max(static_cast<int>((bits + 0x1fffffu) >> 23) - 135, kLeastScale), kMostScale);
+}
+
+}  // namespace gbattn

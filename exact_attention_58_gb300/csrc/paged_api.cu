@@ -14,10 +14,11 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 attn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
-// A stride in elements: positive, a multiple of 16 bytes, and below the 2^40
-// bytes that a tensor map can hold.  A dimension of one element has no stride.
-bool stride_ok(long long stride, long long extent) {
-    return extent == 1 || (stride > 0 && stride % 8 == 0 && stride < (1ll << 39));
+// A stride in elements of `es` bytes: positive, a multiple of 16 bytes, and below
+// the 2^40 bytes that a tensor map can hold.  A dimension of one element has no
+// stride.
+bool stride_ok(long long stride, long long extent, int es = 2) {
+    return extent == 1 || (stride > 0 && stride % (16 / es) == 0 && stride < (1ll << 40) / es);
 }
 
 // Whether [a, a + na) and [b, b + nb) share a byte.
@@ -26,9 +27,11 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// Shape of the cache and of what is read from or written to it.
+// Shape of the cache (of elements of `es` bytes) and of what is read from or
+// written to it (of type dtype).
 attn_status check_cache(int Hkv, int d, attn_dtype dtype, int num_pages, int page_size,
-                        long long page_stride, long long head_stride, long long token_stride) {
+                        long long page_stride, long long head_stride, long long token_stride,
+                        int es = 2) {
     if (Hkv < 1 || num_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
     if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP16)
         return dtype == ATTN_DTYPE_FP32 || dtype == ATTN_DTYPE_FP8_E4M3 ? ATTN_ERR_UNSUPPORTED
@@ -36,8 +39,8 @@ attn_status check_cache(int Hkv, int d, attn_dtype dtype, int num_pages, int pag
     if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
     if (page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<long long>(num_pages) * page_size >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
-    if (!stride_ok(page_stride, num_pages) || !stride_ok(head_stride, Hkv) ||
-        !stride_ok(token_stride, page_size))
+    if (!stride_ok(page_stride, num_pages, es) || !stride_ok(head_stride, Hkv, es) ||
+        !stride_ok(token_stride, page_size, es))
         return ATTN_ERR_MISALIGNED;
     return ATTN_OK;
 }
@@ -219,6 +222,105 @@ bool make_tmap_queries(CUtensorMap* map, const void* ptr, attn_dtype dtype, int 
     return encode_tmap(map, ptr, dtype, 3, dims, strides, box);
 }
 
+// attn_fwd_paged, or (with scales) attn_fwd_paged_fp8.
+attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, bool fp8, const float* k_scale,
+                      const float* v_scale, void* O, float* LSE, const int32_t* cu_seqlens_q,
+                      const int32_t* seq_lens, const int32_t* page_table, int B, int H, int H_kv, int total_q,
+                      int max_seqlen_q, int num_pages, int page_size, int max_pages, int d, attn_dtype dtype,
+                      long long q_token_stride, long long q_head_stride, long long cache_page_stride,
+                      long long cache_head_stride, long long cache_token_stride, float scale, int causal, int window,
+                      void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
+    if (!Q || !k_cache || !v_cache || !O || !LSE || !cu_seqlens_q || !seq_lens || !page_table ||
+        (fp8 && (!k_scale || !v_scale)))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status st = check_cache(H_kv, d, dtype, num_pages, page_size, cache_page_stride,
+                                 cache_head_stride, cache_token_stride, fp8 ? 1 : 2);
+    if (st != ATTN_OK) return st;
+    st = check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (!stride_ok(q_token_stride, total_q) || !stride_ok(q_head_stride, H)) return ATTN_ERR_MISALIGNED;
+    if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(O, 16) ||
+        !aligned(LSE, 16) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) ||
+        !aligned(page_table, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return ATTN_ERR_MISALIGNED;
+    const int max_q = std::min(max_seqlen_q, total_q);
+    const Plans plans = plan_paged(B, H, H_kv, total_q, max_q,
+                                   static_cast<long long>(max_pages) * page_size, d);
+    const size_t need = plans_bytes(plans, d);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
+    }
+    PagedParams p{};
+    p.O = O;
+    p.LSE = LSE;
+    p.seq_lens = seq_lens;
+    p.page_table = page_table;
+    p.dev_status = dev_status;
+    p.lq = SeqLayout{cu_seqlens_q, H, max_q, total_q};
+    p.B = B;
+    p.Hkv = H_kv;
+    p.G = H / H_kv;
+    p.few = plans.few;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.page_magic = (1ull << 62) / static_cast<unsigned long long>(page_size) + 1;
+    p.causal = causal != 0;
+    // a window of 2^30 keys is none: no two positions are that far apart
+    p.window = window > 0 && window < kMaxPagedKeys ? window : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const bool f16 = dtype == ATTN_DTYPE_FP16;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (fp8) {
+        const Fp8Cache c{Q, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale,
+                         v_scale, q_token_stride, q_head_stride, cache_page_stride, cache_head_stride,
+                         cache_token_stride};
+        return from_cuda(launch_paged_fp8(p, c, d, f16, s));
+    }
+    CUtensorMap tq[2], tk[2], tv[2];
+    PagedParams params[2];
+    for (int i = 0; i < plans.count; ++i) {   // all maps before the first launch
+        const Plan& t = plans.plan[i];
+        if (t.slots > 0) carve_pieces(p, workspace, t.slots, t.rows, t.descs);
+        p.box_rows = std::min(kTileRows, page_size & -page_size);
+        // More than 16 boxes of 64 columns a tile: 16 of 8 keys and all columns
+        // instead (the decode kernel issues K and V from two warps and has the time).
+        p.fine = !t.decode && kTileRows / p.box_rows * (d / 64) > 16;
+        if (p.fine) p.box_rows = 8;
+        p.tile_tokens = t.tile_tokens;
+        p.tiles = t.tiles;
+        p.tile_div = t.tile_div;
+        p.uniform_tiles = t.uniform;
+        p.splits = t.splits;
+        p.cluster = t.cluster;
+        p.slot_rows = t.rows;
+        params[i] = p;
+        if (!make_tmap_queries(&tq[i], Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
+                               p.tile_tokens) ||
+            !make_tmap_cache(&tk[i], k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+                             cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
+            !make_tmap_cache(&tv[i], v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+                             cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
+            return ATTN_ERR_CUDA;
+    }
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < plans.count && e == cudaSuccess; ++i) {
+        const Plan& t = plans.plan[i];
+        e = t.decode ? launch_paged_decode(tq[i], tk[i], tv[i], params[i], d, f16, s)
+                     : launch_paged_tiles(tq[i], tk[i], tv[i], params[i], d, f16, s);
+        if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
+            const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
+            // pieces of a tile in the mean: CTAs by tiles
+            const JoinKind kind = !t.decode ? kJoinMany
+                                  : static_cast<long long>(B) * H_kv <= 16 ? kJoinFewRows : kJoinFewPieces;
+            e = launch_paged_join(params[i], static_cast<int>(t.descs), rows, kind, d, f16, s);
+        }
+    }
+    return from_cuda(e);
+}
+
 }  // namespace
 }  // namespace gbattn
 
@@ -313,6 +415,43 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
     return from_cuda(launch_cache_append(p, static_cast<cudaStream_t>(stream)));
 }
 
+attn_status attn_cache_append_fp8(const void* K, const void* V, void* k_cache, void* v_cache,
+                                  float* k_scale, float* v_scale, const int64_t* slots, int T,
+                                  int H_kv, int d, attn_dtype dtype, int64_t token_stride,
+                                  int64_t head_stride, int num_pages, int page_size,
+                                  int64_t cache_page_stride, int64_t cache_head_stride,
+                                  int64_t cache_token_stride, int* dev_status, void* stream) {
+    if (!K || !V || !k_cache || !v_cache || !k_scale || !v_scale || !slots || T < 1) return ATTN_ERR_INVALID_ARG;
+    const attn_status st = check_cache(H_kv, d, dtype, num_pages, page_size, cache_page_stride,
+                                       cache_head_stride, cache_token_stride, 1);
+    if (st != ATTN_OK) return st;
+    if (static_cast<long long>(T) * H_kv >= (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
+    if (!stride_ok(token_stride, T) || !stride_ok(head_stride, H_kv)) return ATTN_ERR_MISALIGNED;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(slots, 8))
+        return ATTN_ERR_MISALIGNED;
+    AppendFp8Params p{};
+    p.x[0] = static_cast<const uint16_t*>(K);
+    p.x[1] = static_cast<const uint16_t*>(V);
+    p.cache[0] = static_cast<uint8_t*>(k_cache);
+    p.cache[1] = static_cast<uint8_t*>(v_cache);
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.slots = slots;
+    p.dev_status = dev_status;
+    p.T = T;
+    p.Hkv = H_kv;
+    p.d = d;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.cache_page_stride = cache_page_stride;
+    p.cache_head_stride = cache_head_stride;
+    p.cache_token_stride = cache_token_stride;
+    return from_cuda(launch_append_fp8(p, dtype == ATTN_DTYPE_FP16, static_cast<cudaStream_t>(stream)));
+}
+
 size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int max_seqlen_q,
                                      int max_pages, int page_size, int d) {
     if (check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d) != ATTN_OK)
@@ -331,88 +470,26 @@ attn_status attn_fwd_paged(const void* Q, const void* k_cache, const void* v_cac
                            int64_t cache_token_stride, float scale, int causal, int window,
                            void* workspace, size_t workspace_bytes, int* dev_status,
                            void* stream) {
-    if (!Q || !k_cache || !v_cache || !O || !LSE || !cu_seqlens_q || !seq_lens || !page_table)
-        return ATTN_ERR_INVALID_ARG;
-    attn_status st = check_cache(H_kv, d, dtype, num_pages, page_size, cache_page_stride,
-                                 cache_head_stride, cache_token_stride);
-    if (st != ATTN_OK) return st;
-    st = check_paged_shape(B, H, H_kv, total_q, max_seqlen_q, max_pages, page_size, d);
-    if (st != ATTN_OK) return st;
-    if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-    if (!stride_ok(q_token_stride, total_q) || !stride_ok(q_head_stride, H)) return ATTN_ERR_MISALIGNED;
-    if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(O, 16) ||
-        !aligned(LSE, 16) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) ||
-        !aligned(page_table, 4))
-        return ATTN_ERR_MISALIGNED;
-    const int max_q = std::min(max_seqlen_q, total_q);
-    const Plans plans = plan_paged(B, H, H_kv, total_q, max_q,
-                                   static_cast<long long>(max_pages) * page_size, d);
-    const size_t need = plans_bytes(plans, d);
-    if (need > 0) {
-        if (workspace == nullptr || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
-        if (!aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
-    }
-    PagedParams p{};
-    p.O = O;
-    p.LSE = LSE;
-    p.seq_lens = seq_lens;
-    p.page_table = page_table;
-    p.dev_status = dev_status;
-    p.lq = SeqLayout{cu_seqlens_q, H, max_q, total_q};
-    p.B = B;
-    p.Hkv = H_kv;
-    p.G = H / H_kv;
-    p.few = plans.few;
-    p.num_pages = num_pages;
-    p.page_size = page_size;
-    p.max_pages = max_pages;
-    p.page_magic = (1ull << 62) / static_cast<unsigned long long>(page_size) + 1;
-    p.causal = causal != 0;
-    // a window of 2^30 keys is none: no two positions are that far apart
-    p.window = window > 0 && window < kMaxPagedKeys ? window : 0;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    const bool f16 = dtype == ATTN_DTYPE_FP16;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    CUtensorMap tq[2], tk[2], tv[2];
-    PagedParams params[2];
-    for (int i = 0; i < plans.count; ++i) {   // all maps before the first launch
-        const Plan& t = plans.plan[i];
-        if (t.slots > 0) carve_pieces(p, workspace, t.slots, t.rows, t.descs);
-        p.box_rows = std::min(kTileRows, page_size & -page_size);
-        // More than 16 boxes of 64 columns a tile: 16 of 8 keys and all columns
-        // instead (the decode kernel issues K and V from two warps and has the time).
-        p.fine = !t.decode && kTileRows / p.box_rows * (d / 64) > 16;
-        if (p.fine) p.box_rows = 8;
-        p.tile_tokens = t.tile_tokens;
-        p.tiles = t.tiles;
-        p.tile_div = t.tile_div;
-        p.uniform_tiles = t.uniform;
-        p.splits = t.splits;
-        p.cluster = t.cluster;
-        p.slot_rows = t.rows;
-        params[i] = p;
-        if (!make_tmap_queries(&tq[i], Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
-                               p.tile_tokens) ||
-            !make_tmap_cache(&tk[i], k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
-                             cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
-            !make_tmap_cache(&tv[i], v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
-                             cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
-            return ATTN_ERR_CUDA;
-    }
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < plans.count && e == cudaSuccess; ++i) {
-        const Plan& t = plans.plan[i];
-        e = t.decode ? launch_paged_decode(tq[i], tk[i], tv[i], params[i], d, f16, s)
-                     : launch_paged_tiles(tq[i], tk[i], tv[i], params[i], d, f16, s);
-        if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
-            const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
-            // pieces of a tile in the mean: CTAs by tiles
-            const JoinKind kind = !t.decode ? kJoinMany
-                                  : static_cast<long long>(B) * H_kv <= 16 ? kJoinFewRows : kJoinFewPieces;
-            e = launch_paged_join(params[i], static_cast<int>(t.descs), rows, kind, d, f16, s);
-        }
-    }
-    return from_cuda(e);
+    return fwd_paged(Q, k_cache, v_cache, false, nullptr, nullptr, O, LSE, cu_seqlens_q, seq_lens, page_table, B, H,
+                     H_kv, total_q, max_seqlen_q, num_pages, page_size, max_pages, d, dtype, q_token_stride,
+                     q_head_stride, cache_page_stride, cache_head_stride, cache_token_stride, scale, causal, window,
+                     workspace, workspace_bytes, dev_status, stream);
+}
+
+attn_status attn_fwd_paged_fp8(const void* Q, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, void* O, float* LSE,
+                               const int32_t* cu_seqlens_q, const int32_t* seq_lens,
+                               const int32_t* page_table, int B, int H, int H_kv, int total_q,
+                               int max_seqlen_q, int num_pages, int page_size, int max_pages,
+                               int d, attn_dtype dtype, int64_t q_token_stride,
+                               int64_t q_head_stride, int64_t cache_page_stride,
+                               int64_t cache_head_stride, int64_t cache_token_stride, float scale,
+                               int causal, int window, void* workspace, size_t workspace_bytes,
+                               int* dev_status, void* stream) {
+    return fwd_paged(Q, k_cache, v_cache, true, k_scale, v_scale, O, LSE, cu_seqlens_q, seq_lens, page_table, B, H,
+                     H_kv, total_q, max_seqlen_q, num_pages, page_size, max_pages, d, dtype, q_token_stride,
+                     q_head_stride, cache_page_stride, cache_head_stride, cache_token_stride, scale, causal, window,
+                     workspace, workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,181 @@
+// paged_cache_fp8.cu — writing new rows into a paged key/value cache held in
+// e4m3, with one scale per page and head.
+#include "fp8.cuh"
+#include "paged_cache.h"
+#include "ptx.cuh"
+
+namespace gbattn {
+namespace {
+
+// A block (a page's rows of one head of K or V) stands for e4m3 x 2^e with the
+// smallest e for which its largest value fits, so rounding to e4m3's four
+// significant bits is the only rounding: the scale, a power of two, adds none.  New rows that
+// exceed what the block's scale can hold raise e: the rows that it held are
+// rounded again, by a power of two, which loses only what falls below e4m3's normal numbers.
+// A row written to a page's row 0 starts the block anew.
+//
+// A step's new rows of one page are a run of consecutive tokens.  A CTA takes the
+// runs that begin in its share of the tokens, for one head of K or V, one after
+// the other: it finds the run, the largest value (the rows stay in registers, as
+// far as they fit), the scale, and writes: one launch, no word between CTAs, and
+// no atomics.  Bound by memory for prompts; for single tokens, where each CTA has
+// one row, by the chain slot -> scale and row -> store.
+constexpr int kThreads = 128;
+constexpr int kKept = 8;   // 16-byte pieces of the run's rows that a thread keeps
+
+template <bool kF16>
+__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = h2lo_to_f32<kF16>(w[i]);
+        f[2 * i + 1] = h2hi_to_f32<kF16>(w[i]);
+    }
+}
+
+// 16 e4m3 values times `factor`, rounded again.
+__device__ __forceinline__ uint4 round_again(const uint4& v, float factor) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = e4m3x2_to_f16x2(w[i] & 0xffffu), hi = e4m3x2_to_f16x2(w[i] >> 16);
+        o[i] = pack_e4m3x4(f16lo_to_f32(lo) * factor, f16hi_to_f32(lo) * factor, f16lo_to_f32(hi) * factor,
+                           f16hi_to_f32(hi) * factor);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool kF16>
+__global__ void __launch_bounds__(kThreads) append_fp8_kernel(const AppendFp8Params p) {
+    grid_dep_wait();
+    grid_dep_launch_dependents();   // the next kernel sets itself up meanwhile
+    __shared__ int s_start[kThreads];   // runs found: their first tokens
+    __shared__ int s_count, s_len;
+    __shared__ uint32_t s_amax[kThreads / 32];
+    const int tid = static_cast<int>(threadIdx.x);
+    const int which = static_cast<int>(blockIdx.x & 1);   // K, V
+    const int unit = static_cast<int>(blockIdx.x >> 1);
+    const int tile = unit / p.Hkv, h = unit - tile * p.Hkv;
+    const long long slots_all = static_cast<long long>(p.num_pages) * p.page_size;
+    const unsigned size = static_cast<unsigned>(p.page_size);
+    const int t_end = static_cast<int>(min(static_cast<long long>(p.T), (tile + 1ll) * p.tile_tokens));
+    const int vecs = p.d / 8;                  // 16-byte pieces of a row
+    const int c = tid & (vecs - 1), r0 = tid / vecs, rows_at_once = kThreads / vecs;
+    const uint16_t* const src_head = p.x[which] + h * p.head_stride + 8 * c;
+    for (int base = tile * p.tile_tokens; base < t_end; base += kThreads) {
+        if (tid == 0) s_count = 0;
+        __syncthreads();
+        const int t = base + tid;
+        if (t < t_end) {
+            const long long slot = p.slots[t];
+            if (slot >= 0 && slot < slots_all) {
+                if (t == 0 || static_cast<unsigned>(slot) % size == 0 || p.slots[t - 1] != slot - 1)
+                    s_start[atomicAdd(&s_count, 1)] = t;
+            } else if (slot != -1 && p.dev_status != nullptr) {
+                // -1 marks a token without a slot; anything else out of range is an error
+                atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+            }
+        }
+        __syncthreads();
+        const int count = s_count;
+        for (int run = 0; run < count; ++run) {
+            const int first = s_start[run];
+            const unsigned slot = static_cast<unsigned>(p.slots[first]);
+            const unsigned page = slot / size;
+            const int row0 = static_cast<int>(slot - page * size);
+            const int room = min(static_cast<int>(size) - row0, p.T - first);
+            // ---- the run's length ----
+            int len = 0;
+            for (bool more = true; more;) {
+                if (tid == 0) s_len = room;
+                __syncthreads();
+                const int i = len + tid;
+                if (i < room && p.slots[first + i] != static_cast<long long>(slot) + i) atomicMin(&s_len, i);
+                __syncthreads();
+                more = s_len == room && len + kThreads < room;
+                len = more ? len + kThreads : s_len;
+                __syncthreads();
+            }
+            // ---- its largest value ----
+            const uint16_t* const src = src_head + first * p.token_stride;
+            uint4 kept[kKept];
+            float amax = 0.f;
+            auto grow = [&](const uint4& v) {
+                float f[8];
+                widen8<kF16>(v, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));   // (a NaN counts for nothing)
+            };
+#pragma unroll
+            for (int i = 0; i < kKept; ++i) {
+                const int r = r0 + i * rows_at_once;
+                if (r < len) kept[i] = *reinterpret_cast<const uint4*>(src + r * p.token_stride);
+            }
+#pragma unroll
+            for (int i = 0; i < kKept; ++i)
+                if (r0 + i * rows_at_once < len) grow(kept[i]);
+            for (int r = r0 + kKept * rows_at_once; r < len; r += rows_at_once)
+                grow(*reinterpret_cast<const uint4*>(src + r * p.token_stride));
+            const uint32_t warp_max = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+            if ((tid & 31) == 0) s_amax[tid >> 5] = warp_max;
+            __syncthreads();
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) top = max(top, s_amax[w]);
+            // ---- the scale ----
+            float* const scale = p.scale[which] + static_cast<size_t>(page) * p.Hkv + h;
+            int e = fit_exponent(top), old = kLeastScale;
+            if (row0 > 0) {
+                const uint32_t bits = __float_as_uint(*scale);
+                old = scale_exponent(bits);
+                if (bad_scale(bits) && tid == 0 && p.dev_status != nullptr)
+                    atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+                e = max(e, old);
+            }
+            __syncthreads();   // every thread has read the old one
+            if (tid == 0) *scale = exp2_int(e);
+            // ---- rows of the block before ----
+            uint8_t* const block = p.cache[which] + page * p.cache_page_stride + h * p.cache_head_stride;
+            if (row0 > 0 && e > old) {
+                const float factor = exp2_int(old - e);
+                const int per = p.d / 16;
+                for (int i = tid; i < row0 * per; i += kThreads) {
+                    const int r = i / per;
+                    uint4* at = reinterpret_cast<uint4*>(block + r * p.cache_token_stride + 16 * (i - r * per));
+                    *at = round_again(*at, factor);
+                }
+            }
+            // ---- the run's ----
+            const float inv = exp2_int(-e);
+            auto put = [&](const uint4& v, int r) {
+                float f[8];
+                widen8<kF16>(v, f);
+                const uint32_t lo = pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                const uint32_t hi = pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+                *reinterpret_cast<uint2*>(block + (row0 + r) * p.cache_token_stride + 8 * c) = make_uint2(lo, hi);
+            };
+#pragma unroll
+            for (int i = 0; i < kKept; ++i)
+                if (r0 + i * rows_at_once < len) put(kept[i], r0 + i * rows_at_once);
+            for (int r = r0 + kKept * rows_at_once; r < len; r += rows_at_once)
+                put(*reinterpret_cast<const uint4*>(src + r * p.token_stride), r);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_fp8(const AppendFp8Params& params, bool f16, cudaStream_t stream) {
+    AppendFp8Params p = params;
+    // Tokens of a CTA: one for a decoding step's few, up to a page of a prompt's many.
+    const long long want = static_cast<long long>(p.T) * p.Hkv * 2 / (152 * 8);
+    p.tile_tokens = static_cast<int>(want < 1 ? 1 : want > p.page_size ? p.page_size : want);
+    const long long tiles = (p.T - 1ll) / p.tile_tokens + 1;
+    const unsigned grid = static_cast<unsigned>(tiles * p.Hkv * 2);
+    return f16 ? launch_overlapped(append_fp8_kernel<true>, grid, kThreads, 0, stream, p)
+               : launch_overlapped(append_fp8_kernel<false>, grid, kThreads, 0, stream, p);
+}
+
+}  // namespace gbattn

@@ -371,6 +371,112 @@ size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int ma
                                      int max_pages, int page_size, int d);
 
 /*
+ * Rotary positions of queries and keys.  A pair (a, b) of the first rotary_dim
+ * elements of a row at position t becomes
+ *     (scaling (a cos w - b sin w), scaling (b cos w + a sin w)),  w = t inv_freq[i],
+ * for the pairs i = 0 .. rotary_dim / 2 - 1: elements i and i + rotary_dim / 2, or
+ * with interleaved != 0 elements 2 i and 2 i + 1.  The row's other elements are
+ * copied.  inverse != 0 turns by -w, with the same factor: the transposed map, which
+ * gives the gradient of the inputs from that of the outputs.  Long contexts scaled by
+ * interpolation, another base or by parts are other inv_freq; `scaling` is
+ * the factor that some of them put on cosine and sine (else 1).
+ *   Q, Q_out   [B, H, N, d], d innermost, any strides that are multiples of 16
+ *              bytes: dense tensors, packed tokens [T, H, d] (B = 1, N = T), slices of
+ *              a fused projection.  Strides of inputs may be 0 (a broadcast row).  The
+ *              stride of a dimension of extent 1 is ignored
+ *   K, K_out   [B, H_k, N, d], the same; not used when H_k = 0
+ *   inv_freq   float [rotary_dim / 2], finite
+ *   positions  int32, row n of batch entry b is at positions[b position_batch_stride
+ *              + n] (position_batch_stride 0: the same for all b); NULL: at n.  Any
+ *              value, negative ones too: an angle is off by at most |t| 2^-53 + 2^-25
+ *              turns, and its cosine and sine by 2^-20 (fp32: 2^-22)
+ * Q_out may be Q, and K_out K, with the same strides (in place); otherwise outputs
+ * overlap neither inputs nor one another.  bf16, fp16 or fp32; d in {64, 128, 256};
+ * rotary_dim a multiple of 16 up to d; N <= 2^30.  One launch.
+ */
+attn_status attn_rope(const void* Q, const void* K, void* Q_out, void* K_out, const float* inv_freq,
+                      const int32_t* positions, int B, int H, int H_k, int N, int d, int rotary_dim,
+                      attn_dtype dtype, int64_t q_batch_stride, int64_t q_head_stride,
+                      int64_t q_token_stride, int64_t k_batch_stride, int64_t k_head_stride,
+                      int64_t k_token_stride, int64_t q_out_batch_stride, int64_t q_out_head_stride,
+                      int64_t q_out_token_stride, int64_t k_out_batch_stride,
+                      int64_t k_out_head_stride, int64_t k_out_token_stride,
+                      int64_t position_batch_stride, float scaling, int interleaved, int inverse,
+                      void* stream);
+
+/*
+ * attn_cache_append with the rotation of attn_rope on the way: the rotated row t of
+ * K and row t of V go to slot slots[t], and the rotated row t of Q to row t of
+ * Q_out ([T, H, d], d innermost, the given strides; may be Q with the same strides).
+ *   positions     int32 [T], or NULL:
+ *   cu_seqlens_q  int32 [B + 1], seq_lens int32 [B], as attn_page_table leaves
+ *                 them: token t of request b stands at seq_lens[b] -
+ *                 cu_seqlens_q[b+1] + t.  Tokens behind the last request are left
+ *                 out, rows of Q_out included.  (Not used where positions is given,
+ *                 and all T rows of Q_out are then written.)
+ * Slots as in attn_cache_append (a token without a slot still has its Q rotated);
+ * a slot of a token behind the last request is reported as ATTN_ERR_INVALID_ARG.
+ * T >= 1; bf16 or fp16; d and rotary_dim as in attn_rope.  One launch.
+ */
+attn_status attn_cache_append_rope(const void* Q, const void* K, const void* V, void* Q_out,
+                                   void* k_cache, void* v_cache, const int64_t* slots,
+                                   const float* inv_freq, const int32_t* positions,
+                                   const int32_t* cu_seqlens_q, const int32_t* seq_lens, int B, int T,
+                                   int H, int H_kv, int d, int rotary_dim, attn_dtype dtype,
+                                   int64_t q_token_stride, int64_t q_head_stride,
+                                   int64_t kv_token_stride, int64_t kv_head_stride,
+                                   int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                   int num_pages, int page_size, int64_t cache_page_stride,
+                                   int64_t cache_head_stride, int64_t cache_token_stride,
+                                   float scaling, int interleaved, int* dev_status, void* stream);
+
+/*
+ * A paged cache held in 8 bits.  k_cache and v_cache are [num_pages, H_kv,
+ * page_size, d] arrays of e4m3 with strides as above (multiples of 16 elements), and
+ * k_scale and v_scale contiguous float [num_pages, H_kv] arrays: the block of a page
+ * and head stands for its e4m3 values times its scale, a power of two from 2^-48 to
+ * 2^48 (so that the scale adds no rounding).  The kernels go by a scale's exponent,
+ * clamped to that range; one that is no power of two is reported as
+ * ATTN_ERR_INVALID_ARG through dev_status.  0 counts as 2^-48 and is not reported.
+ *
+ * attn_cache_append_fp8 writes row t of K and V (bf16 or fp16, as in
+ * attn_cache_append) to slot slots[t], rounded to the nearest e4m3 number of the block's
+ * scale, ties to even.  The scale becomes the smallest one that holds all of the
+ * block's rows: those that this call writes, and the rows before the first of them,
+ * whose scale is the block's old one; where it grows, those rows are rounded again
+ * on the new one.  A row written to a page's row 0 starts the block
+ * anew: the old scale does not count.  Infinities, and values past 448 x 2^48, become
+ * the largest number; a NaN stays one.
+ * The slots of a page that one call names are one ascending run of consecutive rows at
+ * consecutive tokens, as attn_page_table makes them; what a page named by several runs
+ * holds afterwards is unspecified.  A slot of -1 is skipped, any other slot outside the
+ * cache skipped and reported.  No two requests may write to one page.
+ * T H_kv < 2^30.  One launch.
+ */
+attn_status attn_cache_append_fp8(const void* K, const void* V, void* k_cache, void* v_cache,
+                                  float* k_scale, float* v_scale, const int64_t* slots, int T,
+                                  int H_kv, int d, attn_dtype dtype, int64_t token_stride,
+                                  int64_t head_stride, int num_pages, int page_size,
+                                  int64_t cache_page_stride, int64_t cache_head_stride,
+                                  int64_t cache_token_stride, int* dev_status, void* stream);
+
+/*
+ * attn_fwd_paged over a cache held in 8 bits: Q and O in bf16 or fp16 (dtype is
+ * theirs), everything else as there, the workspace's size included.  Scales are read
+ * for the pages with a key that some query attends.
+ */
+attn_status attn_fwd_paged_fp8(const void* Q, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, void* O, float* LSE,
+                               const int32_t* cu_seqlens_q, const int32_t* seq_lens,
+                               const int32_t* page_table, int B, int H, int H_kv, int total_q,
+                               int max_seqlen_q, int num_pages, int page_size, int max_pages,
+                               int d, attn_dtype dtype, int64_t q_token_stride,
+                               int64_t q_head_stride, int64_t cache_page_stride,
+                               int64_t cache_head_stride, int64_t cache_token_stride, float scale,
+                               int causal, int window, void* workspace, size_t workspace_bytes,
+                               int* dev_status, void* stream);
+
+/*
  * Device self-test of the failure detection the kernels rely on: one warp
  * waits on an mbarrier with the same bounded wait (about 2 s of
  * %globaltimer) that every kernel uses.  arrive != 0: one thread arrives
