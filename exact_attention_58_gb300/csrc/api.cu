@@ -119,13 +119,14 @@ bool encode_3d(CUtensorMap* map, const void* ptr, attn_dtype dtype, const cuuint
 }  // namespace
 
 bool encode_tmap(CUtensorMap* map, const void* ptr, attn_dtype dtype, int rank,
-                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                 CUtensorMapSwizzle swizzle) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (enc == nullptr) return false;
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUresult r = enc(map, tmap_type(dtype), static_cast<cuuint32_t>(rank),
                            const_cast<void*>(ptr), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -42,36 +42,44 @@
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
+#include "fp8.cuh"
 #include "paged.cuh"
 
 namespace gbattn {
 namespace {
 
-template <int D, int N>
+template <int D, int N, bool kFp8>
 struct DecodeCfg {
     static constexpr int CHUNKS = D == 256 ? 2 : 1;          // ring slots of one tile
     static constexpr int CW = D / CHUNKS;                    // head-dim columns of a slot
-    static constexpr int CCB = CW / 64;                      // 128-byte column blocks of a slot
+    static constexpr int CCB = CW / 64;                      // 128-byte column blocks of a 16-bit chunk
     static constexpr int CB_BYTES = kTileRows * 128;
-    static constexpr int SLOT = CCB * CB_BYTES;
+    static constexpr int CHUNK = CCB * CB_BYTES;             // a chunk's bytes in 16 bits
+    static constexpr int SLOT = kFp8 ? CHUNK / 2 : CHUNK;    // and as loaded
     static constexpr int QCB_BYTES = N * 128;                // Q: column blocks of N rows
     static constexpr int Q_BYTES = (D / 64) * QCB_BYTES;
     static constexpr int P_BYTES = kTileRows * 128;          // P^T: 128 keys of up to 64 rows
-    static constexpr int MISC = 2944;                        // barriers, segments, row values
-    static constexpr int AVAIL = 232448 - MISC - 2 * Q_BYTES - 2 * P_BYTES;
+    static constexpr int MISC0 = 2944;                       // barriers, segments, row values
+    static constexpr int MISC = MISC0 + (kFp8 ? 3200 : 0);   // barriers, scales
+    static constexpr int WIDE = kFp8 ? 2 * CHUNK : 0;        // two chunks of V widened to fp16
+    static constexpr int AVAIL = 232448 - MISC - 2 * Q_BYTES - 2 * P_BYTES - WIDE;
     static constexpr int NSLOT = AVAIL / SLOT < 11 ? AVAIL / SLOT : 11;
     static constexpr int NK = (NSLOT + 1) / 2, NV = NSLOT / 2;   // K and V rings
-    static constexpr int SMEM = 2 * Q_BYTES + 2 * P_BYTES + NSLOT * SLOT + MISC;
+    static constexpr int SMEM = 2 * Q_BYTES + 2 * P_BYTES + NSLOT * SLOT + WIDE + MISC;
     static constexpr int HALVES = D == 256 ? 2 : 1;          // 128-lane halves of O^T
     static constexpr uint32_t O_COL = 2 * N;                 // S^T in [0, 2N), two buffers
-    static constexpr uint32_t TMEM_COLS = 4 * N;
+    static constexpr uint32_t K_COL = O_COL + HALVES * N;    // (fp8) two chunks of K widened to fp16
+    static constexpr uint32_t USED_COLS = K_COL + CW;
+    static constexpr uint32_t TMEM_COLS = !kFp8 ? 4 * N : USED_COLS <= 128 ? 128 : USED_COLS <= 256 ? 256 : 512;
     // Softmax warpgroups: with 32 or 64 rows two of them share the columns.
     static constexpr int GROUPS = N > 16 ? 2 : 1;
     static constexpr int NC = N / GROUPS;                    // columns of a thread
     static constexpr int K_WARP = 4 * GROUPS, V_WARP = K_WARP + 1, S_WARP = K_WARP + 2, PV_WARP = K_WARP + 3;
-    static constexpr int THREADS = 32 * (4 * GROUPS + 4);
-    static_assert(N * D * 4 <= NK * SLOT, "a cluster's piece fits the K ring");
-    static_assert(NV >= 2 && NV >= CHUNKS, "two slots a ring, and a tile");
+    static constexpr int K_CONV = 4 * GROUPS + 4, V_CONV = K_CONV + 4;   // (fp8) four warps each that widen
+    static constexpr int THREADS = 32 * (4 * GROUPS + (kFp8 ? 12 : 4));
+    static_assert(N * D * 4 <= (kFp8 ? WIDE : NK * SLOT), "a cluster's piece fits the widened V, or the K ring");
+    static_assert(kFp8 ? NV >= 1 : NV >= 2 && NV >= CHUNKS, "two slots a ring, and a tile");
+    static_assert(USED_COLS <= 512, "tensor memory");
 };
 
 // One tile's part of a CTA's run.
@@ -224,15 +232,17 @@ __device__ __forceinline__ bool walk_run(const PagedParams& p, const Run& run, i
     return true;
 }
 
-template <int D, bool kF16, int N>
-__global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
+template <int D, bool kF16, int N, bool kFp8>
+__global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-    using C = DecodeCfg<D, N>;
+    using C = DecodeCfg<D, N, kFp8>;
     constexpr int NC = C::NC;
     constexpr int kSoftmax = 128 * C::GROUPS;   // threads of the softmax warps
-    constexpr uint32_t FMT = fmt16<kF16>();
+    constexpr bool kMmaF16 = kF16 || kFp8;      // type of the products' operands
+    constexpr bool kTurnQ = kFp8 && !kF16;      // bf16 queries become fp16 times a power of two a row
+    constexpr uint32_t FMT = fmt16<kMmaF16>();
     constexpr uint32_t IDESC_S = idesc_f32acc(128, N, FMT, false, false);
     constexpr uint32_t IDESC_O = idesc_f32acc(128, N, FMT, true, true);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -246,7 +256,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     }
     uint8_t* sK = smem;                          // NK slots
     uint8_t* sV = sK + C::NK * C::SLOT;          // NV slots
-    uint8_t* sP = sV + C::NV * C::SLOT;          // two buffers
+    uint8_t* sW = sV + C::NV * C::SLOT;          // (fp8) two chunks of V in fp16
+    uint8_t* sP = sW + C::WIDE;                  // two buffers
     uint8_t* sQ = sP + 2 * C::P_BYTES;           // two buffers
     uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + 2 * C::Q_BYTES);
     uint64_t* q_full = bars;            // [2] a segment and its queries are there
@@ -269,10 +280,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     int* s_lo = reinterpret_cast<int*>(s_fac + N);         // [N] first key that a row attends,
     uint32_t* s_num = reinterpret_cast<uint32_t*>(s_lo + N);   // [N] and how many from there on
     float* s_lse = reinterpret_cast<float*>(s_num + N);        // [N] of a cluster's piece
-    long long* s_scan = reinterpret_cast<long long*>(s_lse + N);   // [18] set-up only
+    long long* s_scan = reinterpret_cast<long long*>(s_lse + N);   // [22] set-up only
     static_assert(C::NK <= 6 && C::NV <= 6, "ring barriers");
     static_assert(2 * sizeof(Segment) <= 12 * 8, "segments fit their place");
-    static_assert(50 * 8 + 9 * N * 4 + 18 * 8 <= C::MISC, "row values fit their place");
+    static_assert(50 * 8 + 9 * N * 4 + 22 * 8 <= C::MISC0, "row values fit their place");
+    // (fp8)
+    uint64_t* bars8 = bars + C::MISC0 / 8;
+    uint64_t* q_turned = bars8;         // [2] the queries are fp16
+    uint64_t* kt_full = bars8 + 2;      // [2] a chunk of K in tensor memory
+    uint64_t* kt_empty = bars8 + 4;
+    uint64_t* vt_full = bars8 + 6;      // [2] a chunk of V in fp16
+    uint64_t* vt_empty = bars8 + 8;
+    volatile int* s_vrows = reinterpret_cast<volatile int*>(bars8 + 10);   // [NV] rows of a V slot that hold keys: lo | hi << 8
+    float* s_qs = reinterpret_cast<float*>(bars8 + 13);           // [4][64] a segment's rows' powers of two
+    volatile float* s_scale = s_qs + 4 * 64;                      // [16 blocks][16 boxes][2] K's factor, V's exponent
+    static_assert(13 * 8 + 4 * 64 * 4 + 16 * 16 * 2 * 4 <= C::MISC - C::MISC0 || !kFp8, "scales fit their place");
     constexpr int kFirst = 1, kStop = 2;   // s_kind: O^T starts anew; no more blocks
 
     const int warp = threadIdx.x >> 5;
@@ -283,19 +305,26 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1 + kSoftmax);
+            mbar_init(&q_empty[s], 1 + kSoftmax + (kFp8 ? 128 : 0));
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], kSoftmax);
             mbar_init(&pv_done[s], 1);
             mbar_init(&bar_fin[s], 1);
         }
         for (int s = 0; s < C::NK; ++s) {
-            mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1);
+            mbar_init(&k_full[s], kFp8 ? 2 : 1);   // (the scales come a little later)
+            mbar_init(&k_empty[s], kFp8 ? 128 : 1);
         }
         for (int s = 0; s < C::NV; ++s) {
             mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], 1);
+            mbar_init(&v_empty[s], kFp8 ? 128 : 1);
+        }
+        for (int s = 0; s < 2 && kFp8; ++s) {
+            mbar_init(&q_turned[s], 128);
+            mbar_init(&kt_full[s], 128);
+            mbar_init(&kt_empty[s], 1);
+            mbar_init(&vt_full[s], 128);
+            mbar_init(&vt_empty[s], 1);
         }
         *s_abort = 0;
         fence_mbar_init();
@@ -333,7 +362,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     // to 32 requests their run, one request per lane (a microsecond less).
     const bool alone = p.cluster > 0 || p.B <= 32;
     if (!alone) {
-        long long* s_at = s_scan + 16;   // request that holds unit u0, and where it starts
+        long long* s_at = s_scan + 20;   // request that holds unit u0, and where it starts
         long long mine = 0, excl = 0;
         for (int b0 = 0; b0 < p.B; b0 += C::THREADS) {
             const int b = b0 + static_cast<int>(threadIdx.x);
@@ -368,8 +397,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     if (!alone && run.u0 < run.u1) {
-        run.b = static_cast<int>(s_scan[16]);
-        run.b_unit = s_scan[17];
+        run.b = static_cast<int>(s_scan[20]);
+        run.b_unit = s_scan[21];
     }
 
     // Calls body for every segment of the CTA: those of its run, or its even
@@ -421,6 +450,64 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 load_chunk(map, ring + slot * C::SLOT, &full[slot], box, bytes, c * C::CW, hk);
             }
             box = next;
+        }
+        return true;
+    };
+    // The same for 8-bit tiles.  With K's (keys) go the scales of its boxes' pages, K's
+    // with the softmax scale as a factor of the scores, V's as an exponent of the
+    // weights; the 16 blocks' worth of room is more than K runs ahead of the softmax
+    // (by the ring, two chunks in tensor memory and two of S^T).
+    int scaled = 0;   // blocks whose scales are there
+    auto load_tiles8 = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, int slots,
+                           int& fills, PageBox box, int b, const Request& r, int hk, int blk, int nblk, bool keys) {
+        if (r.khi <= r.klo) return true;
+        const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
+        const int jbeg = r.j0 + blk;
+        uint32_t kb = 0, vb = 0;
+        auto ask = [&](const PageBox& x) {
+            kb = vb = 127u << 23;
+            if (keys && x.needed && static_cast<unsigned>(x.page) < static_cast<unsigned>(p.num_pages)) {
+                const size_t at = static_cast<size_t>(x.page) * p.Hkv + hk;
+                kb = __float_as_uint(p.k_scale[at]);
+                vb = __float_as_uint(p.v_scale[at]);
+            }
+        };
+        ask(box);
+        for (int j = jbeg; j < jbeg + nblk; ++j) {
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
+                                   static_cast<uint32_t>(p.box_rows) * C::CW;
+            PageBox next{false, 0, 0};
+            if (j + 1 < jbeg + nblk) next = page_box(p, table, (j + 1) * kTileRows, r.klo, r.khi, lane);
+            for (int c = 0; c < C::CHUNKS; ++c, ++fills) {
+                const int slot = fills % slots;
+                if (!mbar_wait_warp_soon(&empty[slot], ((fills / slots) & 1) ^ 1, s_abort)) return false;
+                if (lane == 0) {
+                    if (!keys)
+                        s_vrows[slot] = max(0, r.klo - j * kTileRows) | min(kTileRows, r.khi - j * kTileRows) << 8;
+                    mbar_arrive_expect_tx(&full[slot], bytes);
+                }
+                __syncwarp();
+                if (box.needed)
+                    tma_load_4d(ring + slot * C::SLOT + lane * p.box_rows * C::CW, map, &full[slot], c * C::CW, box.row,
+                                hk, page_box_checked(p, box));
+                if (keys) {
+                    if (c == 0) {
+                        if (lane < 16) {
+                            volatile float* at = s_scale + ((scaled & 15) * 16 + lane) * 2;
+                            at[0] = exp2_int(scale_exponent(kb)) * p.scale_log2;
+                            at[1] = static_cast<float>(scale_exponent(vb));
+                        }
+                        ++scaled;
+                        if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
+                            atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[slot]);
+                }
+                __syncwarp();
+            }
+            box = next;
+            ask(box);
         }
         return true;
     };
@@ -497,7 +584,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             }
             __syncwarp();
             ++seg;
-            return load_tiles(&tmK, sK, k_full, k_empty, C::NK, fills, box, b, r, hk, blk, nblk);
+            if constexpr (kFp8)
+                return load_tiles8(&tmK, sK, k_full, k_empty, C::NK, fills, box, b, r, hk, blk, nblk, true);
+            else
+                return load_tiles(&tmK, sK, k_full, k_empty, C::NK, fills, box, b, r, hk, blk, nblk);
         });
         // no more segments
         bool told = false;
@@ -521,11 +611,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         // ================= producer of V =================
         if (lane == 0) tma_prefetch_desc(&tmV);
         int fills = 0;
-        each_segment([&](int b, const Request& r, int hk, int blk, int nblk, long long) {
-            return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk);
+        const bool ok = each_segment([&](int b, const Request& r, int hk, int blk, int nblk, long long) {
+            if constexpr (kFp8)
+                return load_tiles8(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk,
+                                   false);
+            else
+                return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk);
         });
         if (lane == 0) drain(v_full, C::NV, fills);
         __syncwarp();
+        if (kFp8 && ok && mbar_wait_warp(&v_empty[fills % C::NV], ((fills / C::NV) & 1) ^ 1, s_abort)) {
+            if (lane == 0) {   // no more tiles
+                s_vrows[fills % C::NV] = -1;
+                mbar_arrive(&v_full[fills % C::NV]);
+            }
+            __syncwarp();
+        }
     } else if (warp == C::S_WARP) {
         // ================= S^T = K Q^T =================
         if (lane == 0) {
@@ -536,7 +637,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             bool ok = true;
             for (int seg = 0; ok; ++seg) {
                 const int buf = seg & 1;
-                if (!mbar_wait(&q_full[buf], (seg >> 1) & 1, s_abort)) break;
+                if (!mbar_wait(kTurnQ ? &q_turned[buf] : &q_full[buf], (seg >> 1) & 1, s_abort)) break;
                 tc_fence_after();
                 const int nblk = s_seg[buf].nblk;
                 if (nblk == 0) break;
@@ -548,6 +649,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     // S^T's buffer is read once P^T of two blocks before is there
                     ok = blk < 2 || mbar_wait(&p_full[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
                     for (int c = 0; c < C::CHUNKS && ok; ++c, ++fill) {
+                        if constexpr (kFp8) {
+                            ok = mbar_wait(&kt_full[fill & 1], (fill >> 1) & 1, s_abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            for (int cb = 0; cb < C::CCB; ++cb)
+                                mma_run_ts_f16<4, 8, 2>(
+                                    tmem + (blk & 1) * N, tmem + C::K_COL + (fill & 1) * (C::CW / 2) + 32 * cb,
+                                    sdesc_adv(dq0, buf * C::Q_BYTES + (c * C::CCB + cb) * C::QCB_BYTES), IDESC_S,
+                                    c + cb > 0 ? 1u : 0u);
+                            if (c == C::CHUNKS - 1) tc_commit(&s_full[blk & 1]);
+                            tc_commit(&kt_empty[fill & 1]);
+                            continue;
+                        }
                         const int slot = fill % C::NK;
                         ok = mbar_wait(&k_full[slot], (fill / C::NK) & 1, s_abort);
                         if (!ok) break;
@@ -576,7 +690,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         if (lane == 0) {
             // V^T: 64 head-dim columns, the next 64 a column block on (for
             // d = 64 the same again: lanes 64-127 of O^T are not used)
-            const uint64_t dv0 = sdesc_sw128(smem_u32(sV), D == 64 ? 0 : C::CB_BYTES, 1024);
+            const uint64_t dv0 = sdesc_sw128(smem_u32(kFp8 ? sW : sV), D == 64 ? 0 : C::CB_BYTES, 1024);
+            constexpr int NVS = kFp8 ? 2 : C::NV;
+            uint64_t* const full = kFp8 ? vt_full : v_full;
+            uint64_t* const empty = kFp8 ? vt_empty : v_empty;
             const uint64_t dp0 = sdesc_sw128(smem_u32(sP), 16, 1024);
             int fill = 0;
             bool ok = true;
@@ -586,15 +703,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                 const int kind = s_kind[blk & 1];
                 if (kind == kStop) break;
                 for (int c = 0; c < C::CHUNKS; ++c, ++fill) {
-                    const int slot = fill % C::NV;
-                    ok = mbar_wait(&v_full[slot], (fill / C::NV) & 1, s_abort);
+                    const int slot = fill % NVS;
+                    ok = mbar_wait(&full[slot], (fill / NVS) & 1, s_abort);
                     if (!ok) break;
                     tc_fence_after();
                     mma8_ss_f16<128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128>(
-                        tmem + C::O_COL + c * N, sdesc_adv(dv0, slot * C::SLOT),
+                        tmem + C::O_COL + c * N, sdesc_adv(dv0, slot * C::CHUNK),
                         sdesc_adv(dp0, (blk & 1) * C::P_BYTES), IDESC_O, kind == kFirst ? 0u : 1u);
                     if (c == C::CHUNKS - 1) tc_commit(&pv_done[blk & 1]);
-                    tc_commit(&v_empty[slot]);
+                    tc_commit(&empty[slot]);
                 }
             }
             // Drain: no MMA of this warp is in flight at teardown.
@@ -603,6 +720,125 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             mbar_wait(&bar_fin[1], 0, &no_abort);
         }
         __syncwarp();
+    } else if (kFp8 && warp >= C::V_CONV) {
+        // ================= V from e4m3 to fp16 =================
+        // A thread takes 16 bytes of a row at a time.  Eight consecutive ones take 64
+        // head-dim columns of rows r and r ^ 5: their reads lie in opposite
+        // halves of the swizzled 128 bytes (at d = 64: in rows of unlike parity), and
+        // their two writes each in the even and the odd 16-byte groups: no two meet in a bank.
+        const int tid = static_cast<int>(threadIdx.x) - 32 * C::V_CONV;
+        const int cq = tid & 3, other = (tid & 4) ? 5 : 0;
+        for (int fill = 0;; ++fill) {
+            const int slot = fill % C::NV;
+            if (!mbar_wait_warp_soon(&v_full[slot], (fill / C::NV) & 1, s_abort)) break;
+            const int rows = s_vrows[slot];
+            if (rows < 0) break;
+            const int lo = rows & 255, hi = rows >> 8;
+            if (fill >= 2 && !mbar_wait_warp_soon(&vt_empty[fill & 1], ((fill >> 1) & 1) ^ 1, s_abort)) break;
+            const uint8_t* const raw = sV + slot * C::SLOT;
+            uint8_t* const wide = sW + (fill & 1) * C::CHUNK;
+#pragma unroll
+            for (int it = 0; it < C::CW / 16; ++it) {
+                const int x = it * 16 + (tid >> 3);
+                const int cb = C::CCB == 2 ? x & 1 : 0, y = C::CCB == 2 ? x >> 1 : x;
+                const int r = ((y >> 2) * 8 + (y & 3)) ^ other, c = 4 * cb + cq;
+                const uint4 v = *reinterpret_cast<const uint4*>(
+                    raw + r * C::CW + ((c ^ (C::CW == 128 ? r & 7 : (r >> 1) & 3)) << 4));
+                uint32_t w[8];
+                e4m3x16_to_f16(v, w);
+                if (r < lo || r >= hi) {   // outside what is attended: whatever is there, even NaN
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = 0u;
+                }
+                uint8_t* const dst = wide + cb * C::CB_BYTES + r * 128;
+                *reinterpret_cast<uint4*>(dst + (((2 * cq) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(dst + (((2 * cq + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            mbar_arrive_warp(&v_empty[slot]);
+            fence_proxy_async_smem();
+            mbar_arrive_warp(&vt_full[fill & 1]);
+        }
+    } else if (kFp8 && warp >= C::K_CONV) {
+        // ================= K from e4m3 to fp16, bf16 queries to fp16 =================
+        const int tid = static_cast<int>(threadIdx.x) - 32 * C::K_CONV;
+        const uint32_t t_K = tmem + C::K_COL + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int fill = 0;
+        bool ok = true;
+        for (int seg = 0; ok; ++seg) {
+            const int buf = seg & 1;
+            if (!mbar_wait_warp_soon(&q_full[buf], (seg >> 1) & 1, s_abort)) break;
+            const int nblk = s_seg[buf].nblk;
+            const bool none = s_seg[buf].none != 0;
+            if constexpr (kTurnQ) {
+                // A row's largest element goes to [2^14, 2^15): elements down to 2^-28 of
+                // it keep all bits, smaller ones are off by 2^-39 of it.
+                if (nblk > 0 && !none) {
+                    constexpr int TPR = 128 / N, PIECES = D / 8 / TPR;   // threads and 16-byte pieces of a row
+                    const int n = tid / TPR;
+                    auto piece = [&](int i) {
+                        const int c = tid % TPR + i * TPR;
+                        return reinterpret_cast<uint4*>(sQ + buf * C::Q_BYTES + (c >> 3) * C::QCB_BYTES + n * 128 +
+                                                        (((c & 7) ^ (n & 7)) << 4));
+                    };
+                    uint32_t top = 0;   // largest magnitude, as bf16 bits in either half
+#pragma unroll 4
+                    for (int i = 0; i < PIECES; ++i) {
+                        const uint4 v = *piece(i);
+                        top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    }
+                    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                    for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int ea = max(static_cast<int>(top >> 7) - 127, -100);
+                    const float up = exp2_int(14 - ea);
+                    // (four of them: the softmax, which has let go of the queries' buffer by
+                    // then, reads them while this warp may be two segments ahead)
+                    if (tid % TPR == 0) s_qs[(seg & 3) * 64 + n] = exp2_int(ea - 14);
+#pragma unroll 4
+                    for (int i = 0; i < PIECES; ++i) {
+                        uint4* const at = piece(i);
+                        const uint4 v = *at;
+                        auto turn = [&](uint32_t w) {
+                            return pack_f16x2(bf16lo_to_f32(w) * up, bf16hi_to_f32(w) * up);
+                        };
+                        *at = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+                    }
+                    fence_proxy_async_smem();
+                }
+                mbar_arrive_warp(&q_turned[buf]);
+            }
+            mbar_arrive_warp(&q_empty[buf]);
+            if (nblk == 0) break;
+            for (int x = 0; x < (none ? 0 : nblk * C::CHUNKS) && ok; ++x, ++fill) {
+                const int slot = fill % C::NK;
+                ok = mbar_wait_warp_soon(&k_full[slot], (fill / C::NK) & 1, s_abort);
+                if (ok && fill >= 2) ok = mbar_wait_warp_soon(&kt_empty[fill & 1], ((fill >> 1) & 1) ^ 1, s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                // a key per lane: 64 head-dim elements at a time
+#pragma unroll
+                for (int cb = 0; cb < C::CCB; ++cb) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = 4 * cb + i;
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            sK + slot * C::SLOT + tid * C::CW +
+                            ((c ^ (C::CW == 128 ? tid & 7 : (tid >> 1) & 3)) << 4));
+                        uint32_t h[8];
+                        e4m3x16_to_f16(v, h);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[8 * i + e] = h[e];
+                    }
+                    tmem_st32(t_K + (fill & 1) * (C::CW / 2) + 32 * cb, w);
+                }
+                mbar_arrive_warp(&k_empty[slot]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(&kt_full[fill & 1]);
+            }
+        }
     } else {
         // ================= softmax (one thread per key and group of columns) =================
         // The groups share nothing but the barriers: rows are columns here.
@@ -622,9 +858,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
         const int G = p.G;
         const float sc = p.scale_log2;
         const uint64_t sc2 = f2_pack(sc, sc);
+        const int box_shift = 31 - __clz(p.box_rows);
         // Pieces go to the workspace, or, in a cluster, to shared memory where
-        // the K ring was (this CTA's only segment is over by then).
-        float* const piece_o = p.cluster > 0 ? reinterpret_cast<float*>(sK) : p.part_o;
+        // the K ring (fp8: widened V) was (this CTA's only segment is over by then).
+        float* const piece_o = p.cluster > 0 ? reinterpret_cast<float*>(kFp8 ? sW : sK) : p.part_o;
         float* const piece_lse = p.cluster > 0 ? s_lse : p.part_lse;
         const int piece_rows = p.cluster > 0 ? N : p.slot_rows;
         int blk = 0;    // blocks so far, over all segments
@@ -688,15 +925,32 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     for (int n = 0; n < NC; ++n)
                         if (static_cast<uint32_t>(key - g_lo[n]) >= g_num[n]) sr[n] = __float_as_uint(-INFINITY);
                 }
+                // (fp8) The key's factor of its scores, and the exponent ev of its V's
+                // scale: weights are taken times 2^ev, references are of s + ev, and
+                // the sum takes 2^ev off again.
+                uint64_t f2 = 0, ev2 = 0, off2 = 0;
+                if constexpr (kFp8) {
+                    volatile const float* at = s_scale + ((blk & 15) * 16 + (tid >> box_shift)) * 2;
+                    const float f = at[0], ev = at[1];
+                    f2 = f2_pack(f, f);
+                    ev2 = f2_pack(ev, ev);
+                    const float off = exp2_int(-static_cast<int>(ev));
+                    off2 = f2_pack(off, off);
+                }
+                const uint64_t* const qs = reinterpret_cast<const uint64_t*>(s_qs + (seg & 3) * 64 + c0);
                 // Exponents s scale log2e - m, two rows at a time.  Rows past the
                 // tile's have m = inf: exponent -inf, weight 0.
+                auto exponent2 = [&](int n, uint64_t nm) {   // of rows n and n + 1, minus m given
+                    const uint64_t s2 = f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1]));
+                    if constexpr (!kFp8) return f2_fma(s2, sc2, nm);
+                    else if constexpr (kTurnQ) return f2_fma(f2_mul(s2, f2), qs[n / 2], f2_add(nm, ev2));
+                    else return f2_fma(s2, f2, f2_add(nm, ev2));
+                };
                 auto exponents = [&](int c, float (&e)[8]) {   // of rows 8 c .. 8 c + 7
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = 8 * c + 2 * i;
-                        const uint64_t nm = reinterpret_cast<const uint64_t*>(g_negm)[n / 2];
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1])), sc2, nm),
-                                  e[2 * i], e[2 * i + 1]);
+                        f2_unpack(exponent2(n, reinterpret_cast<const uint64_t*>(g_negm)[n / 2]), e[2 * i], e[2 * i + 1]);
                     }
                 };
                 bool grows = false;
@@ -708,14 +962,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                         exponents(c, e);
                         mx = max3f(max3f(e[0], e[1], e[2]), max3f(e[3], e[4], e[5]), max3f(e[6], e[7], mx));
                     }
-                    grows = mx > kRescaleThreshold + kWeightShift<kF16>;
+                    grows = mx > kRescaleThreshold + kWeightShift<kMmaF16>;
                 }
                 if (x == 0 || named_barrier_or(bar, 128, grows)) {
                     // new references, from the maxima over the warp's keys, then over the four warps
                     float mine_max = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
-                        const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(__uint_as_float(sr[n]))));
+                        float v = __uint_as_float(sr[n]);
+                        if constexpr (kFp8) {   // scaled already
+                            float lo, hi;
+                            f2_unpack(exponent2(n & ~1, f2_pack(0.f, 0.f)), lo, hi);
+                            v = n & 1 ? hi : lo;
+                        }
+                        const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(v)));
                         if (n == lane) mine_max = wm;
                     }
                     if (lane < NC) g_row[quarter * N + lane] = mine_max;
@@ -724,7 +984,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                         const float old = x > 0 ? -g_negm[tid] : kNoMax;
                         const float mx = fmaxf(fmaxf(g_row[tid], g_row[N + tid]),
                                                fmaxf(g_row[2 * N + tid], g_row[3 * N + tid]));
-                        const float mt = fmaxf(old, sc * mx - kWeightShift<kF16>);
+                        const float mt = fmaxf(old, (kFp8 ? mx : sc * mx) - kWeightShift<kMmaF16>);
                         g_negm[tid] = tid < rows ? -mt : -INFINITY;
                         g_fac[tid] = tid < rows ? ex2_approx(old - mt) : 0.f;
                     }
@@ -762,12 +1022,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
                     for (int i = 0; i < 4; ++i) {
                         const float p0 = ex2_approx(e[2 * i]);
                         const float p1 = ex2_approx(e[2 * i + 1]);
-                        l[4 * c + i] = f2_add(l[4 * c + i], f2_pack(p0, p1));
-                        w[i] = pack_h2<kF16>(p0, p1);
+                        if constexpr (kFp8) l[4 * c + i] = f2_fma(f2_pack(p0, p1), off2, l[4 * c + i]);
+                        else l[4 * c + i] = f2_add(l[4 * c + i], f2_pack(p0, p1));
+                        w[i] = pack_h2<kMmaF16>(p0, p1);
                     }
                     *reinterpret_cast<uint4*>(row + (((c0 / 8 + c) ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (cut) {
+                if (!kFp8 && cut) {
                     // V rows of keys outside [klo, khi) become zero.  Their slots'
                     // fills before this one must have landed, or the parity would
                     // be theirs: with a tile in two slots that takes P V of the
@@ -897,7 +1158,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
             for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             sum = __shfl_sync(0xffffffffu, sum, 0);
             constexpr int PER = D / 32;
-            const float* src = reinterpret_cast<const float*>(sK) + n * D + lane * PER;
+            const float* src = reinterpret_cast<const float*>(kFp8 ? sW : sK) + n * D + lane * PER;
             float2 x[8][PER / 2];   // all pieces' loads before the first is used
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -942,11 +1203,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, N>::THREADS, 1)
     if (blockIdx.x == 0) paged_report(p);
 }
 
-template <int D, bool kF16, int N>
+template <int D, bool kF16, int N, bool kFp8>
 cudaError_t launch_decode_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const PagedParams& p, cudaStream_t stream) {
-    using C = DecodeCfg<D, N>;
-    auto kern = attn_decode_kernel<D, kF16, N>;
+    using C = DecodeCfg<D, N, kFp8>;
+    auto kern = attn_decode_kernel<D, kF16, N, kFp8>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
@@ -954,13 +1215,13 @@ cudaError_t launch_decode_t(const CUtensorMap& tq, const CUtensorMap& tk, const 
                                      tq, tk, tv, p);
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kFp8 = false>
 cudaError_t launch_decode_n(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const PagedParams& p, cudaStream_t stream) {
     switch (p.slot_rows) {
-        case 16: return launch_decode_t<D, kF16, 16>(tq, tk, tv, p, stream);
-        case 32: return launch_decode_t<D, kF16, 32>(tq, tk, tv, p, stream);
-        case 64: return launch_decode_t<D, kF16, 64>(tq, tk, tv, p, stream);
+        case 16: return launch_decode_t<D, kF16, 16, kFp8>(tq, tk, tv, p, stream);
+        case 32: return launch_decode_t<D, kF16, 32, kFp8>(tq, tk, tv, p, stream);
+        case 64: return launch_decode_t<D, kF16, 64, kFp8>(tq, tk, tv, p, stream);
     }
     return cudaErrorInvalidValue;
 }

@@ -18,6 +18,17 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     return r;
 }
 
+// Sixteen e4m3 values to eight pairs of fp16.
+__device__ __forceinline__ void e4m3x16_to_f16(const uint4& v, uint32_t (&w)[8]) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(w[2 * i]), "=r"(w[2 * i + 1])
+            : "r"(x[i]));
+}
+
 // 2^e as a float, e in [-126, 127].
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 

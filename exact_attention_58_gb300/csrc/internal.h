@@ -117,9 +117,11 @@ cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned bl
 }
 
 // Tensor map of `rank` dimensions (innermost first; strides in bytes, one
-// fewer than dims), boxes of `box` elements, 128-byte swizzle, zeros outside.
+// fewer than dims), boxes of `box` elements, 128-byte swizzle unless given,
+// zeros outside.
 bool encode_tmap(CUtensorMap* map, const void* ptr, attn_dtype dtype, int rank,
-                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
+                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 // Tensor map over a contiguous [B*H][N][d] array, boxes of `rows` rows (128
 // unless given) and 128 bytes along d, 128-byte swizzle.  Returns false if the
 // driver rejected it.

@@ -42,6 +42,8 @@ struct PagedParams {
     float* LSE;                 // [H][total_q]
     const int32_t* seq_lens;    // [B] keys of each request, its new tokens included
     const int32_t* page_table;  // [B][max_pages]
+    const float* k_scale;       // [num_pages][Hkv] of a cache of e4m3, or nullptr
+    const float* v_scale;
     int* dev_status;
     SeqLayout lq;               // packed queries: cu, H, N = max_seqlen_q, total
     int B, Hkv, G;              // G = H / Hkv query heads read one key/value head
@@ -171,6 +173,13 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tk, co
 cudaError_t launch_paged_decode_d256(const CUtensorMap& tq, const CUtensorMap& tk,
                                      const CUtensorMap& tv, const PagedParams& p, bool f16,
                                      cudaStream_t stream);
+// The same over a cache of e4m3 (f16: type of Q and O).
+cudaError_t launch_paged_decode_fp8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    const PagedParams& p, int d, bool f16, cudaStream_t stream);
+cudaError_t launch_paged_decode_fp8_d128(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                         const PagedParams& p, bool f16, cudaStream_t stream);
+cudaError_t launch_paged_decode_fp8_d256(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                         const PagedParams& p, bool f16, cudaStream_t stream);
 cudaError_t launch_paged_fp8(const PagedParams& p, const Fp8Cache& c, int d, bool f16, cudaStream_t stream);
 // Joins the pieces of p.desc[0, descs), up to `rows` rows each.
 enum JoinKind {

@@ -186,12 +186,14 @@ attn_status check_paged_shape(int B, int H, int Hkv, int total_q, int max_q, int
 }
 
 // Tensor map over a cache [num_pages][Hkv][page_size][d] with any strides:
-// boxes of box_rows tokens and 64 columns, or (fine) of 8 tokens and all of d.
+// boxes of box_rows tokens and 64 columns (e4m3: 128, or all 64 in 64-byte rows),
+// or (fine) of 8 tokens and all of d.
 bool make_tmap_cache(CUtensorMap* map, const void* ptr, attn_dtype dtype, int num_pages, int Hkv,
                      int page_size, int d, long long page_stride, long long head_stride,
                      long long token_stride, int box_rows, bool fine) {
+    const bool fp8 = dtype == ATTN_DTYPE_FP8_E4M3;
     auto bytes = [&](long long stride, long long extent) {
-        return static_cast<cuuint64_t>(extent == 1 ? d : stride) * 2;
+        return static_cast<cuuint64_t>(extent == 1 ? d : stride) * (fp8 ? 1 : 2);
     };
     const cuuint64_t ts = bytes(token_stride, page_size), hs = bytes(head_stride, Hkv),
                      ps = bytes(page_stride, num_pages);
@@ -205,8 +207,9 @@ bool make_tmap_cache(CUtensorMap* map, const void* ptr, attn_dtype dtype, int nu
     }
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), rows, heads, pages};
     const cuuint64_t strides[3] = {ts, hs, ps};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
-    return encode_tmap(map, ptr, dtype, 4, dims, strides, box);
+    const cuuint32_t box[4] = {fp8 && d > 64 ? 128u : 64u, static_cast<cuuint32_t>(box_rows), 1, 1};
+    return encode_tmap(map, ptr, dtype, 4, dims, strides, box,
+                       fp8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tensor map over packed queries [total_q][H][d]: boxes of `tokens` tokens of
@@ -257,6 +260,8 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
     p.LSE = LSE;
     p.seq_lens = seq_lens;
     p.page_table = page_table;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
     p.dev_status = dev_status;
     p.lq = SeqLayout{cu_seqlens_q, H, max_q, total_q};
     p.B = B;
@@ -273,7 +278,7 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
     p.scale_log2 = scale * 1.4426950408889634f;
     const bool f16 = dtype == ATTN_DTYPE_FP16;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fp8) {
+    if (fp8 && !(plans.count == 1 && plans.plan[0].decode)) {
         const Fp8Cache c{Q, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale,
                          v_scale, q_token_stride, q_head_stride, cache_page_stride, cache_head_stride,
                          cache_token_stride};
@@ -287,7 +292,7 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
         p.box_rows = std::min(kTileRows, page_size & -page_size);
         // More than 16 boxes of 64 columns a tile: 16 of 8 keys and all columns
         // instead (the decode kernel issues K and V from two warps and has the time).
-        p.fine = !t.decode && kTileRows / p.box_rows * (d / 64) > 16;
+        p.fine = !t.decode && !fp8 && kTileRows / p.box_rows * (d / 64) > 16;
         if (p.fine) p.box_rows = 8;
         p.tile_tokens = t.tile_tokens;
         p.tiles = t.tiles;
@@ -299,16 +304,17 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
         params[i] = p;
         if (!make_tmap_queries(&tq[i], Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
                                p.tile_tokens) ||
-            !make_tmap_cache(&tk[i], k_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+            !make_tmap_cache(&tk[i], k_cache, fp8 ? ATTN_DTYPE_FP8_E4M3 : dtype, num_pages, H_kv, page_size, d, cache_page_stride,
                              cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
-            !make_tmap_cache(&tv[i], v_cache, dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+            !make_tmap_cache(&tv[i], v_cache, fp8 ? ATTN_DTYPE_FP8_E4M3 : dtype, num_pages, H_kv, page_size, d, cache_page_stride,
                              cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
             return ATTN_ERR_CUDA;
     }
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < plans.count && e == cudaSuccess; ++i) {
         const Plan& t = plans.plan[i];
-        e = t.decode ? launch_paged_decode(tq[i], tk[i], tv[i], params[i], d, f16, s)
+        e = t.decode && fp8 ? launch_paged_decode_fp8(tq[i], tk[i], tv[i], params[i], d, f16, s)
+            : t.decode ? launch_paged_decode(tq[i], tk[i], tv[i], params[i], d, f16, s)
                      : launch_paged_tiles(tq[i], tk[i], tv[i], params[i], d, f16, s);
         if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
             const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);

@@ -385,7 +385,7 @@ def test_append(dtype, d, page):
 
 def test_append_single_tokens():
     """Token by token through a page and into the next, as decoding does."""
-    append_and_check([([40 + i, 7 - i % 8 + 64], 2.0 ** (i % 5)) for i in range(30)], 2, 64, 8, 20, seed=1)
+    append_and_check([([40 + i, 7 - i % 8 + 144], 2.0 ** (i % 5)) for i in range(30)], 2, 64, 8, 20, seed=1)
 
 
 def test_append_many():
