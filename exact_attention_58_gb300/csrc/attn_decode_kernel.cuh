@@ -48,6 +48,62 @@
 namespace gbattn {
 namespace {
 
+// The kernel's waits.  Inlined polling loops are a third of its code.  Over a cache
+// of e4m3 four roles' loops run on every SM sub-partition and starve in its
+// instruction buffer, so there (kCall) polling is a function of its own: 48
+// requests of up to 4200 keys 95.6 -> 71.5 us.
+__device__ __forceinline__ bool try_wait_hint(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool poll_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__all_sync(0xffffffffu, try_wait_hint(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (__all_sync(0xffffffffu, try_wait_hint(bar, parity))) return true;
+        int give_up = (*abort != 0) || (elapsed_ns(t0) > static_cast<long long>(kWaitLimitNs));
+        give_up = __shfl_sync(0xffffffffu, give_up, 0);
+        if (give_up) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __noinline__ bool poll_one(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (try_wait_hint(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (try_wait_hint(bar, parity)) return true;
+        if (*abort) return false;
+        if (elapsed_ns(t0) > static_cast<long long>(kWaitLimitNs)) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+template <bool kCall>
+__device__ __forceinline__ bool wait_warp_soon(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if constexpr (!kCall) return mbar_wait_warp_soon(bar, parity, abort);
+    else return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || poll_warp(bar, parity, abort);
+}
+template <bool kCall>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if constexpr (!kCall) return mbar_wait_warp(bar, parity, abort);
+    else return poll_warp(bar, parity, abort);
+}
+template <bool kCall>
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if constexpr (!kCall) return mbar_wait(bar, parity, abort);
+    else return poll_one(bar, parity, abort);
+}
+
 template <int D, int N, bool kFp8>
 struct DecodeCfg {
     static constexpr int CHUNKS = D == 256 ? 2 : 1;          // ring slots of one tile
@@ -60,20 +116,24 @@ struct DecodeCfg {
     static constexpr int Q_BYTES = (D / 64) * QCB_BYTES;
     static constexpr int P_BYTES = kTileRows * 128;          // P^T: 128 keys of up to 64 rows
     static constexpr int MISC0 = 2944;                       // barriers, segments, row values
-    static constexpr int MISC = MISC0 + (kFp8 ? 3200 : 0);   // barriers, scales
-    static constexpr int WIDE = kFp8 ? 2 * CHUNK : 0;        // two chunks of V widened to fp16
-    static constexpr int AVAIL = 232448 - MISC - 2 * Q_BYTES - 2 * P_BYTES - WIDE;
+    static constexpr int MISC = MISC0 + (kFp8 ? 3328 : 0);   // barriers, scales
+    static constexpr int ROOM = 232448 - MISC - 2 * Q_BYTES - 2 * P_BYTES;
+    // (fp8) Chunks of V widened to fp16: three where that leaves five loads, so that
+    // the last blocks' are there when their weights are.
+    static constexpr int NW = ROOM - 3 * CHUNK >= 5 * SLOT ? 3 : 2;
+    static constexpr int WIDE = kFp8 ? NW * CHUNK : 0;
+    static constexpr int AVAIL = ROOM - WIDE;
     static constexpr int NSLOT = AVAIL / SLOT < 11 ? AVAIL / SLOT : 11;
     static constexpr int NK = (NSLOT + 1) / 2, NV = NSLOT / 2;   // K and V rings
     static constexpr int SMEM = 2 * Q_BYTES + 2 * P_BYTES + NSLOT * SLOT + WIDE + MISC;
     static constexpr int HALVES = D == 256 ? 2 : 1;          // 128-lane halves of O^T
     static constexpr uint32_t O_COL = 2 * N;                 // S^T in [0, 2N), two buffers
+    // Softmax warpgroups: with 32 or 64 rows (fp8: always) two of them share the columns.
+    static constexpr int GROUPS = N > 16 || kFp8 ? 2 : 1;
+    static constexpr int NC = N / GROUPS;                    // columns of a thread
     static constexpr uint32_t K_COL = O_COL + HALVES * N;    // (fp8) two chunks of K widened to fp16
     static constexpr uint32_t USED_COLS = K_COL + CW;
     static constexpr uint32_t TMEM_COLS = !kFp8 ? 4 * N : USED_COLS <= 128 ? 128 : USED_COLS <= 256 ? 256 : 512;
-    // Softmax warpgroups: with 32 or 64 rows two of them share the columns.
-    static constexpr int GROUPS = N > 16 ? 2 : 1;
-    static constexpr int NC = N / GROUPS;                    // columns of a thread
     static constexpr int K_WARP = 4 * GROUPS, V_WARP = K_WARP + 1, S_WARP = K_WARP + 2, PV_WARP = K_WARP + 3;
     static constexpr int K_CONV = 4 * GROUPS + 4, V_CONV = K_CONV + 4;   // (fp8) four warps each that widen
     static constexpr int THREADS = 32 * (4 * GROUPS + (kFp8 ? 12 : 4));
@@ -122,8 +182,8 @@ __device__ __forceinline__ int float_key(float x) {
 }
 __device__ __forceinline__ float key_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// Sums of v[0..N) over the warp, N = 16 or 32, scattered: after it, a lane holds
-// in v[0] the sum of the column returned (of N = 16, two lanes each).
+// Sums of v[0..N) over the warp, N = 8, 16 or 32, scattered: after it, a lane holds
+// in v[0] the sum of the column returned (32 / N neighbouring lanes each).
 template <int N>
 __device__ __forceinline__ int warp_sum_scatter(float (&v)[N], int lane) {
     int col = 0;
@@ -150,8 +210,9 @@ __device__ __forceinline__ int warp_sum_scatter(float (&v)[N], int lane) {
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t t, uint32_t (&r)[N]) {
-    static_assert(N == 16 || N == 32, "columns of a thread");
-    if constexpr (N == 16) tmem_ld16(t, r);
+    static_assert(N == 8 || N == 16 || N == 32, "columns of a thread");
+    if constexpr (N == 8) tmem_ld8(t, r);
+    else if constexpr (N == 16) tmem_ld16(t, r);
     else tmem_ld32(t, r);
 }
 
@@ -256,7 +317,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
     }
     uint8_t* sK = smem;                          // NK slots
     uint8_t* sV = sK + C::NK * C::SLOT;          // NV slots
-    uint8_t* sW = sV + C::NV * C::SLOT;          // (fp8) two chunks of V in fp16
+    uint8_t* sW = sV + C::NV * C::SLOT;          // (fp8) NW chunks of V in fp16
     uint8_t* sP = sW + C::WIDE;                  // two buffers
     uint8_t* sQ = sP + 2 * C::P_BYTES;           // two buffers
     uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + 2 * C::Q_BYTES);
@@ -289,12 +350,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
     uint64_t* q_turned = bars8;         // [2] the queries are fp16
     uint64_t* kt_full = bars8 + 2;      // [2] a chunk of K in tensor memory
     uint64_t* kt_empty = bars8 + 4;
-    uint64_t* vt_full = bars8 + 6;      // [2] a chunk of V in fp16
-    uint64_t* vt_empty = bars8 + 8;
-    volatile int* s_vrows = reinterpret_cast<volatile int*>(bars8 + 10);   // [NV] rows of a V slot that hold keys: lo | hi << 8
-    float* s_qs = reinterpret_cast<float*>(bars8 + 13);           // [4][64] a segment's rows' powers of two
+    uint64_t* vt_full = bars8 + 6;      // [NW] a chunk of V in fp16
+    uint64_t* vt_empty = bars8 + 9;
+    uint64_t* sc_full = bars8 + 12;     // [16] the scales of a block
+    volatile int* s_vrows = reinterpret_cast<volatile int*>(bars8 + 28);   // [NV] rows of a V slot that hold keys: lo | hi << 8
+    float* s_qs = reinterpret_cast<float*>(bars8 + 32);           // [4][64] a segment's rows' powers of two
     volatile float* s_scale = s_qs + 4 * 64;                      // [16 blocks][16 boxes][2] K's factor, V's exponent
-    static_assert(13 * 8 + 4 * 64 * 4 + 16 * 16 * 2 * 4 <= C::MISC - C::MISC0 || !kFp8, "scales fit their place");
+    static_assert(32 * 8 + 4 * 64 * 4 + 16 * 16 * 2 * 4 <= C::MISC - C::MISC0 || !kFp8, "scales fit their place");
     constexpr int kFirst = 1, kStop = 2;   // s_kind: O^T starts anew; no more blocks
 
     const int warp = threadIdx.x >> 5;
@@ -312,7 +374,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             mbar_init(&bar_fin[s], 1);
         }
         for (int s = 0; s < C::NK; ++s) {
-            mbar_init(&k_full[s], kFp8 ? 2 : 1);   // (the scales come a little later)
+            mbar_init(&k_full[s], 1);
             mbar_init(&k_empty[s], kFp8 ? 128 : 1);
         }
         for (int s = 0; s < C::NV; ++s) {
@@ -323,9 +385,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             mbar_init(&q_turned[s], 128);
             mbar_init(&kt_full[s], 128);
             mbar_init(&kt_empty[s], 1);
+        }
+        for (int s = 0; s < C::NW && kFp8; ++s) {
             mbar_init(&vt_full[s], 128);
             mbar_init(&vt_empty[s], 1);
         }
+        for (int s = 0; s < 16 && kFp8; ++s) mbar_init(&sc_full[s], 1);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -427,11 +492,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         }
         __syncwarp();
     };
-    // The boxes of a segment's first tile: asked for before anything else.
-    auto first_box = [&](int b, const Request& r, int blk) {
-        return page_box(p, p.page_table + static_cast<size_t>(b) * p.max_pages, (r.j0 + blk) * kTileRows, r.klo,
-                        r.khi, lane);
-    };
     // The K (or V) tiles of one segment through their ring.
     auto load_tiles = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty,
                           int slots, int& fills, PageBox box, int b, const Request& r, int hk, int blk,
@@ -446,77 +506,110 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             if (j + 1 < jbeg + nblk) next = page_box(p, table, (j + 1) * kTileRows, r.klo, r.khi, lane);
             for (int c = 0; c < C::CHUNKS; ++c, ++fills) {
                 const int slot = fills % slots;
-                if (!mbar_wait_warp_soon(&empty[slot], ((fills / slots) & 1) ^ 1, s_abort)) return false;
+                if (!wait_warp_soon<kFp8>(&empty[slot], ((fills / slots) & 1) ^ 1, s_abort)) return false;
                 load_chunk(map, ring + slot * C::SLOT, &full[slot], box, bytes, c * C::CW, hk);
             }
             box = next;
         }
         return true;
     };
-    // The same for 8-bit tiles.  With K's (keys) go the scales of its boxes' pages, K's
-    // with the softmax scale as a factor of the scores, V's as an exponent of the
-    // weights; the 16 blocks' worth of room is more than K runs ahead of the softmax
-    // (by the ring, two chunks in tensor memory and two of S^T).
-    int scaled = 0;   // blocks whose scales are there
+    // The same for 8-bit tiles.  A lane per box finds the pages of 32 boxes, two tiles
+    // and more, at a time: what is done for each tile stays short (tiles come
+    // twice as fast as of 16 bits, and a warp that runs now and then finds its code
+    // gone from the instruction buffer each time).  K's producer (keys) also gets
+    // the scales of the boxes' pages, K's with the softmax scale as a factor of
+    // the scores, V's as an exponent of the weights; it passes on a tile's behind the
+    // next tile's loads.  The 16 tiles' worth of room is more than K runs ahead of
+    // the softmax (by the ring, two chunks in tensor memory and two of S^T).
+    const int box_log = 31 - __clz(p.box_rows);
+    const int per_log = 7 - box_log;   // boxes of a tile
+    int scaled = 0;                    // tiles whose scales have been passed on
+    auto boxes8 = [&](int b, const Request& r, int j, int jend) {   // of tiles j, j + 1, ...
+        PageBox x{false, 0, 0};
+        const int key = j * kTileRows + lane * p.box_rows;
+        if (key < min(r.khi, jend * kTileRows) && key + p.box_rows > r.klo) {
+            x.needed = true;
+            const int col = static_cast<int>(__umul64hi(static_cast<unsigned long long>(key) << 2, p.page_magic));
+            x.row = key - col * p.page_size;
+            x.page = p.page_table[static_cast<size_t>(b) * p.max_pages + col];
+        }
+        return x;
+    };
     auto load_tiles8 = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, int slots,
-                           int& fills, PageBox box, int b, const Request& r, int hk, int blk, int nblk, bool keys) {
+                           int& fills, PageBox next, int b, const Request& r, int hk, int blk, int nblk, bool keys) {
         if (r.khi <= r.klo) return true;
-        const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
-        const int jbeg = r.j0 + blk;
+        const int jend = r.j0 + blk + nblk, tiles = 32 >> per_log;
+        const int mine = lane >> per_log, box = lane & ((1 << per_log) - 1);
         uint32_t kb = 0, vb = 0;
         auto ask = [&](const PageBox& x) {
-            kb = vb = 127u << 23;
+            kb = vb = 127u << 23;   // (of a box that is not loaded: any)
             if (keys && x.needed && static_cast<unsigned>(x.page) < static_cast<unsigned>(p.num_pages)) {
                 const size_t at = static_cast<size_t>(x.page) * p.Hkv + hk;
                 kb = __float_as_uint(p.k_scale[at]);
                 vb = __float_as_uint(p.v_scale[at]);
             }
         };
-        ask(box);
-        for (int j = jbeg; j < jbeg + nblk; ++j) {
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
-                                   static_cast<uint32_t>(p.box_rows) * C::CW;
-            PageBox next{false, 0, 0};
-            if (j + 1 < jbeg + nblk) next = page_box(p, table, (j + 1) * kTileRows, r.klo, r.khi, lane);
-            for (int c = 0; c < C::CHUNKS; ++c, ++fills) {
-                const int slot = fills % slots;
-                if (!mbar_wait_warp_soon(&empty[slot], ((fills / slots) & 1) ^ 1, s_abort)) return false;
-                if (lane == 0) {
-                    if (!keys)
-                        s_vrows[slot] = max(0, r.klo - j * kTileRows) | min(kTileRows, r.khi - j * kTileRows) << 8;
-                    mbar_arrive_expect_tx(&full[slot], bytes);
+        ask(next);
+#pragma unroll 1
+        for (int j0 = r.j0 + blk; j0 < jend; j0 += tiles) {
+            const PageBox x = next;
+            const int page = x.needed ? page_box_checked(p, x) : 0;
+            const unsigned needed = __ballot_sync(0xffffffffu, x.needed);
+            const float kf = exp2_int(scale_exponent(kb)) * p.scale_log2, ve = static_cast<float>(scale_exponent(vb));
+            if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
+                atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+            next = boxes8(b, r, j0 + tiles, jend);
+            const int n = min(tiles, jend - j0);
+            auto pass_on = [&](int t) {
+                if (mine == t) {
+                    volatile float* at = s_scale + ((scaled & 15) * 16 + box) * 2;
+                    at[0] = kf;
+                    at[1] = ve;
                 }
                 __syncwarp();
-                if (box.needed)
-                    tma_load_4d(ring + slot * C::SLOT + lane * p.box_rows * C::CW, map, &full[slot], c * C::CW, box.row,
-                                hk, page_box_checked(p, box));
-                if (keys) {
-                    if (c == 0) {
-                        if (lane < 16) {
-                            volatile float* at = s_scale + ((scaled & 15) * 16 + lane) * 2;
-                            at[0] = exp2_int(scale_exponent(kb)) * p.scale_log2;
-                            at[1] = static_cast<float>(scale_exponent(vb));
+                if (lane == 0) mbar_arrive(&sc_full[scaled & 15]);
+                ++scaled;
+            };
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                const uint32_t bytes = static_cast<uint32_t>(__popc(needed >> (t << per_log) & ((1u << (1 << per_log)) - 1u)))
+                                       << box_log;
+#pragma unroll 1
+                for (int c = 0; c < C::CHUNKS; ++c, ++fills) {
+                    const int slot = fills % slots;
+                    if (!wait_warp_soon<kFp8>(&empty[slot], ((fills / slots) & 1) ^ 1, s_abort)) return false;
+                    if (lane == 0) {
+                        if (!keys) {
+                            const int k0 = (j0 + t) * kTileRows;
+                            s_vrows[slot] = max(0, r.klo - k0) | min(kTileRows, r.khi - k0) << 8;
                         }
-                        ++scaled;
-                        if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
-                            atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+                        mbar_arrive_expect_tx(&full[slot], bytes * C::CW);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[slot]);
+                    if (mine == t && x.needed)
+                        tma_load_4d(ring + slot * C::SLOT + (box << box_log) * C::CW, map, &full[slot], c * C::CW, x.row,
+                                    hk, page);
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (keys && t > 0) pass_on(t - 1);
             }
-            box = next;
-            ask(box);
+            if (keys) pass_on(n - 1);
+            ask(next);
         }
         return true;
+    };
+    // The boxes of a segment's first tile: asked for before anything else.
+    auto first_box = [&](int b, const Request& r, int blk, int nblk) {
+        if constexpr (kFp8) return boxes8(b, r, r.j0 + blk, r.j0 + blk + nblk);
+        else return page_box(p, p.page_table + static_cast<size_t>(b) * p.max_pages, (r.j0 + blk) * kTileRows, r.klo,
+                        r.khi, lane);
     };
     // Every load of a ring has landed.
     auto drain = [&](uint64_t* full, int slots, int fills) {
         volatile int no_abort = 0;
         for (int s = 0; s < slots && s < fills; ++s) {
             const int uses = (fills - s + slots - 1) / slots;
-            mbar_wait(&full[s], (uses - 1) & 1, &no_abort);
+            wait_one<kFp8>(&full[s], (uses - 1) & 1, &no_abort);
         }
     };
 
@@ -546,8 +639,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         bool ok = each_segment([&](int b, const Request& r, int hk, int blk, int nblk,
                                                             long long u) {
             const int buf = seg & 1;
-            const PageBox box = first_box(b, r, blk);
-            if (seg >= 2 && !mbar_wait_warp_soon(&q_empty[buf], ((seg >> 1) & 1) ^ 1, s_abort)) return false;
+            const PageBox box = first_box(b, r, blk, nblk);
+            if (seg >= 2 && !wait_warp_soon<kFp8>(&q_empty[buf], ((seg >> 1) & 1) ^ 1, s_abort)) return false;
             if (lane == 0) {
                 const bool whole = nblk == r.units, none = r.khi <= r.klo;
                 volatile Segment& s = s_seg[buf];
@@ -591,7 +684,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         });
         // no more segments
         bool told = false;
-        if (ok && (seg < 2 || mbar_wait_warp(&q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, s_abort))) {
+        if (ok && (seg < 2 || wait_warp<kFp8>(&q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, s_abort))) {
             if (lane == 0) {
                 s_seg[seg & 1].nblk = 0;
                 mbar_arrive(&q_full[seg & 1]);
@@ -603,7 +696,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         // its barrier has moved on).
         if (lane == 0) {
             volatile int no_abort = 0;
-            for (int s = max(0, seg - (told ? 1 : 2)); s < seg; ++s) mbar_wait(&q_full[s & 1], (s >> 1) & 1, &no_abort);
+            for (int s = max(0, seg - (told ? 1 : 2)); s < seg; ++s) wait_one<kFp8>(&q_full[s & 1], (s >> 1) & 1, &no_abort);
             drain(k_full, C::NK, fills);
         }
         __syncwarp();
@@ -613,14 +706,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         int fills = 0;
         const bool ok = each_segment([&](int b, const Request& r, int hk, int blk, int nblk, long long) {
             if constexpr (kFp8)
-                return load_tiles8(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk,
+                return load_tiles8(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk, nblk), b, r, hk, blk, nblk,
                                    false);
             else
-                return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk), b, r, hk, blk, nblk);
+                return load_tiles(&tmV, sV, v_full, v_empty, C::NV, fills, first_box(b, r, blk, nblk), b, r, hk, blk, nblk);
         });
         if (lane == 0) drain(v_full, C::NV, fills);
         __syncwarp();
-        if (kFp8 && ok && mbar_wait_warp(&v_empty[fills % C::NV], ((fills / C::NV) & 1) ^ 1, s_abort)) {
+        if (kFp8 && ok && wait_warp<kFp8>(&v_empty[fills % C::NV], ((fills / C::NV) & 1) ^ 1, s_abort)) {
             if (lane == 0) {   // no more tiles
                 s_vrows[fills % C::NV] = -1;
                 mbar_arrive(&v_full[fills % C::NV]);
@@ -637,7 +730,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             bool ok = true;
             for (int seg = 0; ok; ++seg) {
                 const int buf = seg & 1;
-                if (!mbar_wait(kTurnQ ? &q_turned[buf] : &q_full[buf], (seg >> 1) & 1, s_abort)) break;
+                if (!wait_one<kFp8>(kTurnQ ? &q_turned[buf] : &q_full[buf], (seg >> 1) & 1, s_abort)) break;
                 tc_fence_after();
                 const int nblk = s_seg[buf].nblk;
                 if (nblk == 0) break;
@@ -647,10 +740,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                 }
                 for (int x = 0; x < nblk && ok; ++x, ++blk) {
                     // S^T's buffer is read once P^T of two blocks before is there
-                    ok = blk < 2 || mbar_wait(&p_full[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
+                    ok = blk < 2 || wait_one<kFp8>(&p_full[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
                     for (int c = 0; c < C::CHUNKS && ok; ++c, ++fill) {
                         if constexpr (kFp8) {
-                            ok = mbar_wait(&kt_full[fill & 1], (fill >> 1) & 1, s_abort);
+                            ok = wait_one<kFp8>(&kt_full[fill & 1], (fill >> 1) & 1, s_abort);
                             if (!ok) break;
                             tc_fence_after();
                             for (int cb = 0; cb < C::CCB; ++cb)
@@ -663,7 +756,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                             continue;
                         }
                         const int slot = fill % C::NK;
-                        ok = mbar_wait(&k_full[slot], (fill / C::NK) & 1, s_abort);
+                        ok = wait_one<kFp8>(&k_full[slot], (fill / C::NK) & 1, s_abort);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t ad = sdesc_adv(dk0, slot * C::SLOT);
@@ -682,7 +775,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             // Drain: no MMA of this warp is in flight at teardown.
             tc_commit(&bar_fin[0]);
             volatile int no_abort = 0;
-            mbar_wait(&bar_fin[0], 0, &no_abort);
+            wait_one<kFp8>(&bar_fin[0], 0, &no_abort);
         }
         __syncwarp();
     } else if (warp == C::PV_WARP) {
@@ -691,20 +784,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             // V^T: 64 head-dim columns, the next 64 a column block on (for
             // d = 64 the same again: lanes 64-127 of O^T are not used)
             const uint64_t dv0 = sdesc_sw128(smem_u32(kFp8 ? sW : sV), D == 64 ? 0 : C::CB_BYTES, 1024);
-            constexpr int NVS = kFp8 ? 2 : C::NV;
+            constexpr int NVS = kFp8 ? C::NW : C::NV;
             uint64_t* const full = kFp8 ? vt_full : v_full;
             uint64_t* const empty = kFp8 ? vt_empty : v_empty;
             const uint64_t dp0 = sdesc_sw128(smem_u32(sP), 16, 1024);
             int fill = 0;
             bool ok = true;
             for (int blk = 0; ok; ++blk) {
-                if (!mbar_wait(&p_full[blk & 1], (blk >> 1) & 1, s_abort)) break;
+                if (!wait_one<kFp8>(&p_full[blk & 1], (blk >> 1) & 1, s_abort)) break;
                 tc_fence_after();
                 const int kind = s_kind[blk & 1];
                 if (kind == kStop) break;
                 for (int c = 0; c < C::CHUNKS; ++c, ++fill) {
                     const int slot = fill % NVS;
-                    ok = mbar_wait(&full[slot], (fill / NVS) & 1, s_abort);
+                    ok = wait_one<kFp8>(&full[slot], (fill / NVS) & 1, s_abort);
                     if (!ok) break;
                     tc_fence_after();
                     mma8_ss_f16<128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128, 128>(
@@ -717,7 +810,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             // Drain: no MMA of this warp is in flight at teardown.
             tc_commit(&bar_fin[1]);
             volatile int no_abort = 0;
-            mbar_wait(&bar_fin[1], 0, &no_abort);
+            wait_one<kFp8>(&bar_fin[1], 0, &no_abort);
         }
         __syncwarp();
     } else if (kFp8 && warp >= C::V_CONV) {
@@ -727,36 +820,40 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         // halves of the swizzled 128 bytes (at d = 64: in rows of unlike parity), and
         // their two writes each in the even and the odd 16-byte groups: no two meet in a bank.
         const int tid = static_cast<int>(threadIdx.x) - 32 * C::V_CONV;
-        const int cq = tid & 3, other = (tid & 4) ? 5 : 0;
+        const int cq = tid & 3, x = tid >> 3;
+        const int cb = C::CCB == 2 ? x & 1 : 0, y = C::CCB == 2 ? x >> 1 : x;
+        constexpr int STEP = 2048 / C::CW;   // rows from one piece of a thread to its next
+        const int r0 = ((y >> 2) * 8 + (y & 3)) ^ ((tid & 4) ? 5 : 0);
+        const int sw = C::CW == 128 ? r0 & 7 : (r0 >> 1) & 3;   // (the same in all its rows)
+        const uint8_t* const src0 = sV + r0 * C::CW + (((4 * cb + cq) ^ sw) << 4);
+        uint8_t* const dst0 = sW + cb * C::CB_BYTES + r0 * 128;
+        const int d0 = ((2 * cq) ^ (r0 & 7)) << 4, d1 = ((2 * cq + 1) ^ (r0 & 7)) << 4;
         for (int fill = 0;; ++fill) {
             const int slot = fill % C::NV;
-            if (!mbar_wait_warp_soon(&v_full[slot], (fill / C::NV) & 1, s_abort)) break;
+            if (!wait_warp_soon<kFp8>(&v_full[slot], (fill / C::NV) & 1, s_abort)) break;
             const int rows = s_vrows[slot];
             if (rows < 0) break;
             const int lo = rows & 255, hi = rows >> 8;
-            if (fill >= 2 && !mbar_wait_warp_soon(&vt_empty[fill & 1], ((fill >> 1) & 1) ^ 1, s_abort)) break;
-            const uint8_t* const raw = sV + slot * C::SLOT;
-            uint8_t* const wide = sW + (fill & 1) * C::CHUNK;
-#pragma unroll
-            for (int it = 0; it < C::CW / 16; ++it) {
-                const int x = it * 16 + (tid >> 3);
-                const int cb = C::CCB == 2 ? x & 1 : 0, y = C::CCB == 2 ? x >> 1 : x;
-                const int r = ((y >> 2) * 8 + (y & 3)) ^ other, c = 4 * cb + cq;
-                const uint4 v = *reinterpret_cast<const uint4*>(
-                    raw + r * C::CW + ((c ^ (C::CW == 128 ? r & 7 : (r >> 1) & 3)) << 4));
+            const int to = fill % C::NW;
+            if (!wait_warp_soon<kFp8>(&vt_empty[to], ((fill / C::NW) & 1) ^ 1, s_abort)) break;
+            const uint8_t* const src = src0 + slot * C::SLOT;
+            uint8_t* const dst = dst0 + to * C::CHUNK;
+            // (a short loop: the four roles' loops on an SM sub-partition share its
+            // instruction buffer, and unrolled ones starved one another, 118 -> 96 us
+            // for 48 requests of up to 4200 keys)
+#pragma unroll 4
+            for (int it = 0; it < kTileRows / STEP; ++it) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);   // outside what is attended: whatever is there, even NaN
+                if (static_cast<unsigned>(r0 + it * STEP - lo) < static_cast<unsigned>(hi - lo))
+                    v = *reinterpret_cast<const uint4*>(src + it * STEP * C::CW);
                 uint32_t w[8];
                 e4m3x16_to_f16(v, w);
-                if (r < lo || r >= hi) {   // outside what is attended: whatever is there, even NaN
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = 0u;
-                }
-                uint8_t* const dst = wide + cb * C::CB_BYTES + r * 128;
-                *reinterpret_cast<uint4*>(dst + (((2 * cq) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4*>(dst + (((2 * cq + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                *reinterpret_cast<uint4*>(dst + it * STEP * 128 + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(dst + it * STEP * 128 + d1) = make_uint4(w[4], w[5], w[6], w[7]);
             }
             mbar_arrive_warp(&v_empty[slot]);
             fence_proxy_async_smem();
-            mbar_arrive_warp(&vt_full[fill & 1]);
+            mbar_arrive_warp(&vt_full[to]);
         }
     } else if (kFp8 && warp >= C::K_CONV) {
         // ================= K from e4m3 to fp16, bf16 queries to fp16 =================
@@ -766,7 +863,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
             const int buf = seg & 1;
-            if (!mbar_wait_warp_soon(&q_full[buf], (seg >> 1) & 1, s_abort)) break;
+            if (!wait_warp_soon<kFp8>(&q_full[buf], (seg >> 1) & 1, s_abort)) break;
             const int nblk = s_seg[buf].nblk;
             const bool none = s_seg[buf].none != 0;
             if constexpr (kTurnQ) {
@@ -812,12 +909,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             if (nblk == 0) break;
             for (int x = 0; x < (none ? 0 : nblk * C::CHUNKS) && ok; ++x, ++fill) {
                 const int slot = fill % C::NK;
-                ok = mbar_wait_warp_soon(&k_full[slot], (fill / C::NK) & 1, s_abort);
-                if (ok && fill >= 2) ok = mbar_wait_warp_soon(&kt_empty[fill & 1], ((fill >> 1) & 1) ^ 1, s_abort);
+                ok = wait_warp_soon<kFp8>(&k_full[slot], (fill / C::NK) & 1, s_abort);
+                if (ok && fill >= 2) ok = wait_warp_soon<kFp8>(&kt_empty[fill & 1], ((fill >> 1) & 1) ^ 1, s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 // a key per lane: 64 head-dim elements at a time
-#pragma unroll
+#pragma unroll 1
                 for (int cb = 0; cb < C::CCB; ++cb) {
                     uint32_t w[32];
 #pragma unroll
@@ -855,23 +952,23 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
         float* const g_fac = s_fac + c0;
         int* const g_lo = s_lo + c0;
         uint32_t* const g_num = s_num + c0;
+        constexpr int W = NC < 16 ? NC : 16;   // columns of O^T at a time
         const int G = p.G;
         const float sc = p.scale_log2;
         const uint64_t sc2 = f2_pack(sc, sc);
-        const int box_shift = 31 - __clz(p.box_rows);
         // Pieces go to the workspace, or, in a cluster, to shared memory where
         // the K ring (fp8: widened V) was (this CTA's only segment is over by then).
         float* const piece_o = p.cluster > 0 ? reinterpret_cast<float*>(kFp8 ? sW : sK) : p.part_o;
         float* const piece_lse = p.cluster > 0 ? s_lse : p.part_lse;
         const int piece_rows = p.cluster > 0 ? N : p.slot_rows;
-        int blk = 0;    // blocks so far, over all segments
+        int blk0 = 0;   // blocks of the segments before
         bool ok = true;
         for (int seg = 0;; ++seg) {
             const int buf = seg & 1;
             // A group's warps meet at barriers inside a segment, so all of them
             // take it or none does; a wait that fails inside leaves the results
             // unspecified and ends the walk at the next segment.
-            ok = ok && mbar_wait_warp(&q_full[buf], (seg >> 1) & 1, s_abort);
+            ok = ok && wait_warp<kFp8>(&q_full[buf], (seg >> 1) & 1, s_abort);
             if (named_barrier_or(bar, 128, !ok)) break;
             Segment s;
             s.nblk = s_seg[buf].nblk;
@@ -899,83 +996,97 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                 g_lo[tid] = lo;
                 g_num[tid] = static_cast<uint32_t>(max(0, hi - lo));
             }
+            // Blocks where some row does not attend some key: the range's ends, the
+            // causal diagonal (queries are the last ntok keys), and a window's
+            // start, which moves with the query.  The others begin at keys [clear_lo, clear_hi].
+            int clear_lo = s.klo, clear_hi = s.khi - kTileRows;
+            if (p.causal) clear_hi = min(clear_hi, s.off - kTileRows + 1);
+            if (p.window > 0) {
+                clear_lo = max(clear_lo, s.off + s.ntok - p.window);
+                if (!p.causal) clear_hi = min(clear_hi, s.off + p.window - kTileRows);
+            }
             named_barrier_sync(bar, 128);
+            // With eight rows a thread, what a block needs of them stays in registers.
+            constexpr bool kKeep = NC == 8;
+            uint64_t kept_nm[NC / 2], kept_qs[NC / 2];
             uint64_t l[NC / 2];   // this thread's sums, two rows each
 #pragma unroll
             for (int n = 0; n < NC / 2; ++n) l[n] = f2_pack(0.f, 0.f);
-            for (int x = 0; x < (s.none ? 0 : s.nblk); ++x, ++blk) {
+            const int nblk = s.none ? 0 : s.nblk;
+            for (int x = 0; x < nblk; ++x) {
+                const int blk = blk0 + x;
                 const int k0 = (s.j0 + x) * kTileRows;
                 const int key = k0 + tid;
-                ok = ok && mbar_wait_warp_soon(&s_full[blk & 1], (blk >> 1) & 1, s_abort);
+                // (fp8) The factor of this key's scores and the exponent ev of its V's scale
+                float key_f = 1.f, key_ev = 0.f;
+                if constexpr (kFp8) {
+                    ok = ok && wait_warp_soon<kFp8>(&sc_full[blk & 15], (blk >> 4) & 1, s_abort);
+                    const float2 both = const_cast<const float2*>(reinterpret_cast<volatile float2*>(s_scale))[
+                        (blk & 15) * 16 + (tid >> box_log)];
+                    key_f = both.x;
+                    key_ev = both.y;
+                }
+                ok = ok && wait_warp_soon<kFp8>(&s_full[blk & 1], (blk >> 1) & 1, s_abort);
                 tc_fence_after();
                 uint32_t sr[NC];
                 tmem_ld_cols<NC>(t_S + (blk & 1) * N, sr);
                 tmem_ld_wait();
                 reg_fence(sr);
-                // Blocks where some row does not attend some key: the range's
-                // ends, the causal diagonal (queries are the last ntok keys), and
-                // a window's start, which moves with the query.
-                const bool cut = k0 < s.klo || k0 + kTileRows > s.khi;
-                const bool diagonal = p.causal && k0 + kTileRows - 1 > s.off;
-                const bool sliding = p.window > 0 &&
-                                     (k0 < s.off + s.ntok - p.window ||
-                                      (!p.causal && k0 + kTileRows - 1 > s.off + p.window - 1));
-                if (cut || diagonal || sliding) {
+                if (k0 < clear_lo || k0 > clear_hi) {
 #pragma unroll
                     for (int n = 0; n < NC; ++n)
                         if (static_cast<uint32_t>(key - g_lo[n]) >= g_num[n]) sr[n] = __float_as_uint(-INFINITY);
                 }
-                // (fp8) The key's factor of its scores, and the exponent ev of its V's
-                // scale: weights are taken times 2^ev, references are of s + ev, and
-                // the sum takes 2^ev off again.
-                uint64_t f2 = 0, ev2 = 0, off2 = 0;
+                // (fp8) Scores become exponents s scale log2e + ev in place: weights are
+                // taken times 2^ev, references are of s + ev, and the sum takes 2^ev off again.
+                uint64_t off2 = 0;
                 if constexpr (kFp8) {
-                    volatile const float* at = s_scale + ((blk & 15) * 16 + (tid >> box_shift)) * 2;
-                    const float f = at[0], ev = at[1];
-                    f2 = f2_pack(f, f);
-                    ev2 = f2_pack(ev, ev);
-                    const float off = exp2_int(-static_cast<int>(ev));
+                    const float off = exp2_int(-static_cast<int>(key_ev));
+                    const uint64_t f2 = f2_pack(key_f, key_f), ev2 = f2_pack(key_ev, key_ev);
                     off2 = f2_pack(off, off);
+                    const uint64_t* const qs = reinterpret_cast<const uint64_t*>(s_qs + (seg & 3) * 64 + c0);
+#pragma unroll
+                    for (int n = 0; n < NC; n += 2) {
+                        uint64_t v = f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1]));
+                        if (kTurnQ && kKeep && x == 0) kept_qs[n / 2] = qs[n / 2];
+                        v = kTurnQ ? f2_fma(f2_mul(v, f2), kKeep ? kept_qs[n / 2] : qs[n / 2], ev2) : f2_fma(v, f2, ev2);
+                        float lo, hi;
+                        f2_unpack(v, lo, hi);
+                        sr[n] = __float_as_uint(lo);
+                        sr[n + 1] = __float_as_uint(hi);
+                    }
                 }
-                const uint64_t* const qs = reinterpret_cast<const uint64_t*>(s_qs + (seg & 3) * 64 + c0);
                 // Exponents s scale log2e - m, two rows at a time.  Rows past the
                 // tile's have m = inf: exponent -inf, weight 0.
-                auto exponent2 = [&](int n, uint64_t nm) {   // of rows n and n + 1, minus m given
-                    const uint64_t s2 = f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1]));
-                    if constexpr (!kFp8) return f2_fma(s2, sc2, nm);
-                    else if constexpr (kTurnQ) return f2_fma(f2_mul(s2, f2), qs[n / 2], f2_add(nm, ev2));
-                    else return f2_fma(s2, f2, f2_add(nm, ev2));
-                };
                 auto exponents = [&](int c, float (&e)[8]) {   // of rows 8 c .. 8 c + 7
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = 8 * c + 2 * i;
-                        f2_unpack(exponent2(n, reinterpret_cast<const uint64_t*>(g_negm)[n / 2]), e[2 * i], e[2 * i + 1]);
+                        const uint64_t nm = kKeep ? kept_nm[n / 2] : reinterpret_cast<const uint64_t*>(g_negm)[n / 2];
+                        const uint64_t s2 = f2_pack(__uint_as_float(sr[n]), __uint_as_float(sr[n + 1]));
+                        f2_unpack(kFp8 ? f2_add(s2, nm) : f2_fma(s2, sc2, nm), e[2 * i], e[2 * i + 1]);
                     }
                 };
+                float kept_e[8];
                 bool grows = false;
                 if (x > 0) {
                     float mx = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < NC / 8; ++c) {
-                        float e[8];
+                        float now[8];
+                        float(&e)[8] = kKeep ? kept_e : now;
                         exponents(c, e);
                         mx = max3f(max3f(e[0], e[1], e[2]), max3f(e[3], e[4], e[5]), max3f(e[6], e[7], mx));
                     }
                     grows = mx > kRescaleThreshold + kWeightShift<kMmaF16>;
                 }
-                if (x == 0 || named_barrier_or(bar, 128, grows)) {
+                const bool renewed = x == 0 || named_barrier_or(bar, 128, grows);
+                if (renewed) {
                     // new references, from the maxima over the warp's keys, then over the four warps
                     float mine_max = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
-                        float v = __uint_as_float(sr[n]);
-                        if constexpr (kFp8) {   // scaled already
-                            float lo, hi;
-                            f2_unpack(exponent2(n & ~1, f2_pack(0.f, 0.f)), lo, hi);
-                            v = n & 1 ? hi : lo;
-                        }
-                        const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(v)));
+                        const float wm = key_float(__reduce_max_sync(0xffffffffu, float_key(__uint_as_float(sr[n]))));
                         if (n == lane) mine_max = wm;
                     }
                     if (lane < NC) g_row[quarter * N + lane] = mine_max;
@@ -990,33 +1101,40 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                     }
                     named_barrier_sync(bar, 128);
                     if (x > 0) {   // sums and O^T columns, once P V of the block before is in
-                        ok = ok && mbar_wait_warp(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
+                        ok = ok && wait_warp<kFp8>(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
                         tc_fence_after();
 #pragma unroll
                         for (int n = 0; n < NC / 2; ++n) l[n] = f2_mul(l[n], reinterpret_cast<const uint64_t*>(g_fac)[n]);
 #pragma unroll 1
-                        for (int c = 0; c < C::HALVES * NC / 16; ++c) {
-                            const uint32_t at = t_O + c / (NC / 16) * N + 16 * (c % (NC / 16));
-                            uint32_t o[16];
-                            tmem_ld16(at, o);
+                        for (int c = 0; c < C::HALVES * NC / W; ++c) {
+                            const uint32_t at = t_O + c / (NC / W) * N + W * (c % (NC / W));
+                            uint32_t o[W];
+                            tmem_ld_cols<W>(at, o);
                             tmem_ld_wait();
                             reg_fence(o);
 #pragma unroll
-                            for (int n = 0; n < 16; ++n)
-                                o[n] = __float_as_uint(__uint_as_float(o[n]) * g_fac[(16 * c + n) % NC]);
-                            tmem_st16(at, o);
+                            for (int n = 0; n < W; ++n)
+                                o[n] = __float_as_uint(__uint_as_float(o[n]) * g_fac[(W * c + n) % NC]);
+                            if constexpr (W == 8) tmem_st8(at, o);
+                            else tmem_st16(at, o);
                         }
                         tmem_st_wait();
                     }
                 }
+                if (kKeep && renewed) {
+#pragma unroll
+                    for (int n = 0; n < NC / 2; ++n) kept_nm[n] = reinterpret_cast<const uint64_t*>(g_negm)[n];
+                    exponents(0, kept_e);
+                }
                 // P^T: this key's N weights, rounded to the storage type for the
                 // product with V; the sum takes them unrounded
-                if (blk >= 2) ok = ok && mbar_wait_warp_soon(&pv_done[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
+                if (blk >= 2) ok = ok && wait_warp_soon<kFp8>(&pv_done[blk & 1], ((blk >> 1) & 1) ^ 1, s_abort);
                 uint8_t* row = sP + (blk & 1) * C::P_BYTES + tid * 128;
 #pragma unroll
                 for (int c = 0; c < NC / 8; ++c) {
-                    float e[8];
-                    exponents(c, e);
+                    float now[8];
+                    float(&e)[8] = kKeep ? kept_e : now;
+                    if (!kKeep) exponents(c, e);
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -1028,16 +1146,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                     }
                     *reinterpret_cast<uint4*>(row + (((c0 / 8 + c) ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (!kFp8 && cut) {
+                if (!kFp8 && (k0 < s.klo || k0 + kTileRows > s.khi)) {
                     // V rows of keys outside [klo, khi) become zero.  Their slots'
                     // fills before this one must have landed, or the parity would
                     // be theirs: with a tile in two slots that takes P V of the
                     // block before, else that of two blocks before (above).
                     if (C::CHUNKS == 2 && blk > 0)
-                        ok = ok && mbar_wait_warp(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
+                        ok = ok && wait_warp<kFp8>(&pv_done[(blk - 1) & 1], ((blk - 1) >> 1) & 1, s_abort);
                     for (int c = 0; c < C::CHUNKS; ++c) {   // (each group clears all of them)
                         const int f = C::CHUNKS * blk + c;
-                        ok = ok && mbar_wait_warp(&v_full[f % C::NV], (f / C::NV) & 1, s_abort);
+                        ok = ok && wait_warp<kFp8>(&v_full[f % C::NV], (f / C::NV) & 1, s_abort);
                         if (ok && (key < s.klo || key >= s.khi)) {
                             for (int cb = 0; cb < C::CCB; ++cb) {
                                 uint4* vr = reinterpret_cast<uint4*>(sV + (f % C::NV) * C::SLOT + cb * C::CB_BYTES +
@@ -1058,7 +1176,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
 #pragma unroll
             for (int n = 0; n < NC / 2; ++n) f2_unpack(l[n], ls[2 * n], ls[2 * n + 1]);
             const int col = warp_sum_scatter<NC>(ls, lane);
-            if (NC == 32 || (lane & 1) == 0) g_row[quarter * N + col] = ls[0];
+            if ((lane & (32 / NC - 1)) == 0) g_row[quarter * N + col] = ls[0];
             named_barrier_sync(bar, 128);
             if (tid < NC) {
                 const float sum = (g_row[tid] + g_row[N + tid]) + (g_row[2 * N + tid] + g_row[3 * N + tid]);
@@ -1075,9 +1193,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                     }
                 }
             }
+            blk0 += nblk;
             if (!s.none) {
-                const int last = blk - 1;
-                ok = ok && mbar_wait_warp(&pv_done[last & 1], (last >> 1) & 1, s_abort);
+                const int last = blk0 - 1;
+                ok = ok && wait_warp<kFp8>(&pv_done[last & 1], (last >> 1) & 1, s_abort);
                 tc_fence_after();
             }
             named_barrier_sync(bar, 128);
@@ -1093,22 +1212,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
                 size_t at = out0 + h * 128 + tid;
                 int g = g0;
 #pragma unroll 1
-                for (int c = 0; c < NC / 16; ++c) {
-                    if (16 * c >= rows) break;
-                    uint32_t o[16];
+                for (int c = 0; c < NC / W; ++c) {
+                    if (W * c >= rows) break;
+                    uint32_t o[W];
                     if (!s.none) {
-                        tmem_ld16(t_O + h * N + 16 * c, o);
+                        tmem_ld_cols<W>(t_O + h * N + W * c, o);
                         tmem_ld_wait();
                         reg_fence(o);
                     } else {
 #pragma unroll
-                        for (int n = 0; n < 16; ++n) o[n] = 0u;
+                        for (int n = 0; n < W; ++n) o[n] = 0u;
                     }
                     if (D >= 128 || tid < D) {
 #pragma unroll
-                        for (int n = 0; n < 16; ++n) {
-                            if (16 * c + n < rows) {
-                                const float y = __uint_as_float(o[n]) * g_fac[16 * c + n];
+                        for (int n = 0; n < W; ++n) {
+                            if (W * c + n < rows) {
+                                const float y = __uint_as_float(o[n]) * g_fac[W * c + n];
                                 if (s.out >= 0)
                                     piece_o[at] = y;
                                 else
@@ -1130,8 +1249,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             tc_fence_before();
         }
         if (ok) {   // tell the P V warp
-            if (threadIdx.x == 0) s_kind[blk & 1] = kStop;
-            mbar_arrive_warp(&p_full[blk & 1]);
+            if (threadIdx.x == 0) s_kind[blk0 & 1] = kStop;
+            mbar_arrive_warp(&p_full[blk0 & 1]);
         }
     }
 
