@@ -34,6 +34,7 @@
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
+#include "fp8.cuh"
 #include "paged.cuh"
 
 namespace gbattn {
@@ -66,9 +67,15 @@ __device__ __forceinline__ void find_packed_tile(const PagedParams& p, int x, in
     local = x - packed_tile_base(p, b);
 }
 
-template <int D, bool kF16, int kTiles>
-struct PagedCfg : FwdCfg<D, false, kF16, false, kTiles> {
-    using Base = FwdCfg<D, false, kF16, false, kTiles>;
+// (kFp8) What the producer passes to the warps that widen e4m3, and to the softmax.
+struct Widening {
+    uint2 factor[2][16];   // [block][8 keys]: scales over the block's largest, K's and V's, as fp16 twice
+    float2 block[16];      // largest scale of K times the softmax scale, exponent of V's
+};
+
+template <int D, bool kF16, int kTiles, bool kFp8>
+struct PagedCfg : FwdCfg<D, false, kF16 || kFp8, false, kTiles> {
+    using Base = FwdCfg<D, false, kF16 || kFp8, false, kTiles>;
     // Softmax threads of a row, which share its keys.  One query tile alone has
     // nothing to run while its softmax does: two threads a row halve that (8
     // chunks of 33 to 65 tokens, d = 256: 27.4 -> 25.4 us).  Two tiles fill in for
@@ -78,26 +85,36 @@ struct PagedCfg : FwdCfg<D, false, kF16, false, kTiles> {
     static constexpr int NC = kTileRows / PARTS;      // keys of a thread
     static constexpr int DC = D / PARTS;              // output columns of a thread
     static constexpr int ROW_THREADS = kTileRows * PARTS;
-    static constexpr int THREADS = kTiles * ROW_THREADS + 64;
+    static constexpr int CONV_WARP = kTiles * ROW_THREADS / 32 + 2;   // (kFp8) two that widen
+    static constexpr int THREADS = kTiles * ROW_THREADS + (kFp8 ? 128 : 64);
     static constexpr int PRODUCER_WARP = kTiles * ROW_THREADS / 32;
     static constexpr int MMA_WARP = PRODUCER_WARP + 1;
     static constexpr int ROW_FLOATS = kTiles * ROW_THREADS;   // one per softmax thread
-    static constexpr int SMEM = Base::SMEM + (PARTS > 1 ? 3 * ROW_FLOATS * 4 : 0);   // maxima; sums of two units
+    static constexpr int PART_BYTES = PARTS > 1 ? 3 * ROW_FLOATS * 4 : 0;   // maxima; sums of two units
+    // (kFp8) e4m3 as loaded: 64 rows of up to 128 head-dim columns a slot
+    static constexpr int RAW_COLS = D < 128 ? D : 128;
+    static constexpr int RAW = 64 * RAW_COLS;
+    static constexpr int NRAW = D == 64 ? 8 : D == 128 ? 4 : 3;
+    static constexpr int UNITS = 2 * D / RAW_COLS;    // slots of a K or V tile
+    static constexpr int TURN_BYTES = 2 * 2 * kTileRows;
+    static constexpr int SMEM = Base::SMEM + PART_BYTES + (kFp8 ? NRAW * RAW + TURN_BYTES : 0);
 };
 
-template <int D, bool kF16, int kTiles, bool kFine, bool kLoop>
-__global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
+template <int D, bool kF16, int kTiles, bool kFine, bool kLoop, bool kFp8>
+__global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-    using C = PagedCfg<D, kF16, kTiles>;
+    using C = PagedCfg<D, kF16, kTiles, kFp8>;
+    constexpr bool kMmaF16 = kF16 || kFp8;   // type of the products' operands
+    constexpr bool kTurnQ = kFp8 && !kF16;   // bf16 queries become fp16 times a power of two a row
     grid_dep_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sQ = smem;                                   // C::TILES tiles
     uint8_t* sKV = smem + C::TILES * C::TILE;             // NSLOT tiles
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (C::TILES + C::NSLOT) * C::TILE);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (C::TILES + C::NSLOT) * C::TILE + (kFp8 ? C::NRAW * C::RAW : 0));
     uint64_t* bar_q = bars;               // [2] one per query tile
     uint64_t* full = bars + 2;
     constexpr int kPairs = C::NSLOT / 2;
@@ -110,6 +127,15 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
     uint64_t* q_free = bar_fin + 1;       // (kLoop) a tile's last S has read the queries
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(q_free + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    uint64_t* q_turned = bars + 32;       // (kFp8) [2] a query tile is fp16
+    uint64_t* meta_full = bars + 34;      // [2] a block's factors
+    uint64_t* meta_empty = bars + 36;
+    uint64_t* raw_full = bars + 38;       // [NRAW]
+    uint64_t* raw_empty = bars + 46;
+    volatile Widening& wide = *reinterpret_cast<volatile Widening*>(bars + 80);
+    static_assert(80 * 8 + sizeof(Widening) <= 1024, "factors fit behind the barriers");
+    uint8_t* sRaw = smem + (C::TILES + C::NSLOT) * C::TILE;   // (kFp8: the ring, and the barriers behind it)
+    int8_t* s_turn = reinterpret_cast<int8_t*>(bars) + 1024 + C::PART_BYTES;   // [unit & 1][tile][row] exponents
     float* s_max = reinterpret_cast<float*>(bars + 128);   // (PARTS = 2) [tile][part][row]
     float* s_sum = s_max + C::ROW_FLOATS;                  // and [unit & 1][tile][part][row]
 
@@ -280,8 +306,17 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
         mbar_init(&bar_q[0], 1);
         mbar_init(&bar_q[1], 1);
         for (int s = 0; s < C::NSLOT; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], kFp8 ? 64 : 1);
             mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < C::NRAW && kFp8; ++s) {
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], 64);
+        }
+        for (int s = 0; s < 2 && kFp8; ++s) {
+            mbar_init(&q_turned[s], 64);
+            mbar_init(&meta_full[s], 1);
+            mbar_init(&meta_empty[s], 64);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar_s[t], 1);
@@ -309,7 +344,8 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
         }
-        int seq = 0;                        // ring fills so far
+        int seq = 0;                        // ring fills (kFp8: blocks) so far
+        int raw_fills = 0;
         int tiles = 0, q_n0 = 0, q_n1 = 0;  // units with blocks; loads of each query tile
         bool ok = true;
         do {
@@ -333,7 +369,64 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
             }
             q_n0 += pl.jhi0 > pl.jlo0;
             q_n1 += pl.jhi1 > pl.jlo1;
-            for (int j = jbeg; j < jbeg + nkv && ok; ++j) {
+            // (kFp8) A block's scales are taken relative to its largest, so that one
+            // factor holds for all its scores and one exponent for all its weights;
+            // values are exact in fp16 down to 2^-15 of the largest scale, and
+            // below are off by 2^-25 of it.  They are passed on behind the
+            // block's first load, before any other wait.
+            for (int j = jbeg; kFp8 && j < jbeg + nkv && ok; ++j, ++seq) {
+                const unsigned needed = __ballot_sync(0xffffffffu, box.needed);
+                PageBox next = box;
+                if (j + 1 < jbeg + nkv) next = page_box(p, table, (j + 1) * kTileRows, pl.klo, pl.khi, lane);
+                const int page = box.needed ? page_box_checked(p, box) : p.num_pages;
+                const bool there = page < p.num_pages;
+                uint32_t kb = 127u << 23, vb = kb;
+                if (there) {
+                    const size_t at = static_cast<size_t>(page) * p.Hkv + pl.hk;
+                    kb = __float_as_uint(p.k_scale[at]);
+                    vb = __float_as_uint(p.v_scale[at]);
+                }
+                const int half_boxes = 64 / p.box_rows;
+                for (int u = 0; u < 2 * C::UNITS; ++u) {
+                    const int which = u / C::UNITS, part = u % C::UNITS;   // part: 64 rows, then columns
+                    const int n = 2 * C::UNITS * seq + u, slot = n % C::NRAW;
+                    ok = mbar_wait_warp_soon(&raw_empty[slot], ((n / C::NRAW) & 1) ^ 1, s_abort);
+                    if (!ok) break;
+                    const unsigned mine = needed >> ((part & 1) * half_boxes) & ((1u << half_boxes) - 1u);
+                    ++raw_fills;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&raw_full[slot], __popc(mine) * static_cast<uint32_t>(p.box_rows) * C::RAW_COLS);
+                    __syncwarp();
+                    if (box.needed && lane / half_boxes == (part & 1))
+                        tma_load_4d(sRaw + slot * C::RAW + lane % half_boxes * p.box_rows * C::RAW_COLS, which ? &tmV : &tmK,
+                                    &raw_full[slot], (part >> 1) * C::RAW_COLS, box.row, pl.hk, page);
+                    __syncwarp();
+                    if (u == 0) {
+                        if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
+                            atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+                        const int ke = scale_exponent(kb), ve = scale_exponent(vb);
+                        const int k_top = __reduce_max_sync(0xffffffffu, there ? ke : kLeastScale);
+                        const int v_top = __reduce_max_sync(0xffffffffu, there ? ve : kLeastScale);
+                        ok = mbar_wait_warp_soon(&meta_empty[seq & 1], ((seq >> 1) & 1) ^ 1, s_abort);
+                        if (!ok) break;
+                        const float kf = there ? exp2_int(max(ke - k_top, -60)) : 0.f;
+                        const float vf = there ? exp2_int(max(ve - v_top, -60)) : 0.f;
+                        for (int i = 0; i < p.box_rows / 8 && lane < kTileRows / p.box_rows; ++i) {
+                            volatile uint2& f = wide.factor[seq & 1][lane * (p.box_rows / 8) + i];
+                            f.x = pack_f16x2(kf, kf);
+                            f.y = pack_f16x2(vf, vf);
+                        }
+                        if (lane == 0) {
+                            wide.block[seq & 15].x = exp2_int(k_top) * p.scale_log2;
+                            wide.block[seq & 15].y = static_cast<float>(v_top);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&meta_full[seq & 1]);
+                    }
+                }
+                box = next;
+            }
+            for (int j = jbeg; !kFp8 && j < jbeg + nkv && ok; ++j) {
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
                                        static_cast<uint32_t>(p.box_rows) * C::ROWB;
                 // the next tile's table entries arrive while this tile waits
@@ -378,9 +471,11 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
             volatile int no_abort = 0;
             if (q_n0 > 0) mbar_wait(&bar_q[0], (q_n0 - 1) & 1, &no_abort);
             if (q_n1 > 0) mbar_wait(&bar_q[1], (q_n1 - 1) & 1, &no_abort);
-            for (int s = 0; s < C::NSLOT && s < seq; ++s) {
-                const int uses = (seq - s + C::NSLOT - 1) / C::NSLOT;
-                mbar_wait(&full[s], (uses - 1) & 1, &no_abort);
+            constexpr int slots = kFp8 ? C::NRAW : C::NSLOT;
+            if (kFp8) seq = raw_fills;
+            for (int s = 0; s < slots && s < seq; ++s) {
+                const int uses = (seq - s + slots - 1) / slots;
+                mbar_wait(kFp8 ? &raw_full[s] : &full[s], (uses - 1) & 1, &no_abort);
             }
         }
         __syncwarp();
@@ -464,7 +559,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
                             }
                             if (qk) {     // S_t = Q_t K_j^T
                                 if (!q_ready[t]) {
-                                    ok = mbar_wait(&bar_q[t], (t ? q_n1 : q_n0) & 1, s_abort);
+                                    ok = mbar_wait(kTurnQ ? &q_turned[t] : &bar_q[t], (t ? q_n1 : q_n0) & 1, s_abort);
                                     q_ready[t] = true;
                                     if (!ok) break;
                                     tc_fence_after();
@@ -520,6 +615,112 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
             }
         }
         __syncwarp();
+    } else if (kFp8 && warp >= C::CONV_WARP) {
+        // ================= K and V from e4m3 to fp16, bf16 queries to fp16 =================
+        // A thread takes 16 bytes of a row at a time.  Eight consecutive ones take 64
+        // head-dim columns of rows r and r ^ 5: their reads lie in opposite halves of
+        // the swizzled 128 bytes (at d = 64: in rows of unlike parity), and their two
+        // writes each in the even and the odd 16-byte groups: no two meet in a bank.
+        const int tid = static_cast<int>(threadIdx.x) - 32 * C::CONV_WARP;
+        constexpr int STEP = D == 64 ? 16 : 8;           // rows from one piece of a thread to its next
+        const int cq = tid & 3, x = tid >> 3;
+        const int cb = D == 64 ? 0 : x & 1, y = D == 64 ? x : x >> 1;
+        const int r0 = ((y >> 2) * 8 + (y & 3)) ^ ((tid & 4) ? 5 : 0);
+        const uint8_t* const src0 = sRaw + r0 * C::RAW_COLS +
+                                    (((4 * cb + cq) ^ (D == 64 ? (r0 >> 1) & 3 : r0 & 7)) << 4);
+        uint8_t* const dst0 = sKV + cb * C::CB_BYTES + r0 * 128;
+        const int d0 = ((2 * cq) ^ (r0 & 7)) << 4, d1 = ((2 * cq + 1) ^ (r0 & 7)) << 4;
+        int raw = 0;                            // raw slots so far
+        int fills = 0, blk = 0;                 // ring fills and blocks so far
+        int units8 = 0, q_n0 = 0, q_n1 = 0;     // units with blocks; of each query tile
+        bool ok = true;
+        do {
+            const int jbeg = first_block(pl), nkv = num_blocks(pl);
+            if (nkv == 0) continue;
+            if constexpr (kTurnQ) {
+                // A row's largest element goes to [2^14, 2^15): elements down to 2^-28
+                // of it keep all bits, smaller ones are off by 2^-39 of it.
+                for (int t = 0; t < C::TILES && ok; ++t) {
+                    if (!(t ? pl.jhi1 > pl.jlo1 : pl.jhi0 > pl.jlo0)) continue;
+                    ok = mbar_wait_warp(&bar_q[t], (t ? q_n1 : q_n0) & 1, s_abort);
+                    if (!ok) break;
+                    (t ? q_n1 : q_n0) += 1;
+#pragma unroll 1
+                    for (int r = tid; r < kTileRows; r += 64) {
+                    auto piece = [&](int c) {
+                        return reinterpret_cast<uint4*>(sQ + t * C::TILE + (c >> 3) * C::CB_BYTES + r * 128 +
+                                                        (((c & 7) ^ (r & 7)) << 4));
+                    };
+                    uint32_t top = 0;   // largest magnitude, as bf16 bits in either half
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 v = *piece(c);
+                        top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    }
+                    top = max(top & 0xffffu, top >> 16);
+                    const int ea = max(static_cast<int>(top >> 7) - 127, -100);
+                    const float up = exp2_int(14 - ea);
+                    s_turn[((units8 & 1) * 2 + t) * kTileRows + r] = static_cast<int8_t>(ea - 14);
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4* const at = piece(c);
+                        const uint4 v = *at;
+                        auto turn = [&](uint32_t w) { return pack_f16x2(bf16lo_to_f32(w) * up, bf16hi_to_f32(w) * up); };
+                        *at = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+                    }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive_warp(&q_turned[t]);
+                }
+                if (!ok) break;
+            }
+            ++units8;
+            for (int j = jbeg; j < jbeg + nkv && ok; ++j, ++blk) {
+                ok = mbar_wait_warp_soon(&meta_full[blk & 1], (blk >> 1) & 1, s_abort);
+                for (int u = 0; u < 2 * C::UNITS && ok; ++u, ++raw) {
+                    const int which = u / C::UNITS, part = u % C::UNITS;
+                    const int from = raw % C::NRAW;
+                    ok = mbar_wait_warp_soon(&raw_full[from], (raw / C::NRAW) & 1, s_abort);
+                    if (!ok) break;
+                    if (part == 0) {   // the slot is free
+                        if constexpr (kBlockRelease) {
+                            const int bi = fills / 2;
+                            const int wb = which == 0 ? bi - kPairs : bi - kPairs + 1;
+                            ok = bi < kPairs || mbar_wait_warp_soon(&empty[wb % kPairs], (wb / kPairs) & 1, s_abort);
+                        } else {
+                            ok = mbar_wait_warp_soon(&empty[fills % C::NSLOT], ((fills / C::NSLOT) & 1) ^ 1, s_abort);
+                        }
+                        if (!ok) break;
+                    }
+                    const int half = (part & 1) * 64;   // first row
+                    const int lo = pl.klo - j * kTileRows - half, hi = pl.khi - j * kTileRows - half;
+                    const uint8_t* const src = src0 + from * C::RAW;
+                    uint8_t* const dst = dst0 + (fills % C::NSLOT) * C::TILE + (part >> 1) * 2 * C::CB_BYTES + half * 128;
+                    const volatile uint2* const f = wide.factor[blk & 1] + (half + r0) / 8;
+#pragma unroll 4
+                    for (int i = 0; i < 64 / STEP; ++i) {
+                        const int r = r0 + STEP * i;
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);   // outside what is attended: whatever is there, even NaN
+                        if (r >= lo && r < hi) v = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
+                        uint32_t w[8];
+                        e4m3x16_to_f16(v, w);
+                        const uint32_t m = which ? f[STEP / 8 * i].y : f[STEP / 8 * i].x;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], m);
+                        *reinterpret_cast<uint4*>(dst + STEP * i * 128 + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(dst + STEP * i * 128 + d1) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                    mbar_arrive_warp(&raw_empty[from]);
+                    if (part == C::UNITS - 1) {
+                        if (which == 1) mbar_arrive_warp(&meta_empty[blk & 1]);
+                        fence_proxy_async_smem();
+                        mbar_arrive_warp(&full[fills % C::NSLOT]);
+                        ++fills;
+                    }
+                }
+            }
+        } while (ok && next_unit());
     } else {
         // ================= softmax (one or two threads per row) =================
         const int t = warp / (C::ROW_THREADS / 32);
@@ -541,6 +742,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
         int s_n = 0;     // blocks of this query tile in them
         int o_n = 0;     // of them with blocks of this query tile
         int u_n = 0;     // units before
+        int t_n = 0;     // of them with blocks
         bool ok = true;  // of the warp; a tile's warps agree on it at a unit's end
         do {
         const int L = pl.L, klo = pl.klo, khi = pl.khi;
@@ -549,6 +751,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
         const int pos = first_pos + tl;
         const int fill0 = 2 * (g - first_block(pl)) + 1;   // ring fill of V_j: fill0 + 2 j
         const int s_b = s_n - jlo;                         // parity of S_j: (s_b + j) & 1
+        float turn = 1.f;                                  // (kFp8) the row's power of two
         float m_ref = -INFINITY;   // reference, log2 units of scaled scores: a maximum less kWeightShift
         float l = 0.f;             // of this thread's keys
         // A failed wait leaves the results unspecified.  Where a tile's warps meet
@@ -558,10 +761,19 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
             ok = ok && mbar_wait_warp(&bar_s[t], (s_b + j) & 1, s_abort);
             if (C::PARTS == 1 && !ok) break;
             tc_fence_after();
+            // Factor of the scores and (kFp8) exponent of V's scale: weights are taken
+            // times 2^ev, references are of s + ev, and the sum takes 2^ev off again.
+            float sc = p.scale_log2, ev = 0.f;
+            if constexpr (kFp8) {
+                if (kTurnQ && j == jlo) turn = exp2_int(s_turn[((t_n & 1) * 2 + t) * kTileRows + r]);
+                volatile const float2& block = wide.block[(g - first_block(pl) + j) & 15];
+                sc = block.x * turn;
+                ev = block.y;
+            }
             // V rows outside [klo, khi) become zero.  Only after S_j: by then
             // every earlier fill of V_j's slot has been waited for, so that
             // the parity below can only mean this one.
-            if (k0 < klo || k0 + kTileRows > khi) {
+            if (!kFp8 && (k0 < klo || k0 + kTileRows > khi)) {
                 const int fill = fill0 + 2 * j;
                 const int slot = fill % C::NSLOT;
                 ok = ok && mbar_wait_warp(&full[slot], (fill / C::NSLOT) & 1, s_abort);
@@ -612,7 +824,8 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
                                              __uint_as_float(sr[c >> 5][(c & 31) + 1]));
                 mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
             }
-            float m_new = fmaxf(m_ref, mx * p.scale_log2 - kWeightShift<kF16>);
+            float m_new = fmaxf(m_ref, kFp8 ? fmaf(mx, sc, ev - kWeightShift<kMmaF16>)
+                                            : mx * p.scale_log2 - kWeightShift<kMmaF16>);
             float alpha = 1.f;
             bool warp_rescale = false;
             auto adopt = [&]() {
@@ -644,8 +857,9 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
 
             // ---- P = exp2(s scale log2e - m), rounded to the storage type for
             // the P V product; the row sum adds the unrounded P ----
-            const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-            const uint64_t nm2 = f2_pack(neg_m, neg_m);
+            const uint64_t sc2 = f2_pack(sc, sc);
+            const float nm = kFp8 ? neg_m + ev : neg_m;
+            const uint64_t nm2 = f2_pack(nm, nm);
             uint64_t acc2[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc2[k] = f2_pack(0.f, 0.f);
@@ -662,7 +876,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
                               x0, x1);
                     x0 = ex2_approx(x0);
                     x1 = ex2_approx(x1);
-                    pk[e] = pack_h2<kF16>(x0, x1);
+                    pk[e] = pack_h2<kMmaF16>(x0, x1);
                     acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(x0, x1));
                 }
                 tmem_st8(t_P + 8 * c8, pk);
@@ -674,6 +888,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
                 f2_unpack(f2_add(acc2[2], acc2[3]), a2, a3);
                 rowsum = (a0 + a1) + (a2 + a3);
             }
+            if constexpr (kFp8) rowsum *= exp2_int(-static_cast<int>(ev));
             l = l * alpha + rowsum;
             if (warp_rescale && j > jlo) {   // O row *= alpha (PV of block j-1 is complete)
 #pragma unroll
@@ -706,6 +921,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
             l = sums[0] + sums[kTileRows];
             ++u_n;
         }
+        t_n += num_blocks(pl) > 0;
         g += num_blocks(pl);
         s_n += jhi - jlo;
         o_n += any;
@@ -782,11 +998,11 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles>::THREADS, 1)
         atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_DEVICE_TIMEOUT));
 }
 
-template <int D, bool kF16, int kTiles, bool kFine, bool kLoop>
+template <int D, bool kF16, int kTiles, bool kFine, bool kLoop, bool kFp8 = false>
 cudaError_t launch_paged_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PagedParams& p, cudaStream_t stream) {
-    using C = PagedCfg<D, kF16, kTiles>;
-    auto kern = attn_paged_kernel<D, kF16, kTiles, kFine, kLoop>;
+    using C = PagedCfg<D, kF16, kTiles, kFp8>;
+    auto kern = attn_paged_kernel<D, kF16, kTiles, kFine, kLoop, kFp8>;
     static std::atomic<unsigned long long> smem_ready{0};
     const cudaError_t e = enable_smem_per_device(kern, C::SMEM, smem_ready);
     if (e != cudaSuccess) return e;
@@ -804,6 +1020,16 @@ cudaError_t launch_paged_f(const CUtensorMap& tq, const CUtensorMap& tk, const C
                    : launch_paged_t<D, false, kTiles, kFine, true>(tq, tk, tv, p, s);
     return f16 ? launch_paged_t<D, true, kTiles, kFine, false>(tq, tk, tv, p, s)
                : launch_paged_t<D, false, kTiles, kFine, false>(tq, tk, tv, p, s);
+}
+
+template <int D, int kTiles>
+cudaError_t launch_paged_8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                           bool f16, cudaStream_t s) {
+    if (p.splits == 1)
+        return f16 ? launch_paged_t<D, true, kTiles, false, true, true>(tq, tk, tv, p, s)
+                   : launch_paged_t<D, false, kTiles, false, true, true>(tq, tk, tv, p, s);
+    return f16 ? launch_paged_t<D, true, kTiles, false, false, true>(tq, tk, tv, p, s)
+               : launch_paged_t<D, false, kTiles, false, false, true>(tq, tk, tv, p, s);
 }
 
 }  // namespace

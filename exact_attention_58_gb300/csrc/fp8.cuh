@@ -29,6 +29,12 @@ __device__ __forceinline__ void e4m3x16_to_f16(const uint4& v, uint32_t (&w)[8])
             : "r"(x[i]));
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // 2^e as a float, e in [-126, 127].
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 

@@ -68,16 +68,6 @@ struct PagedParams {
     int cluster;                // > 0: CTAs of a cluster, which takes one tile and joins its pieces itself
 };
 
-// A cache of e4m3, its scales, and the queries (strides in elements).
-struct Fp8Cache {
-    const void* Q;
-    const uint8_t* k;
-    const uint8_t* v;
-    const float* k_scale;       // [num_pages][Hkv]
-    const float* v_scale;
-    long long q_token_stride, q_head_stride, page_stride, head_stride, token_stride;
-};
-
 // Keys of request b, clamped to what its page-table row can hold.
 __device__ __forceinline__ int paged_keys(const PagedParams& p, int b) {
     const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
@@ -180,7 +170,8 @@ cudaError_t launch_paged_decode_fp8_d128(const CUtensorMap& tq, const CUtensorMa
                                          const PagedParams& p, bool f16, cudaStream_t stream);
 cudaError_t launch_paged_decode_fp8_d256(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                          const PagedParams& p, bool f16, cudaStream_t stream);
-cudaError_t launch_paged_fp8(const PagedParams& p, const Fp8Cache& c, int d, bool f16, cudaStream_t stream);
+cudaError_t launch_paged_tiles_fp8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const PagedParams& p, int d, bool f16, cudaStream_t stream);
 // Joins the pieces of p.desc[0, descs), up to `rows` rows each.
 enum JoinKind {
     kJoinFewPieces,   // a few pieces a row

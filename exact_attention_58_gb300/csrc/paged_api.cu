@@ -278,12 +278,7 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
     p.scale_log2 = scale * 1.4426950408889634f;
     const bool f16 = dtype == ATTN_DTYPE_FP16;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fp8 && !(plans.count == 1 && plans.plan[0].decode)) {
-        const Fp8Cache c{Q, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale,
-                         v_scale, q_token_stride, q_head_stride, cache_page_stride, cache_head_stride,
-                         cache_token_stride};
-        return from_cuda(launch_paged_fp8(p, c, d, f16, s));
-    }
+    const attn_dtype cache_dtype = fp8 ? ATTN_DTYPE_FP8_E4M3 : dtype;
     CUtensorMap tq[2], tk[2], tv[2];
     PagedParams params[2];
     for (int i = 0; i < plans.count; ++i) {   // all maps before the first launch
@@ -294,6 +289,7 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
         // instead (the decode kernel issues K and V from two warps and has the time).
         p.fine = !t.decode && !fp8 && kTileRows / p.box_rows * (d / 64) > 16;
         if (p.fine) p.box_rows = 8;
+        if (fp8 && !t.decode) p.box_rows = std::min(64, p.box_rows);   // (half tiles)
         p.tile_tokens = t.tile_tokens;
         p.tiles = t.tiles;
         p.tile_div = t.tile_div;
@@ -304,18 +300,18 @@ attn_status fwd_paged(const void* Q, const void* k_cache, const void* v_cache, b
         params[i] = p;
         if (!make_tmap_queries(&tq[i], Q, dtype, total_q, H, d, q_token_stride, q_head_stride, p.G,
                                p.tile_tokens) ||
-            !make_tmap_cache(&tk[i], k_cache, fp8 ? ATTN_DTYPE_FP8_E4M3 : dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+            !make_tmap_cache(&tk[i], k_cache, cache_dtype, num_pages, H_kv, page_size, d, cache_page_stride,
                              cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0) ||
-            !make_tmap_cache(&tv[i], v_cache, fp8 ? ATTN_DTYPE_FP8_E4M3 : dtype, num_pages, H_kv, page_size, d, cache_page_stride,
+            !make_tmap_cache(&tv[i], v_cache, cache_dtype, num_pages, H_kv, page_size, d, cache_page_stride,
                              cache_head_stride, cache_token_stride, p.box_rows, p.fine != 0))
             return ATTN_ERR_CUDA;
     }
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < plans.count && e == cudaSuccess; ++i) {
         const Plan& t = plans.plan[i];
-        e = t.decode && fp8 ? launch_paged_decode_fp8(tq[i], tk[i], tv[i], params[i], d, f16, s)
-            : t.decode ? launch_paged_decode(tq[i], tk[i], tv[i], params[i], d, f16, s)
-                     : launch_paged_tiles(tq[i], tk[i], tv[i], params[i], d, f16, s);
+        const auto launch = t.decode ? (fp8 ? launch_paged_decode_fp8 : launch_paged_decode)
+                                     : (fp8 ? launch_paged_tiles_fp8 : launch_paged_tiles);
+        e = launch(tq[i], tk[i], tv[i], params[i], d, f16, s);
         if (e == cudaSuccess && t.splits > 1 && t.cluster == 0) {
             const int rows = t.tile_tokens * p.G * (t.decode ? 1 : t.rows / kTileRows);
             // pieces of a tile in the mean: CTAs by tiles
