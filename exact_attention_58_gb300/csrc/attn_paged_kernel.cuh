@@ -697,17 +697,23 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                     const int lo = pl.klo - j * kTileRows - half, hi = pl.khi - j * kTileRows - half;
                     const uint8_t* const src = src0 + from * C::RAW;
                     uint8_t* const dst = dst0 + (fills % C::NSLOT) * C::TILE + (part >> 1) * 2 * C::CB_BYTES + half * 128;
-                    const volatile uint2* const f = wide.factor[blk & 1] + (half + r0) / 8;
-#pragma unroll 4
-                    for (int i = 0; i < 64 / STEP; ++i) {
-                        const int r = r0 + STEP * i;
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);   // outside what is attended: whatever is there, even NaN
-                        if (r >= lo && r < hi) v = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
-                        uint32_t w[8];
-                        e4m3x16_to_f16(v, w);
-                        const uint32_t m = which ? f[STEP / 8 * i].y : f[STEP / 8 * i].x;
+                    const uint32_t* const f = const_cast<const uint32_t*>(&wide.factor[blk & 1][(half + r0) / 8].x) + which;
+                    constexpr int PIECES = 64 / STEP;   // all asked for before the first is used
+                    uint4 v[PIECES];
+                    uint32_t m[PIECES];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], m);
+                    for (int i = 0; i < PIECES; ++i) {
+                        const int r = r0 + STEP * i;
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);   // outside what is attended: whatever is there, even NaN
+                        if (r >= lo && r < hi) v[i] = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
+                        m[i] = f[STEP / 4 * i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) {
+                        uint32_t w[8];
+                        e4m3x16_to_f16(v[i], w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], m[i]);
                         *reinterpret_cast<uint4*>(dst + STEP * i * 128 + d0) = make_uint4(w[0], w[1], w[2], w[3]);
                         *reinterpret_cast<uint4*>(dst + STEP * i * 128 + d1) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
