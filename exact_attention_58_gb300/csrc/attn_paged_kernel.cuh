@@ -71,6 +71,7 @@ __device__ __forceinline__ void find_packed_tile(const PagedParams& p, int x, in
 struct Widening {
     uint2 factor[2][16];   // [block][8 keys]: scales over the block's largest, K's and V's, as fp16 twice
     float2 block[16];      // largest scale of K times the softmax scale, exponent of V's
+    int plain[2];          // [block] bit 0, 1: all of K's, V's factors are one
 };
 
 template <int D, bool kF16, int kTiles, bool kFp8>
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
     uint64_t* meta_empty = bars + 36;
     uint64_t* raw_full = bars + 38;       // [NRAW]
     uint64_t* raw_empty = bars + 46;
-    volatile Widening& wide = *reinterpret_cast<volatile Widening*>(bars + 80);
-    static_assert(80 * 8 + sizeof(Widening) <= 1024, "factors fit behind the barriers");
+    volatile Widening& wide = *reinterpret_cast<volatile Widening*>(bars + 54);
+    static_assert(54 * 8 + sizeof(Widening) <= 1024, "factors fit behind the barriers");
     uint8_t* sRaw = smem + (C::TILES + C::NSLOT) * C::TILE;   // (kFp8: the ring, and the barriers behind it)
     int8_t* s_turn = reinterpret_cast<int8_t*>(bars) + 1024 + C::PART_BYTES;   // [unit & 1][tile][row] exponents
     float* s_max = reinterpret_cast<float*>(bars + 128);   // (PARTS = 2) [tile][part][row]
@@ -416,7 +417,10 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                             f.x = pack_f16x2(kf, kf);
                             f.y = pack_f16x2(vf, vf);
                         }
+                        const int plain = (__all_sync(0xffffffffu, !there || ke == k_top) ? 1 : 0) |
+                                          (__all_sync(0xffffffffu, !there || ve == v_top) ? 2 : 0);
                         if (lane == 0) {
+                            wide.plain[seq & 1] = plain;
                             wide.block[seq & 15].x = exp2_int(k_top) * p.scale_log2;
                             wide.block[seq & 15].y = static_cast<float>(v_top);
                         }
@@ -700,22 +704,38 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                     const uint32_t* const f = const_cast<const uint32_t*>(&wide.factor[blk & 1][(half + r0) / 8].x) + which;
                     constexpr int PIECES = 64 / STEP;   // all asked for before the first is used
                     uint4 v[PIECES];
-                    uint32_t m[PIECES];
-#pragma unroll
-                    for (int i = 0; i < PIECES; ++i) {
-                        const int r = r0 + STEP * i;
-                        v[i] = make_uint4(0u, 0u, 0u, 0u);   // outside what is attended: whatever is there, even NaN
-                        if (r >= lo && r < hi) v[i] = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
-                        m[i] = f[STEP / 4 * i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < PIECES; ++i) {
-                        uint32_t w[8];
-                        e4m3x16_to_f16(v[i], w);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], m[i]);
+                    auto put = [&](int i, const uint32_t (&w)[8]) {
                         *reinterpret_cast<uint4*>(dst + STEP * i * 128 + d0) = make_uint4(w[0], w[1], w[2], w[3]);
                         *reinterpret_cast<uint4*>(dst + STEP * i * 128 + d1) = make_uint4(w[4], w[5], w[6], w[7]);
+                    };
+                    // Most blocks lie within what is attended and have pages of one
+                    // scale: less than half the instructions.
+                    if (lo <= 0 && hi >= 64 && (wide.plain[blk & 1] >> which & 1)) {
+#pragma unroll
+                        for (int i = 0; i < PIECES; ++i) v[i] = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
+#pragma unroll
+                        for (int i = 0; i < PIECES; ++i) {
+                            uint32_t w[8];
+                            e4m3x16_to_f16(v[i], w);
+                            put(i, w);
+                        }
+                    } else {
+                        uint32_t m[PIECES];
+#pragma unroll
+                        for (int i = 0; i < PIECES; ++i) {
+                            const int r = r0 + STEP * i;
+                            v[i] = make_uint4(0u, 0u, 0u, 0u);   // outside what is attended: whatever is there, even NaN
+                            if (r >= lo && r < hi) v[i] = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
+                            m[i] = f[STEP / 4 * i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < PIECES; ++i) {
+                            uint32_t w[8];
+                            e4m3x16_to_f16(v[i], w);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = mul_f16x2(w[e], m[i]);
+                            put(i, w);
+                        }
                     }
                     mbar_arrive_warp(&raw_empty[from]);
                     if (part == C::UNITS - 1) {
