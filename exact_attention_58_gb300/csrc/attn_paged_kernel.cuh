@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                     const unsigned mine = needed >> ((part & 1) * half_boxes) & ((1u << half_boxes) - 1u);
                     ++raw_fills;
                     if (lane == 0)
-                        mbar_arrive_expect_tx(&raw_full[slot], __popc(mine) * static_cast<uint32_t>(p.box_rows) * C::RAW_COLS);
+                        mbar_arrive_expect_tx(&raw_full[slot],
+                                              __popc(mine) * static_cast<uint32_t>(p.box_rows) * C::RAW_COLS);
                     __syncwarp();
                     if (box.needed && lane / half_boxes == (part & 1))
                         tma_load_4d(sRaw + slot * C::RAW + lane % half_boxes * p.box_rows * C::RAW_COLS, which ? &tmV : &tmK,
@@ -660,28 +661,28 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                     (t ? q_n1 : q_n0) += 1;
 #pragma unroll 1
                     for (int r = tid; r < kTileRows; r += 64) {
-                    auto piece = [&](int c) {
-                        return reinterpret_cast<uint4*>(sQ + t * C::TILE + (c >> 3) * C::CB_BYTES + r * 128 +
-                                                        (((c & 7) ^ (r & 7)) << 4));
-                    };
-                    uint32_t top = 0;   // largest magnitude, as bf16 bits in either half
+                        auto piece = [&](int c) {
+                            return reinterpret_cast<uint4*>(sQ + t * C::TILE + (c >> 3) * C::CB_BYTES + r * 128 +
+                                                            (((c & 7) ^ (r & 7)) << 4));
+                        };
+                        uint32_t top = 0;   // largest magnitude, as bf16 bits in either half
 #pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = *piece(c);
-                        top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
-                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-                    }
-                    top = max(top & 0xffffu, top >> 16);
-                    const int ea = max(static_cast<int>(top >> 7) - 127, -100);
-                    const float up = exp2_int(14 - ea);
-                    s_turn[((units8 & 1) * 2 + t) * kTileRows + r] = static_cast<int8_t>(ea - 14);
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 v = *piece(c);
+                            top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                           __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                        }
+                        top = max(top & 0xffffu, top >> 16);
+                        const int ea = max(static_cast<int>(top >> 7) - 127, -100);
+                        const float up = exp2_int(14 - ea);
+                        s_turn[((units8 & 1) * 2 + t) * kTileRows + r] = static_cast<int8_t>(ea - 14);
 #pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint4* const at = piece(c);
-                        const uint4 v = *at;
-                        auto turn = [&](uint32_t w) { return pack_f16x2(bf16lo_to_f32(w) * up, bf16hi_to_f32(w) * up); };
-                        *at = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
-                    }
+                        for (int c = 0; c < D / 8; ++c) {
+                            uint4* const at = piece(c);
+                            const uint4 v = *at;
+                            auto turn = [&](uint32_t w) { return pack_f16x2(bf16lo_to_f32(w) * up, bf16hi_to_f32(w) * up); };
+                            *at = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+                        }
                     }
                     fence_proxy_async_smem();
                     mbar_arrive_warp(&q_turned[t]);
@@ -721,7 +722,8 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                     // scale: less than half the instructions.
                     if (lo <= 0 && hi >= 64 && (wide.plain[blk & 1] >> which & 1)) {
 #pragma unroll
-                        for (int i = 0; i < PIECES; ++i) v[i] = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
+                        for (int i = 0; i < PIECES; ++i)
+                            v[i] = *reinterpret_cast<const uint4*>(src + STEP * i * C::RAW_COLS);
 #pragma unroll
                         for (int i = 0; i < PIECES; ++i) {
                             uint32_t w[8];
