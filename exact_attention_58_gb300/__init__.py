@@ -54,7 +54,8 @@ __all__ = [
     "attn_bwd_main", "attn_bwd_dq_convert", "attn_bwd_noalloc", "attn_fwd_varlen",
     "attn_bwd_varlen", "attn_page_table", "attn_cache_append", "attn_fwd_paged",
     "attn_fwd_paged_workspace_size", "attn_rope", "attn_rope_frequencies",
-    "attn_cache_append_rope", "attn_cache_append_fp8", "attn_fwd_paged_fp8", "attn_selftest_wait", "attn_selftest_fwd_withheld", "attn_status_string",
+    "attn_cache_append_rope", "attn_cache_append_fp8", "attn_fwd_paged_fp8",
+    "attn_selftest_wait", "attn_selftest_fwd_withheld", "attn_status_string",
     "attn_version", "library",
     "LIB_PATH", "STATUS",
 ]
@@ -857,7 +858,7 @@ def attn_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: flo
         # index whose frequency makes `turns` turns in original_len positions
         def index(turns):
             return rotary_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
-        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotary_dim // 2 - 1)
+        lo, hi = math.floor(index(fast)), math.ceil(index(slow))
         mix = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         freq = freq * (1.0 - mix) + freq / factor * mix
         scaling = 0.1 * math.log(factor) + 1.0

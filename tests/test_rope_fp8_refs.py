@@ -176,6 +176,23 @@ def test_frequencies():
             ea.attn_rope_frequencies(r)
 
 
+@pytest.mark.parametrize("n", [1, 40, 300, 4096, 131072, 10**7])
+@pytest.mark.parametrize("r", [16, 64, 128])
+def test_frequencies_by_parts_at_any_length(r, n):
+    """Kept from `fast` turns on, divided up to `slow`, mixed in between, also where
+    all pairs, or none, lie to one side."""
+    f, _ = ea.attn_rope_frequencies(r)
+    g, _ = ea.attn_rope_frequencies(r, factor=4.0, method="parts", original_len=n)
+    turns = n * f.double() / (2 * math.pi)
+    assert torch.equal(g[turns >= 32], f[turns >= 32])
+    # (a division in 64 bits, rounded, is the exact quotient by a power of two of the rounded)
+    assert torch.equal(g[turns <= 1], f[turns <= 1] / 4)
+    # strictly between away from the whole indices that the two ends are rounded to
+    step = 10000.0 ** (2 / r)
+    inside = (turns > 1 * step) & (turns < 32 / step)
+    assert bool((g[inside] < f[inside]).all()) and bool((g[inside] > f[inside] / 4).all())
+
+
 # ---------------------------------------------------------------------------
 # references
 # ---------------------------------------------------------------------------
