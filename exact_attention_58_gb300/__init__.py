@@ -921,6 +921,8 @@ def attn_rope(q, k, inv_freq, positions=None, *, interleaved: bool = False, inve
             raise ValueError("k must match q in all but the number of heads")
         if Hk < 1:
             raise ValueError("k has no heads")
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
     pos, pos_batch = None, 0
     if positions is not None:
         rows = q.dim() == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 2

@@ -128,6 +128,8 @@ def test_rope_binding_refuses(lib):
     q, k, f = torch.zeros(2, 4, 10, 64, dtype=bf), torch.zeros(2, 2, 10, 64, dtype=bf), torch.ones(32)
     with last():
         ea.attn_rope(q, k, f)
+    with refused():   # an output for keys that are not there
+        ea.attn_rope(q, None, f, k_out=k)
     with last():
         ea.attn_rope(q, None, f, torch.zeros(2, 10, dtype=torch.int32))
     i32 = torch.int32
