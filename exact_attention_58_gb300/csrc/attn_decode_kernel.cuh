@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, N, kFp8>::THREADS, 1)
             const PageBox x = next;
             const int page = x.needed ? page_box_checked(p, x) : 0;
             const unsigned needed = __ballot_sync(0xffffffffu, x.needed);
-            const float kf = exp2_int(scale_exponent(kb)) * p.scale_log2, ve = static_cast<float>(scale_exponent(vb));
+            const float kf = score_factor(exp2_int(scale_exponent(kb)) * p.scale_log2);
+            const float ve = static_cast<float>(scale_exponent(vb));
             if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
                 atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
             next = boxes8(b, r, j0 + tiles, jend);

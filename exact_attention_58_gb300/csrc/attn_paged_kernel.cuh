@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
             if constexpr (kFp8) {
                 if (kTurnQ && j == jlo) turn = exp2_int(s_turn[((t_n & 1) * 2 + t) * kTileRows + r]);
                 volatile const float2& block = wide.block[(g - first_block(pl) + j) & 15];
-                sc = block.x * turn;
+                sc = score_factor(block.x * turn);
                 ev = block.y;
             }
             // V rows outside [klo, khi) become zero.  Only after S_j: by then

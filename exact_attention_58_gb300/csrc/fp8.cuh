@@ -47,6 +47,11 @@ __device__ __forceinline__ bool bad_scale(uint32_t bits) {
     return (bits & 0x807fffffu) != 0 || bits == 0x7f800000u;
 }
 
+// A factor of scores, kept in fp32's normal numbers: a masked score (-inf) times 0 would be
+// NaN, and so would a score of 0 times infinity.  What it moves at either end is a
+// score below 2^-90 or far past what exp2 can tell apart.
+__device__ __forceinline__ float score_factor(float f) { return fminf(fmaxf(f, 0x1p-126f), 3.402823466e38f); }
+
 // The smallest exponent e in range with x <= 448 2^e, x >= 0 given by its bits:
 // 448 = 1.75 x 2^8, so one more than x's own exponent less 8 where its mantissa exceeds 1.75.
 __device__ __forceinline__ int fit_exponent(uint32_t bits) {
