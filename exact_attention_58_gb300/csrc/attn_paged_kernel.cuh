@@ -35,11 +35,12 @@
 // kFp8: a cache of e4m3 with a power-of-two scale per page and head.  TMA loads half
 // tiles (D = 256: by 128 columns) as they are, and two warps widen them to fp16 in the
 // ring that the products read; scales are factors over the largest of the block's pages,
-// which is a factor of its scores and an exponent of its weights (attn_decode_kernel.cuh).
+// which is a factor of its scores and an exponent of its weights (attn_decode_kernel.cuh), or,
+// where pages are far apart in size (kSpread), taken page by page in the softmax.
 // bf16 queries become fp16 times a power of two a row.  The widening warps bound it
 // (a block about 2.7 us): registers leave room for no more than three warps an SM
 // sub-partition, and a third on the products' own slows those.  A chunk of 512 over
-// 16100 keys 98 us (700 TFLOP/s), whole prompts of 4 x 16 x 4096 361 us.
+// 16100 keys 98 us (700 TFLOP/s), whole prompts of 4 x 16 x 4096 345 us.
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
@@ -78,10 +79,108 @@ __device__ __forceinline__ void find_packed_tile(const PagedParams& p, int x, in
 
 // (kFp8) What the producer passes to the warps that widen e4m3, and to the softmax.
 struct Widening {
-    uint2 factor[2][16];   // [block][8 keys]: scales over the block's largest, K's and V's, as fp16 twice
-    float2 block[16];      // largest scale of K times the softmax scale, exponent of V's
-    int plain[2];          // [block] bit 0, 1: all of K's, V's factors are one
+    uint2 factor[2][16];        // [block][8 keys]: scales over the block's largest, K's and V's, as fp16 twice
+    float2 block[8];            // largest scale of K times the softmax scale, exponent of V's (or kUneven)
+    int16_t exponents[8][16];   // [block][8 keys] (uneven blocks) of the scales: 256 times K's, plus V's
+    int plain[2];               // [block] bit 0, 1: all of K's, V's factors are one
 };
+
+// (kFp8) Scales of a block's pages are factors over the largest where they are at most
+// 2^kSpread apart: exact in fp16, and the weights, taken times the largest scale of V, count
+// down to 2^-29 of a row's largest (2^-32 where all scales are one).  A block whose scales
+// are further apart is uneven: widened without factors, and the softmax takes the pages' own
+// exponents, so that what a row attends comes out as well whatever pages lie beside it.
+constexpr int kSpread = 3;
+constexpr float kUneven = 1000.f;
+__device__ __forceinline__ int exponent_k(int both) { return (both + 128) >> 8; }
+__device__ __forceinline__ int exponent_v(int both) { return both - 256 * exponent_k(both); }
+
+// Uneven blocks' part of the softmax, in short loops in functions of their own: unrolled
+// beside the ordinary block's code they slowed that, for its registers and the
+// instruction buffer (prompts of 4 x 4096 361 -> 399 us without one uneven block).
+//
+// Scores in tensor memory, a row of 8 x groups keys per lane, become s + ev.
+__device__ __noinline__ void uneven_scores(uint32_t t_S, int groups, const volatile int16_t* exponents,
+                                           float scale_log2, float turn) {
+#pragma unroll 1
+    for (int c = 0; c < groups; ++c) {
+        const int both = exponents[c];
+        const float f = score_factor(exp2_int(exponent_k(both)) * scale_log2 * turn);
+        const float ev = static_cast<float>(exponent_v(both));
+        uint32_t x[8];
+        tmem_ld8(t_S + 8 * c, x);
+        tmem_ld_wait();
+        reg_fence(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), f, ev));
+        tmem_st8(t_S + 8 * c, x);
+    }
+    tmem_st_wait();
+}
+
+// All of it for a row with one thread, which attends the block's keys [lo, lim): weights to
+// t_P, the row's O (o_cols columns) to its new reference.  Returns reference and sum.
+__device__ __noinline__ float2 uneven_block(uint32_t t_S, uint32_t t_P, uint32_t t_O, int o_cols,
+                                            const volatile int16_t* exponents, float scale_log2, float turn, int lo,
+                                            int lim, float m_ref, float l) {
+    uneven_scores(t_S, kTileRows / 8, exponents, scale_log2, turn);
+    auto kept = [&](int key, uint32_t x) { return key >= lo && key < lim ? __uint_as_float(x) : -INFINITY; };
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kTileRows; c += 8) {
+        uint32_t x[8];
+        tmem_ld8(t_S + c, x);
+        tmem_ld_wait();
+        reg_fence(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, kept(c + i, x[i]));
+    }
+    const float m_new = fmaxf(m_ref, mx - kWeightShift<true>);
+    float alpha = 1.f;
+    if (m_ref == -INFINITY) {
+        m_ref = m_new;   // O and l are still zero
+    } else if (m_new > m_ref + kRescaleThreshold) {
+        alpha = ex2_approx(m_ref - m_new);
+        m_ref = m_new;
+    }
+    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c = 0; c < o_cols; c += 8) {
+            uint32_t o[8];
+            tmem_ld8(t_O + c, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st8(t_O + c, o);
+        }
+    }
+    const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kTileRows; c += 16) {   // weights take half the columns, of scores already read
+        uint32_t w[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t x[8];
+            tmem_ld8(t_S + c + 8 * h, x);
+            tmem_ld_wait();
+            reg_fence(x);
+            float some = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const int k = c + 8 * h + i;
+                const float x0 = ex2_approx(kept(k, x[i]) + neg_m), x1 = ex2_approx(kept(k + 1, x[i + 1]) + neg_m);
+                w[4 * h + i / 2] = pack_f16x2(x0, x1);
+                some += x0 + x1;
+            }
+            sum = fmaf(some, exp2_int(-exponent_v(exponents[c / 8 + h])), sum);
+        }
+        tmem_st8(t_P + c / 2, w);
+    }
+    tmem_st_wait();
+    return make_float2(m_ref, fmaf(l, alpha, sum));
+}
 
 template <int D, bool kF16, int kTiles, bool kFp8>
 struct PagedCfg : FwdCfg<D, false, kF16 || kFp8, false, kTiles> {
@@ -380,23 +479,54 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
             q_n0 += pl.jhi0 > pl.jlo0;
             q_n1 += pl.jhi1 > pl.jlo1;
             // (kFp8) A block's scales are taken relative to its largest, so that one
-            // factor holds for all its scores and one exponent for all its weights;
-            // values are exact in fp16 down to 2^-15 of the largest scale, and
-            // below are off by 2^-25 of it.  They are passed on behind the
-            // block's first load, before any other wait.
-            for (int j = jbeg; kFp8 && j < jbeg + nkv && ok; ++j, ++seq) {
-                const unsigned needed = __ballot_sync(0xffffffffu, box.needed);
-                PageBox next = box;
-                if (j + 1 < jbeg + nkv) next = page_box(p, table, (j + 1) * kTileRows, pl.klo, pl.khi, lane);
-                const int page = box.needed ? page_box_checked(p, box) : p.num_pages;
-                const bool there = page < p.num_pages;
-                uint32_t kb = 127u << 23, vb = kb;
-                if (there) {
+            // factor holds for all its scores and one exponent for all its weights, or
+            // (uneven) page by page.  They are read a block ahead and passed on before the
+            // block's loads, while the ring is still full (behind the first load, prompts of 4 x
+            // 4096 took 361 us instead of 351).  The eight blocks' worth of room is more
+            // than this warp runs ahead of the softmax (two blocks, and the ring's up to four).
+            int page = p.num_pages;
+            uint32_t kb = 0, vb = 0;
+            auto ask = [&]() {   // the page of this lane's box, and its scales
+                page = box.needed ? page_box_checked(p, box) : p.num_pages;
+                kb = vb = 127u << 23;
+                if (page < p.num_pages) {
                     const size_t at = static_cast<size_t>(page) * p.Hkv + pl.hk;
                     kb = __float_as_uint(p.k_scale[at]);
                     vb = __float_as_uint(p.v_scale[at]);
                 }
+            };
+            if (kFp8) ask();
+            for (int j = jbeg; kFp8 && j < jbeg + nkv && ok; ++j, ++seq) {
+                const unsigned needed = __ballot_sync(0xffffffffu, box.needed);
+                const int row = box.row, mine_at = box.needed ? page : -1;
+                if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
+                    atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
+                const bool there = page < p.num_pages;
+                const int ke = there ? scale_exponent(kb) : kLeastScale, ve = there ? scale_exponent(vb) : kLeastScale;
+                const int k_top = __reduce_max_sync(0xffffffffu, ke), v_top = __reduce_max_sync(0xffffffffu, ve);
+                ok = mbar_wait_warp_soon(&meta_empty[seq & 1], ((seq >> 1) & 1) ^ 1, s_abort);
+                if (!ok) break;
+                const int plain = (__all_sync(0xffffffffu, !there || ke == k_top) ? 1 : 0) |
+                                  (__all_sync(0xffffffffu, !there || ve == v_top) ? 2 : 0);
+                const bool uneven = __any_sync(0xffffffffu, there && max(k_top - ke, v_top - ve) > kSpread);
+                const float kf = exp2_int(uneven ? 0 : max(ke - k_top, -60)), vf = exp2_int(uneven ? 0 : max(ve - v_top, -60));
+                for (int i = 0; i < p.box_rows / 8 && lane < kTileRows / p.box_rows; ++i) {
+                    const int at = lane * (p.box_rows / 8) + i;
+                    volatile uint2& f = wide.factor[seq & 1][at];
+                    f.x = pack_f16x2(kf, kf);
+                    f.y = pack_f16x2(vf, vf);
+                    wide.exponents[seq & 7][at] = static_cast<int16_t>(256 * ke + ve);
+                }
+                if (lane == 0) {
+                    wide.plain[seq & 1] = uneven ? 3 : plain;
+                    wide.block[seq & 7].x = exp2_int(k_top) * p.scale_log2;
+                    wide.block[seq & 7].y = uneven ? kUneven : static_cast<float>(v_top);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_full[seq & 1]);
+                if (j + 1 < jbeg + nkv) box = page_box(p, table, (j + 1) * kTileRows, pl.klo, pl.khi, lane);
                 const int half_boxes = 64 / p.box_rows;
+#pragma unroll 1
                 for (int u = 0; u < 2 * C::UNITS; ++u) {
                     const int which = u / C::UNITS, part = u % C::UNITS;   // part: 64 rows, then columns
                     const int n = 2 * C::UNITS * seq + u, slot = n % C::NRAW;
@@ -408,37 +538,12 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                         mbar_arrive_expect_tx(&raw_full[slot],
                                               __popc(mine) * static_cast<uint32_t>(p.box_rows) * C::RAW_COLS);
                     __syncwarp();
-                    if (box.needed && lane / half_boxes == (part & 1))
+                    if (mine_at >= 0 && lane / half_boxes == (part & 1))
                         tma_load_4d(sRaw + slot * C::RAW + lane % half_boxes * p.box_rows * C::RAW_COLS, which ? &tmV : &tmK,
-                                    &raw_full[slot], (part >> 1) * C::RAW_COLS, box.row, pl.hk, page);
+                                    &raw_full[slot], (part >> 1) * C::RAW_COLS, row, pl.hk, mine_at);
                     __syncwarp();
-                    if (u == 0) {
-                        if ((bad_scale(kb) || bad_scale(vb)) && p.dev_status != nullptr)
-                            atomicCAS(p.dev_status, 0, static_cast<int>(ATTN_ERR_INVALID_ARG));
-                        const int ke = scale_exponent(kb), ve = scale_exponent(vb);
-                        const int k_top = __reduce_max_sync(0xffffffffu, there ? ke : kLeastScale);
-                        const int v_top = __reduce_max_sync(0xffffffffu, there ? ve : kLeastScale);
-                        ok = mbar_wait_warp_soon(&meta_empty[seq & 1], ((seq >> 1) & 1) ^ 1, s_abort);
-                        if (!ok) break;
-                        const float kf = there ? exp2_int(max(ke - k_top, -60)) : 0.f;
-                        const float vf = there ? exp2_int(max(ve - v_top, -60)) : 0.f;
-                        for (int i = 0; i < p.box_rows / 8 && lane < kTileRows / p.box_rows; ++i) {
-                            volatile uint2& f = wide.factor[seq & 1][lane * (p.box_rows / 8) + i];
-                            f.x = pack_f16x2(kf, kf);
-                            f.y = pack_f16x2(vf, vf);
-                        }
-                        const int plain = (__all_sync(0xffffffffu, !there || ke == k_top) ? 1 : 0) |
-                                          (__all_sync(0xffffffffu, !there || ve == v_top) ? 2 : 0);
-                        if (lane == 0) {
-                            wide.plain[seq & 1] = plain;
-                            wide.block[seq & 15].x = exp2_int(k_top) * p.scale_log2;
-                            wide.block[seq & 15].y = static_cast<float>(v_top);
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&meta_full[seq & 1]);
-                    }
                 }
-                box = next;
+                if (ok) ask();   // (behind the last block once too often)
             }
             for (int j = jbeg; !kFp8 && j < jbeg + nkv && ok; ++j) {
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box.needed)) *
@@ -803,7 +908,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
             float sc = p.scale_log2, ev = 0.f;
             if constexpr (kFp8) {
                 if (kTurnQ && j == jlo) turn = exp2_int(s_turn[((t_n & 1) * 2 + t) * kTileRows + r]);
-                volatile const float2& block = wide.block[(g - first_block(pl) + j) & 15];
+                volatile const float2& block = wide.block[(g - first_block(pl) + j) & 7];
                 sc = score_factor(block.x * turn);
                 ev = block.y;
             }
@@ -836,6 +941,26 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
             if (wmask) {
                 lo = pos - W + 1 - k0 - c0;
                 if (!p.causal) lim = min(lim, pos + W - k0 - c0);
+            }
+
+            bool uneven = false;   // (where a row has one thread, a function does all of such a block)
+            if constexpr (kFp8) {
+                if (__builtin_expect(ev == kUneven, 0)) {
+                    const volatile int16_t* const exponents = &wide.exponents[(g - first_block(pl) + j) & 7][c0 / 8];
+                    if constexpr (C::PARTS == 1) {
+                        const float2 ml = uneven_block(t_S, t_P, t_O, j > jlo ? D : 0, exponents, p.scale_log2, turn, lo,
+                                                       lim, m_ref, l);
+                        m_ref = ml.x;
+                        l = ml.y;
+                        tc_fence_before();
+                        mbar_arrive_warp(&bar_p[t]);
+                        continue;
+                    }
+                    uneven_scores(t_S, C::NC / 8, exponents, p.scale_log2, turn);
+                    sc = 1.f;
+                    ev = 0.f;
+                    uneven = true;
+                }
             }
 
             // ---- row max ----
@@ -897,6 +1022,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
             const uint64_t sc2 = f2_pack(sc, sc);
             const float nm = kFp8 ? neg_m + ev : neg_m;
             const uint64_t nm2 = f2_pack(nm, nm);
+            float take = exp2_int(-static_cast<int>(ev));   // what the weights were taken times, off again
             uint64_t acc2[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc2[k] = f2_pack(0.f, 0.f);
@@ -914,7 +1040,13 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                     x0 = ex2_approx(x0);
                     x1 = ex2_approx(x1);
                     pk[e] = pack_h2<kMmaF16>(x0, x1);
-                    acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(x0, x1));
+                    if constexpr (kFp8 && C::PARTS > 1) {
+                        if ((e & 3) == 0 && uneven)
+                            take = exp2_int(-exponent_v(wide.exponents[(g - first_block(pl) + j) & 7][c0 / 8 + 2 * c8 + e / 4]));
+                        acc2[e & 3] = f2_fma(f2_pack(x0, x1), f2_pack(take, take), acc2[e & 3]);
+                    } else {
+                        acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(x0, x1));
+                    }
                 }
                 tmem_st8(t_P + 8 * c8, pk);
             }
@@ -925,7 +1057,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kF16, kTiles, kFp8>::THREADS, 1)
                 f2_unpack(f2_add(acc2[2], acc2[3]), a2, a3);
                 rowsum = (a0 + a1) + (a2 + a3);
             }
-            if constexpr (kFp8) rowsum *= exp2_int(-static_cast<int>(ev));
+            if constexpr (kFp8 && C::PARTS == 1) rowsum *= exp2_int(-static_cast<int>(ev));
             l = l * alpha + rowsum;
             if (warp_rescale && j > jlo) {   // O row *= alpha (PV of block j-1 is complete)
 #pragma unroll

@@ -14,9 +14,9 @@ def row_bound(x, causal, window=0, scale=None):
 
     To ref_attention's errors (products of 16 bits, fp32 sums, one rounding of O) come those
     of a cache of e4m3 c_j times 2^ev_j, for a row with probabilities p_j:
-      * A weight is rounded as exp2(s_j + ev_j - m) with m at least 7 below the row's
-        largest s_j + ev_j, so that fp16 is off by at most half a step of 2^-24 at 2^7:
-        2^-32 of the largest p_j 2^ev_j, times |c_j|, over the keys attended.
+      * A weight is rounded as exp2(s_j + e - m), e being ev_j or at most 3 more, with m at
+        least 7 below the row's largest s_j + e: fp16 is off by at most half a step of
+        2^-24 at 2^(7 - 3), 2^-29 of the largest p_j 2^ev_j, times |c_j|, over the keys attended.
       * bf16 queries become fp16 times a power of two that puts the row's largest
         element in [2^14, 2^15): an element is off by at most 2^-25, 2^-39 of the largest.
       * s_j + ev_j, the reference and their difference are rounded to fp32 once each:
@@ -56,7 +56,7 @@ def row_bound(x, causal, window=0, scale=None):
             lp = S - torch.where(z == -math.inf, 0.0, z)[:, None]
             most = torch.exp((lp + ev[:, hk] * math.log(2)).amax(1))   # largest p_j 2^ev_j
             codes = torch.where(used[:, None], V[:, hk].abs() * torch.exp2(-ev[:, hk])[:, None], 0.0)
-            weights = 2.0**-32 * most[:, None] * (valid.double() @ codes)
+            weights = 2.0**-29 * most[:, None] * (valid.double() @ codes)
             e_q = (2.0**-39 * q.abs().amax(1) * scale * (valid.double() * K[:, hk].abs().sum(1)).amax(1)
                    if turned else torch.zeros(n, dtype=torch.float64))
             e_q = e_q + 3 * 2.0**-24 * (valid.double() * ev[:, hk].abs()).amax(1)
