@@ -448,9 +448,12 @@ attn_status attn_cache_append_rope(const void* Q, const void* K, const void* V, 
  * anew: the old scale does not count.  Infinities, and values past 448 x 2^48, become
  * the largest number; a NaN stays one.
  * The slots of a page that one call names are one ascending run of consecutive rows at
- * consecutive tokens, as attn_page_table makes them; what a page named by several runs
- * holds afterwards is unspecified.  A slot of -1 is skipped, any other slot outside the
- * cache skipped and reported.  No two requests may write to one page.
+ * consecutive tokens, as attn_page_table makes them.  A slot of -1 is skipped, any other
+ * slot outside the cache skipped and reported.  A second run of a page behind the first, with
+ * no token between them or only tokens without a slot, as many as rows at most (a row
+ * twice, out of order, or rows skipped in the middle of a page), is left out and reported as
+ * ATTN_ERR_INVALID_ARG; what a page holds that is named again elsewhere in the call is
+ * unspecified.  No two requests may write to one page.
  * T H_kv < 2^30.  One launch.
  */
 attn_status attn_cache_append_fp8(const void* K, const void* V, void* k_cache, void* v_cache,
