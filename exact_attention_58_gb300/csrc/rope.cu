@@ -15,8 +15,8 @@ namespace {
 // Angles.  t inv_freq has up to 55 bits, and only its place within a turn counts,
 // which fp32 would lose from t = 1000 on.  So each frequency becomes the fraction
 // of a turn per position, 64 bits after the point (a CTA does it once, in fp64:
-// off by 2^-53 of itself), and t times it modulo 2^64 is the angle, whatever
-// t is, in one integer product.  Its upper 32 bits go to sin and cos: the fast ones
+// off by 2^-53 for frequencies up to 1, by 2^-53 of the frequency above), and t times it
+// modulo 2^64 is the angle, whatever t is, in one integer product.  Its upper 32 bits go to sin and cos: the fast ones
 // for the 16-bit types (off by 2^-21 there, a rounding to fp16 by 2^-11 and more),
 // sincospif for fp32.
 //

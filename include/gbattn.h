@@ -388,8 +388,9 @@ size_t attn_fwd_paged_workspace_size(int B, int H, int H_kv, int total_q, int ma
  *   inv_freq   float [rotary_dim / 2], finite
  *   positions  int32, row n of batch entry b is at positions[b position_batch_stride
  *              + n] (position_batch_stride 0: the same for all b); NULL: at n.  Any
- *              value, negative ones too: an angle is off by at most |t| 2^-53 + 2^-25
- *              turns, and its cosine and sine by 2^-20 (fp32: 2^-22)
+ *              value, negative ones too: an angle is off by at most
+ *              |t| max(1, |inv_freq|) 2^-53 + 2^-25 turns, and cosine and sine of that
+ *              angle by 2^-20 (fp32: 2^-22)
  * Q_out may be Q, and K_out K, with the same strides (in place); otherwise outputs
  * overlap neither inputs nor one another.  bf16, fp16 or fp32; d in {64, 128, 256};
  * rotary_dim a multiple of 16 up to d; N <= 2^30.  One launch.
