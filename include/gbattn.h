@@ -447,7 +447,8 @@ attn_status attn_cache_append_rope(const void* Q, const void* K, const void* V, 
  * whose scale is the block's old one; where it grows, those rows are rounded again
  * on the new one.  A row written to a page's row 0 starts the block
  * anew: the old scale does not count.  Infinities, and values past 448 x 2^48, become
- * the largest number; a NaN stays one.
+ * the largest number, and the scale 2^48, on which the block's other rows are zeros where
+ * they are below 2^38; a NaN stays one and does not count for the scale.
  * The slots of a page that one call names are one ascending run of consecutive rows at
  * consecutive tokens, as attn_page_table makes them.  A slot of -1 is skipped, any other
  * slot outside the cache skipped and reported.  A second run of a page behind the first, with
