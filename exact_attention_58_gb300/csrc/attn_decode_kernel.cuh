@@ -46,11 +46,12 @@
 // that they fall in fp16's range as they count in O), which the sum takes off again.
 // bf16 queries become fp16 times a power of two a row.  Eight more warps widen:
 // four K, a key per lane, into tensor memory, where the product reads it as its
-// first operand; four V into shared memory.  A block then takes an SM about 0.75 us
-// (half the bytes of 16 bits at 1.41), bound by the roles' instructions and
+// first operand; four V into shared memory.  A block then takes an SM 0.89 us at
+// d = 128 (5.6 TB/s; 16 bits 1.4) and 0.78 at d = 64, bound by the roles' instructions and
 // handovers and by the tensor pipe (small products: 515 and 587 cycles of about
-// 1450), not by DRAM: 48 requests of up to 4200 keys, 32/8 heads, 66 us (258 MB, 3.9
-// TB/s); 2 of 70001 and more, 33 us; 997 keys, 12 heads, d = 64, 8.5 us.
+// 1700), and 1.44 at d = 256, by DRAM.  48 requests of up to 4200 keys, 32/8 heads,
+// 66 us (258 MB, 3.9 TB/s; 20 of them start, ends of segments and join); 2 of 70001 and
+// more, 33 us; 997 keys, 12 heads, d = 64, 8.5 us.
 #pragma once
 
 #include "attn_fwd_kernel.cuh"

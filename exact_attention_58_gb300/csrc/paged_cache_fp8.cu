@@ -19,9 +19,9 @@ namespace {
 // the other: its threads look at 128 tokens at once and mark where runs begin; then,
 // run by run, it finds the largest value (the rows stay in registers, as far as they
 // fit), the scale, and writes: one launch, no word between CTAs, and no atomics.
-// Bound by memory for prompts (15900 tokens of 8 heads, d = 128: 19.3 us, 5.0 TB/s); for
+// Bound by issue for prompts (15900 tokens of 8 heads, d = 128: 19.8 us, 4.9 TB/s); for
 // single tokens, where each CTA has one row, by the chain slot -> scale and row ->
-// store (64 tokens 4.1 us).  Eight CTAs an SM (64 registers a thread): with 95
+// store (64 tokens 4.2 us).  Eight CTAs an SM (64 registers a thread): with 95
 // registers and five of them 22.3 and 4.6 us.
 constexpr int kThreads = 128;
 constexpr int kChunk = 64;  // tokens whose runs are begun at a time: half of what is looked at
