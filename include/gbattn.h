@@ -335,8 +335,10 @@ attn_status attn_cache_append(const void* K, const void* V, void* k_cache, void*
  * seq_lens[b]: a request's queries are its last key positions; a query without
  * a key gets O = 0 and LSE = -inf.  Cache slots that no query of a request may
  * attend (past its last key, before its window) may hold anything, NaN
- * included, without effect.  Rows of Q behind cu_seqlens_q[B] are ignored, and
- * those of O and LSE left as they are.
+ * included, without effect; a V row that some query attends is multiplied by a
+ * weight of 0 for queries of the same call that do not, which keeps a NaN or an
+ * infinity.  Rows of Q behind cu_seqlens_q[B] are ignored, and those of O and
+ * LSE left as they are.
  * Clamped on the device (no access leaves the tensors) and reported as
  * ATTN_ERR_INVALID_ARG through dev_status: bad cu_seqlens_q as in
  * attn_fwd_varlen, seq_lens outside [0, max_pages * page_size], and page ids
@@ -468,7 +470,9 @@ attn_status attn_cache_append_fp8(const void* K, const void* V, void* k_cache, v
 /*
  * attn_fwd_paged over a cache held in 8 bits: Q and O in bf16 or fp16 (dtype is
  * theirs), everything else as there, the workspace's size included.  Scales are read
- * for the pages with a key that some query attends.
+ * for the pages with a key that some query attends.  They may be as far apart as they
+ * like, a row's accuracy is that of the pages it attends; where scales within 128 keys are
+ * more than 2^3 apart, chunks and prompts take up to 1.6 times as long.
  */
 attn_status attn_fwd_paged_fp8(const void* Q, const void* k_cache, const void* v_cache,
                                const float* k_scale, const float* v_scale, void* O, float* LSE,
